@@ -37,6 +37,15 @@
  *                                                                     sft_rows_restore
  *   Measurement probes (sustained bandwidth and matrix-core rate) are
  *   declared apart, in sft_probe.h.
+ *   What a model trains whole (norm gains, biases, routers, experts) needs
+ *   the dense counterparts in the same step: the products of layers whose
+ *   rows are grouped by expert, with their gradients, the norm of many
+ *   gradients with its clip factor, and AdamW over many tensors.
+ *                                                                  -> sft_expert_forward,
+ *                                                                     sft_expert_dx,
+ *                                                                     sft_expert_dw,
+ *                                                                     sft_grad_clip,
+ *                                                                     sft_adamw
  *   The element-sparse variant of the blog post "SparseLeaf: synaptic sparse
  *   fine-tuning" (K selected connections of a frozen weight train their own
  *   increments): their gradients and their Adam step.
@@ -78,7 +87,7 @@
 extern "C" {
 #endif
 
-#define SFT_ABI_VERSION 14
+#define SFT_ABI_VERSION 15
 
 enum {
     SFT_OK = 0,
@@ -747,6 +756,106 @@ typedef struct sft_leaf_vec {
 
 int sft_leaf_adam(const sft_leaf_vec *vecs, int32_t n_vecs, int32_t step, const sft_adam *hp,
                   void *stream);
+
+/* ======================================================================= */
+/* device: the dense optimizer step                                         */
+/* ======================================================================= */
+
+/* Storage types of the dense calls. */
+enum { SFT_F32 = 0, SFT_BF16 = 1 };
+
+/* One gradient of sft_grad_clip: n values of `type`, aligned to the type
+ * (16-byte aligned gradients are read faster). */
+typedef struct sft_grad_vec {
+    int64_t n;
+    const void *grad;
+    int32_t type;           /* SFT_F32 or SFT_BF16 */
+} sft_grad_vec;
+
+/* Workspace bytes sft_grad_clip needs for these gradients, or (size_t)-1 on
+ * invalid input (message in sft_last_error). */
+size_t sft_grad_clip_workspace(const sft_grad_vec *vecs, int32_t n_vecs);
+
+/*
+ * The norm of many gradients taken together, and the factor that clips it:
+ *   norm = sqrt(sum over every value g of g^2),  clip = min(1, max_norm / norm)
+ * and clip = 0 where norm is infinite or not a number.  sft_adamw and
+ * sft_coupled_update read such a factor from the device (sft_coupled_update
+ * a pair of them: two calls, each with its half of the pair as `clip`).
+ *   clip      device float, 4-byte aligned
+ *   norm      device float, 4-byte aligned, or NULL
+ *   max_norm  positive; infinity measures only (clip = 1 for a finite norm)
+ *   ws        device scratch of at least sft_grad_clip_workspace() bytes
+ *             (16-byte aligned; no initialisation needed); calls sharing it
+ *             must be ordered on one stream
+ * Summed in fp64 in a fixed order: deterministic, and no square of a float
+ * overflows.  An empty list has norm 0 and clip 1.
+ * Errors: SFT_EINVAL (null pointers, negative sizes, bad type, max_norm not
+ * positive), SFT_EALIGN, SFT_ECAPACITY (workspace too small), SFT_ENOTSUP
+ * (2^42 values in a vector, or 2^31 chunks of 8192 values in a launch),
+ * SFT_EHIP.
+ */
+int sft_grad_clip(const sft_grad_vec *vecs, int32_t n_vecs, float max_norm, float *clip, float *norm, void *ws,
+                  size_t ws_bytes, void *stream);
+
+/*
+ * One tensor of sft_adamw: n parameters with their gradient and moments.
+ *   p, p_type        parameters, fp32 or bf16 (rounded to nearest even)
+ *   grad, g_type     their gradient, fp32 or bf16
+ *   p_live           bf16 copy of the new parameters, or NULL
+ *   states in 32 bits (scale NULL): m, v fp32 [n]
+ *   states in 8 bits: m and v are e4m3 codes [n] (the format without
+ *     infinities) and scale is e8m0 [ceil(n/256) x 2]: in block b of 256
+ *     elements m = m_code * 2^(scale[b][0] - 127) and sqrt(v) = v_code *
+ *     2^(scale[b][1] - 127).  Of v its square root is held, which needs half
+ *     the range.  Each step decodes the states, takes the step in fp32 with
+ *     the values before they are rounded, and holds the new ones: scales that
+ *     bring the block's largest magnitude into [128, 256) (1 for a block of
+ *     zeros, limited below to 2^-127), codes rounded down or up by a fixed
+ *     sequence of 20 bits, w >> 12 with w = i * 0xC2B2AE35 + t * 0x9E3779B9
+ *     for sqrt(v) and w + 0x55555555 for m (mod 2^32; i the element's index,
+ *     t the step): up where the part of a code's width that is cut off, plus
+ *     the sequence / 2^20, reaches 1.  Over the steps this is unbiased, where
+ *     rounding to nearest would keep v from ever decaying.  A root above
+ *     zero keeps at least the lowest code.  A block with a value that is not
+ *     finite gets scale 255, which stands for NaN.  States start as zeros
+ *     with any scale other than 255.
+ * Pointers are aligned to their types; tensors with every pointer 16-byte
+ * aligned are read and written faster.
+ */
+typedef struct sft_adamw_vec {
+    int64_t n;
+    void *p;
+    const void *grad;
+    void *m;
+    void *v;
+    uint8_t *scale;
+    uint16_t *p_live;
+    int32_t p_type, g_type;
+} sft_adamw_vec;
+
+/*
+ * AdamW on every tensor at step t (>= 1), the tensors of one kind (types,
+ * states) in one launch of up to 74 (8-bit states: 64) tensors:
+ *   g = clip * grad,  m = beta1*m + (1-beta1)*g,  v = beta2*v + (1-beta2)*g^2
+ *   p = p*(1 - lr*weight_decay) - (k1*m) / (sqrt(v)*k2 + eps)
+ * with k1 = lr/bc1[t], k2 = 1/sqrt(bc2[t]) (entry min(t, t_max) of the
+ * tables), in fp32 with every operation rounded on its own.
+ *   step      t, where step_dev is NULL
+ *   step_dev  device int32, 4-byte aligned: t is read when the step runs, so
+ *             that a captured call can be replayed for the next steps (the
+ *             caller advances it on the stream); values below 1 read as 1 in
+ *             the tables
+ *   clip      device float, 4-byte aligned, or NULL for 1.  Where it is not a
+ *             positive finite number the step is left out: no tensor changes.
+ * Arrays that the step writes must not overlap.
+ * Errors: SFT_EINVAL (null pointers, bad sizes, types, betas, eps or step,
+ * overlapping arrays), SFT_EALIGN, SFT_ENOTSUP (2^42 values in a tensor, or
+ * 2^31 chunks in a launch), SFT_EHIP; a failed argument check launches
+ * nothing.
+ */
+int sft_adamw(const sft_adamw_vec *vecs, int32_t n_vecs, int32_t step, const int32_t *step_dev, const float *clip,
+              const sft_adam *hp, void *stream);
 
 #ifdef __cplusplus
 }

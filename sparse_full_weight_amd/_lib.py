@@ -36,7 +36,7 @@ EXPORTS = (
     "sft_leaf_grad_workspace", "sft_leaf_grad", "sft_leaf_adam", "sft_helix_init", "sft_helix_step",
     "sft_helix_coupling", "sft_probe_grid", "sft_probe_read", "sft_probe_copy", "sft_probe_mfma", "sft_probe_dw_plan",
     "sft_noalloc_scratch_bytes", "sft_masked_dw_update_noalloc", "sft_plan_layer_words", "sft_plan_layer",
-    "sft_plan_upload",
+    "sft_plan_upload", "sft_grad_clip_workspace", "sft_grad_clip", "sft_adamw",
 )
 
 
@@ -130,6 +130,19 @@ class CLeafVec(C.Structure):
                 ("v", C.c_void_p), ("theta_bf16", C.c_void_p)]
 
 
+SFT_F32 = 0
+SFT_BF16 = 1
+
+
+class CGradVec(C.Structure):
+    _fields_ = [("n", C.c_int64), ("grad", C.c_void_p), ("type", C.c_int32)]
+
+
+class CAdamwVec(C.Structure):
+    _fields_ = [("n", C.c_int64), ("p", C.c_void_p), ("grad", C.c_void_p), ("m", C.c_void_p), ("v", C.c_void_p),
+                ("scale", C.c_void_p), ("p_live", C.c_void_p), ("p_type", C.c_int32), ("g_type", C.c_int32)]
+
+
 _lib: Optional[C.CDLL] = None
 
 
@@ -177,6 +190,10 @@ def lib() -> C.CDLL:
         L.sft_leaf_grad_workspace.restype = C.c_size_t
         L.sft_leaf_grad.argtypes = [C.POINTER(CLeafMat), i32, i64, p, C.c_size_t, p]
         L.sft_leaf_adam.argtypes = [C.POINTER(CLeafVec), i32, i32, C.POINTER(CAdam), p]
+        L.sft_grad_clip_workspace.argtypes = [C.POINTER(CGradVec), i32]
+        L.sft_grad_clip_workspace.restype = C.c_size_t
+        L.sft_grad_clip.argtypes = [C.POINTER(CGradVec), i32, f32, p, p, p, C.c_size_t, p]
+        L.sft_adamw.argtypes = [C.POINTER(CAdamwVec), i32, i32, p, p, C.POINTER(CAdam), p]
         L.sft_probe_grid.argtypes = []
         L.sft_probe_read.argtypes = [p, C.c_size_t, p, p]
         L.sft_probe_copy.argtypes = [p, p, C.c_size_t, p]
@@ -188,7 +205,8 @@ def lib() -> C.CDLL:
         L.sft_helix_coupling.argtypes = [C.POINTER(CHelix), C.c_double, C.c_double, C.POINTER(C.c_double),
                                          C.POINTER(C.c_double)]
         for n in EXPORTS[2:]:
-            if n not in ("sft_masked_dw_workspace", "sft_leaf_grad_workspace", "sft_noalloc_scratch_bytes"):
+            if n not in ("sft_masked_dw_workspace", "sft_leaf_grad_workspace", "sft_grad_clip_workspace",
+                         "sft_noalloc_scratch_bytes"):
                 getattr(L, n).restype = C.c_int
         _lib = L
     return _lib
@@ -911,6 +929,139 @@ def prepare_leaf_adam(vecs: Sequence[LeafVec], step: int, hp: Adam) -> Prepared:
     arr = (CLeafVec * max(len(vecs), 1))(*[v.c() for v in vecs])
     h = hp.c()
     return Prepared(lib().sft_leaf_adam, (arr, len(vecs), int(step), C.byref(h)), (arr, h, vecs, hp))
+
+
+# ------------------------------------------------------------------ dense optimizer step
+def _type(t, what) -> int:
+    import torch
+    if t.dtype == torch.float32:
+        return SFT_F32
+    if t.dtype == torch.bfloat16:
+        return SFT_BF16
+    raise TypeError(f"{what}: expected float32 or bfloat16, got {t.dtype}")
+
+
+def _one_device(tensors) -> None:
+    """The kernels run on the current device: every tensor has to be there."""
+    import torch
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != here:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{here}")
+
+
+class PreparedHere(Prepared):
+    """A prepared call that refuses to run while another device than its
+    tensors' is current."""
+
+    def __init__(self, fn, args, keep):
+        import torch
+        super().__init__(fn, args, keep)
+        self._device = torch.cuda.current_device()
+
+    def __call__(self, stream=None) -> None:
+        import torch
+        if torch.cuda.current_device() != self._device:
+            raise ValueError(f"prepared on cuda:{self._device}, called with cuda:{torch.cuda.current_device()} current")
+        super().__call__(stream)
+
+
+def _scalar(t, dtype, what):
+    """Device pointer of a tensor's single value (None -> NULL)."""
+    if t is not None and t.numel() != 1:
+        raise ValueError(f"{what}: {t.numel()} elements, expected 1")
+    return _dev(t, dtype)
+
+
+def _grad_arr(grads):
+    arr = (CGradVec * max(len(grads), 1))(*[CGradVec(g.numel(), _dev(g), _type(g, f"gradient {i}"))
+                                            for i, g in enumerate(grads)])
+    _one_device(grads)
+    return arr
+
+
+def sft_grad_clip_workspace(grads) -> int:
+    """Workspace bytes of sft_grad_clip for these gradients."""
+    n = lib().sft_grad_clip_workspace(_grad_arr(grads), len(grads))
+    if n == C.c_size_t(-1).value:
+        raise SftError(SFT_EINVAL, lib().sft_last_error().decode())
+    return n
+
+
+def prepare_grad_clip(grads, max_norm: float, clip, norm, ws) -> PreparedHere:
+    """sft_grad_clip with its arguments built once."""
+    import torch
+    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _one_device((clip, norm, ws))
+    args = (_grad_arr(grads), len(grads), float(max_norm), _scalar(clip, torch.float32, "clip"),
+            _scalar(norm, torch.float32, "norm"), _dev(ws), nbytes)
+    return PreparedHere(lib().sft_grad_clip, args, (list(grads), clip, norm, ws))
+
+
+def sft_grad_clip(grads, max_norm: float, clip, norm=None, ws=None, stream=None) -> None:
+    """Norm of the gradients (float32 or bfloat16 GPU tensors) taken together,
+    into `norm`, and the factor that clips it, into `clip` (float32 GPU
+    tensors of one element; clip is 0 where the norm is not finite).  Async
+    on the stream; ws holds sft_grad_clip_workspace(grads) bytes."""
+    prepare_grad_clip(grads, max_norm, clip, norm, ws)(stream)
+
+
+@dataclass
+class AdamwVec:
+    """One tensor of sft_adamw (any shape, contiguous): parameters and gradient
+    in float32 or bfloat16; states float32 of the same size, or 8-bit ones:
+    m and v float8_e4m3fn (v holding its square root) with scale
+    float8_e8m0fnu [ceil(n/256) x 2]."""
+    p: "object"
+    grad: "object"
+    m: "object"
+    v: "object"
+    scale: "object" = None
+    p_live: "object" = None     # bfloat16 copy of the new parameters, or None
+
+    def c(self) -> CAdamwVec:
+        import torch
+        n = self.p.numel()
+        for t, what in ((self.grad, "grad"), (self.m, "m"), (self.v, "v"), (self.p_live, "p_live")):
+            if t is not None and t.numel() != n:
+                raise ValueError(f"{what}: {t.numel()} elements, expected {n}")
+        state = torch.float32 if self.scale is None else torch.float8_e4m3fn
+        if self.scale is not None:
+            _shape(self.scale, ((n + 255) // 256, 2), "scale")
+        _one_device((self.p, self.grad, self.m, self.v, self.scale, self.p_live))
+        return CAdamwVec(n, _dev(self.p), _dev(self.grad), _dev(self.m, state), _dev(self.v, state),
+                         _dev(self.scale, torch.float8_e8m0fnu), _dev(self.p_live, torch.bfloat16),
+                         _type(self.p, "p"), _type(self.grad, "grad"))
+
+    @staticmethod
+    def alloc8(p, grad, p_live=None) -> "AdamwVec":
+        """8-bit states of zero for these parameters."""
+        import torch
+        m, v = (torch.zeros(p.shape, dtype=torch.float8_e4m3fn, device=p.device) for _ in range(2))
+        scale = torch.ones(((p.numel() + 255) // 256, 2), dtype=torch.float32, device=p.device)
+        return AdamwVec(p, grad, m, v, scale.to(torch.float8_e8m0fnu), p_live)
+
+
+def prepare_adamw(vecs: Sequence[AdamwVec], step, hp: Adam, clip=None) -> PreparedHere:
+    """sft_adamw with its arguments built once; with a GPU tensor as `step`
+    the same object takes every step."""
+    import torch
+    arr = (CAdamwVec * max(len(vecs), 1))(*[v.c() for v in vecs])
+    h = hp.c()
+    on_dev = isinstance(step, torch.Tensor)
+    _one_device((clip, hp.bc1, hp.bc2) + ((step,) if on_dev else ()))
+    args = (arr, len(vecs), 0 if on_dev else int(step), _scalar(step, torch.int32, "step") if on_dev else None,
+            _scalar(clip, torch.float32, "clip"), C.byref(h))
+    return PreparedHere(lib().sft_adamw, args, (arr, h, list(vecs), hp, step, clip))
+
+
+def sft_adamw(vecs: Sequence[AdamwVec], step, hp: Adam, clip=None, stream=None) -> None:
+    """AdamW on every tensor (async on the stream).  step: the step number
+    (>= 1), or an int32 GPU tensor of one element that the kernel reads, so
+    that a captured call can be replayed; clip: float32 GPU tensor of one
+    element that multiplies the gradients, as sft_grad_clip writes it (the
+    step is left out where it is not a positive finite number)."""
+    prepare_adamw(vecs, step, hp, clip)(stream)
 
 
 # ------------------------------------------------------------------ coupled-update schedule

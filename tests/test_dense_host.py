@@ -1,0 +1,97 @@
+"""CPU tests of the dense optimizer calls (sft_grad_clip, sft_adamw): what
+they refuse, before anything is launched."""
+import ctypes as C
+
+import numpy as np
+import pytest
+
+from sparse_full_weight_amd import _lib
+
+BUF = np.zeros(1 << 14, np.uint8)
+BASE = (BUF.ctypes.data + 255) // 256 * 256
+HP = (0.1, 0.9, 0.999, 1e-8, 0.0, BASE + 8192, BASE + 8192, 4)
+
+
+def _vec(n=16, at=BASE, scale=None, live=None, p_type=0, g_type=0):
+    return _lib.CAdamwVec(n, at, at + 1024, at + 2048, at + 3072, scale, live, p_type, g_type)
+
+
+def _adamw(vecs, step=1, hp=HP, clip=None, step_dev=None):
+    arr = (_lib.CAdamwVec * max(len(vecs), 1))(*vecs)
+    h = _lib.CAdam(*hp)
+    return _lib.lib().sft_adamw(arr, len(vecs), step, step_dev, clip, C.byref(h), None)
+
+
+def _hp(**kw):
+    names = ("lr", "beta1", "beta2", "eps", "weight_decay", "bc1", "bc2", "t_max")
+    return tuple(kw.get(k, v) for k, v in zip(names, HP))
+
+
+@pytest.mark.parametrize("what,code", [
+    (dict(vecs=[_vec(n=-1)]), _lib.SFT_EINVAL),
+    (dict(vecs=[_vec(n=1 << 42)]), _lib.SFT_ENOTSUP),
+    (dict(vecs=[_vec(p_type=2)]), _lib.SFT_EINVAL),
+    (dict(vecs=[_vec(g_type=-1)]), _lib.SFT_EINVAL),
+    (dict(vecs=[_lib.CAdamwVec(16, BASE, None, BASE + 2048, BASE + 3072, None, None, 0, 0)]), _lib.SFT_EINVAL),
+    (dict(vecs=[_vec(at=BASE + 2)]), _lib.SFT_EALIGN),
+    (dict(vecs=[_vec(live=BASE + 4097)]), _lib.SFT_EALIGN),
+    (dict(vecs=[_vec(), _vec()]), _lib.SFT_EINVAL),                              # the same tensor twice
+    (dict(vecs=[_vec(n=300), _vec(n=16, at=BASE + 4 * 296)]), _lib.SFT_EINVAL),  # p of one inside p of another
+    (dict(vecs=[_vec(live=BASE + 60)]), _lib.SFT_EINVAL),                        # the copy over the master
+    (dict(vecs=[_vec(scale=BASE + 2050)]), _lib.SFT_EINVAL),                     # the scales inside m
+    (dict(vecs=[_vec()], step=0), _lib.SFT_EINVAL),
+    (dict(vecs=[_vec()], step_dev=BASE + 2), _lib.SFT_EALIGN),
+    (dict(vecs=[_vec()], clip=BASE + 2), _lib.SFT_EALIGN),
+    (dict(vecs=[_vec()], hp=_hp(beta1=1.0)), _lib.SFT_EINVAL),
+    (dict(vecs=[_vec()], hp=_hp(beta2=float("nan"))), _lib.SFT_EINVAL),
+    (dict(vecs=[_vec()], hp=_hp(eps=-1.0)), _lib.SFT_EINVAL),
+    (dict(vecs=[_vec()], hp=_hp(t_max=0)), _lib.SFT_EINVAL),
+    (dict(vecs=[_vec()], hp=_hp(bc1=None)), _lib.SFT_EINVAL),
+])
+def test_adamw_refuses(what, code):
+    assert _adamw(**what) == code
+    assert _lib.lib().sft_last_error()
+
+
+def test_adamw_of_nothing_is_nothing():
+    assert _adamw([]) == _lib.SFT_OK
+    assert _adamw([_lib.CAdamwVec(0, None, None, None, None, None, None, 0, 1)]) == _lib.SFT_OK
+
+
+def _clip(vecs, max_norm=1.0, clip=BASE + 8192, norm=None, ws=BASE + 4096, ws_bytes=4096):
+    arr = (_lib.CGradVec * max(len(vecs), 1))(*vecs)
+    return _lib.lib().sft_grad_clip(arr, len(vecs), max_norm, clip, norm, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("what,code", [
+    (dict(vecs=[_lib.CGradVec(-1, BASE, 0)]), _lib.SFT_EINVAL),
+    (dict(vecs=[_lib.CGradVec(1 << 42, BASE, 0)]), _lib.SFT_ENOTSUP),
+    (dict(vecs=[_lib.CGradVec((1 << 42) - 1, BASE, 0)] * 5), _lib.SFT_ENOTSUP),
+    (dict(vecs=[_lib.CGradVec(8, None, 0)]), _lib.SFT_EINVAL),
+    (dict(vecs=[_lib.CGradVec(8, BASE, 7)]), _lib.SFT_EINVAL),
+    (dict(vecs=[_lib.CGradVec(8, BASE + 2, 0)]), _lib.SFT_EALIGN),
+    (dict(vecs=[_lib.CGradVec(8, BASE + 1, 1)]), _lib.SFT_EALIGN),
+    (dict(vecs=[_lib.CGradVec(8, BASE, 0)], max_norm=0.0), _lib.SFT_EINVAL),
+    (dict(vecs=[_lib.CGradVec(8, BASE, 0)], max_norm=float("nan")), _lib.SFT_EINVAL),
+    (dict(vecs=[_lib.CGradVec(8, BASE, 0)], clip=None), _lib.SFT_EINVAL),
+    (dict(vecs=[_lib.CGradVec(8, BASE, 0)], norm=BASE + 1), _lib.SFT_EALIGN),
+    (dict(vecs=[_lib.CGradVec(8, BASE, 0)], ws_bytes=7), _lib.SFT_ECAPACITY),
+    (dict(vecs=[_lib.CGradVec(8, BASE, 0)], ws=None), _lib.SFT_EINVAL),
+    (dict(vecs=[_lib.CGradVec(8, BASE, 0)], ws=BASE + 8), _lib.SFT_EALIGN),
+])
+def test_grad_clip_refuses(what, code):
+    assert _clip(**what) == code
+    assert _lib.lib().sft_last_error()
+
+
+def test_grad_clip_workspace():
+    def need(vecs):
+        return _lib.lib().sft_grad_clip_workspace((_lib.CGradVec * max(len(vecs), 1))(*vecs), len(vecs))
+
+    assert need([]) == 0
+    assert need([_lib.CGradVec(0, None, 1)]) == 0
+    assert need([_lib.CGradVec(1, BASE, 1)]) == 8
+    assert need([_lib.CGradVec(8193, BASE, 1)]) == 16
+    assert need([_lib.CGradVec(1 << 40, BASE, 1)]) == 8 * 2048
+    assert need([_lib.CGradVec(1, BASE, 1)] * 201) == 8 * 201
+    assert need([_lib.CGradVec(-1, BASE, 1)]) == C.c_size_t(-1).value
