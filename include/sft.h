@@ -758,11 +758,50 @@ int sft_leaf_adam(const sft_leaf_vec *vecs, int32_t n_vecs, int32_t step, const 
                   void *stream);
 
 /* ======================================================================= */
-/* device: the dense optimizer step                                         */
+/* device: products grouped by expert                                       */
 /* ======================================================================= */
 
 /* Storage types of the dense calls. */
 enum { SFT_F32 = 0, SFT_BF16 = 1 };
+
+/*
+ * A layer whose tokens each go through one of E weights W_e [R x C] (rows =
+ * output features, as everywhere here).  The T token rows are sorted by
+ * expert: rows first[e] .. first[e+1] belong to expert e.
+ *   first  device int32 [E + 1], ascending, 4-byte aligned.  It is read on
+ *          the device only, so that a router's counts never come back to the
+ *          host; values are clipped into [0, T], and a group that would end
+ *          before it starts is empty.  Experts may have no rows; rows before
+ *          first[0] and from first[E] on belong to none, and what a call
+ *          would write there stays as it was.
+ *   X bf16 [T x C], W bf16 [E x R x C], dY bf16 [T x R]
+ *   out_type  SFT_BF16 (rounded to nearest even) or SFT_F32
+ * Sums are in fp32 on the matrix cores, in an order that depends only on the
+ * sizes: results are deterministic, and a token's do not depend on the other
+ * tokens of its group.  No workspace, nothing allocated.
+ * Limits: R and C multiples of 8 and at most 2^20, T < 2^31, E <= 65536,
+ * fewer than 2^31 output tiles.
+ * Errors: SFT_EINVAL (null pointers, negative sizes, bad out_type),
+ * SFT_ESHAPE (R or C), SFT_EALIGN, SFT_ENOTSUP (beyond the limits), SFT_EHIP.
+ */
+
+/* Y[t, r] = sum_c X[t, c] * W_e[r, c], Y [T x R] of out_type. */
+int sft_expert_forward(int64_t E, int64_t T, int64_t R, int64_t C, const int32_t *first, const uint16_t *X,
+                       const uint16_t *W, void *Y, int32_t out_type, void *stream);
+
+/* dX[t, c] = sum_r dY[t, r] * W_e[r, c], dX [T x C] of out_type. */
+int sft_expert_dx(int64_t E, int64_t T, int64_t R, int64_t C, const int32_t *first, const uint16_t *dY,
+                  const uint16_t *W, void *dX, int32_t out_type, void *stream);
+
+/* dW_e[r, c] = sum over the rows t of expert e of dY[t, r] * X[t, c], dW
+ * [E x R x C] of out_type; 0 for an expert without rows.  accumulate != 0
+ * (fp32 only, else SFT_EINVAL): the sums are added to dW, in fp32. */
+int sft_expert_dw(int64_t E, int64_t T, int64_t R, int64_t C, const int32_t *first, const uint16_t *dY,
+                  const uint16_t *X, void *dW, int32_t out_type, int32_t accumulate, void *stream);
+
+/* ======================================================================= */
+/* device: the dense optimizer step                                         */
+/* ======================================================================= */
 
 /* One gradient of sft_grad_clip: n values of `type`, aligned to the type
  * (16-byte aligned gradients are read faster). */

@@ -37,6 +37,7 @@ EXPORTS = (
     "sft_helix_coupling", "sft_probe_grid", "sft_probe_read", "sft_probe_copy", "sft_probe_mfma", "sft_probe_dw_plan",
     "sft_noalloc_scratch_bytes", "sft_masked_dw_update_noalloc", "sft_plan_layer_words", "sft_plan_layer",
     "sft_plan_upload", "sft_grad_clip_workspace", "sft_grad_clip", "sft_adamw",
+    "sft_expert_forward", "sft_expert_dx", "sft_expert_dw",
 )
 
 
@@ -190,6 +191,9 @@ def lib() -> C.CDLL:
         L.sft_leaf_grad_workspace.restype = C.c_size_t
         L.sft_leaf_grad.argtypes = [C.POINTER(CLeafMat), i32, i64, p, C.c_size_t, p]
         L.sft_leaf_adam.argtypes = [C.POINTER(CLeafVec), i32, i32, C.POINTER(CAdam), p]
+        L.sft_expert_forward.argtypes = [i64, i64, i64, i64, p, p, p, p, i32, p]
+        L.sft_expert_dx.argtypes = [i64, i64, i64, i64, p, p, p, p, i32, p]
+        L.sft_expert_dw.argtypes = [i64, i64, i64, i64, p, p, p, p, i32, i32, p]
         L.sft_grad_clip_workspace.argtypes = [C.POINTER(CGradVec), i32]
         L.sft_grad_clip_workspace.restype = C.c_size_t
         L.sft_grad_clip.argtypes = [C.POINTER(CGradVec), i32, f32, p, p, p, C.c_size_t, p]
@@ -931,7 +935,7 @@ def prepare_leaf_adam(vecs: Sequence[LeafVec], step: int, hp: Adam) -> Prepared:
     return Prepared(lib().sft_leaf_adam, (arr, len(vecs), int(step), C.byref(h)), (arr, h, vecs, hp))
 
 
-# ------------------------------------------------------------------ dense optimizer step
+# ------------------------------------------------------------------ products grouped by expert
 def _type(t, what) -> int:
     import torch
     if t.dtype == torch.float32:
@@ -973,6 +977,73 @@ def _scalar(t, dtype, what):
     return _dev(t, dtype)
 
 
+def prepare_expert_forward(first, X, W, Y) -> PreparedHere:
+    """sft_expert_forward with its arguments built once."""
+    import torch
+    _shape(W, (None, None, None), "W")
+    E, R, Cc = W.shape
+    _shape(first, (E + 1,), "first")
+    _shape(X, (None, Cc), "X")
+    T = X.shape[0]
+    _shape(Y, (T, R), "Y")
+    _one_device((first, X, W, Y))
+    args = (E, T, R, Cc, _dev(first, torch.int32), _dev(X, torch.bfloat16), _dev(W, torch.bfloat16), _dev(Y),
+            _type(Y, "Y"))
+    return PreparedHere(lib().sft_expert_forward, args, (first, X, W, Y))
+
+
+def sft_expert_forward(first, X, W, Y, stream=None) -> None:
+    """Products grouped by expert: Y[t] = X[t] W_e^T for the rows t in
+    first[e] .. first[e+1] (async on the stream).  X bf16 [T x C] sorted by
+    expert, W bf16 [E x R x C], first int32 [E + 1], Y [T x R] bf16 or fp32;
+    rows that belong to no expert are not written."""
+    prepare_expert_forward(first, X, W, Y)(stream)
+
+
+def prepare_expert_dx(first, dY, W, dX) -> PreparedHere:
+    """sft_expert_dx with its arguments built once."""
+    import torch
+    _shape(W, (None, None, None), "W")
+    E, R, Cc = W.shape
+    _shape(first, (E + 1,), "first")
+    _shape(dY, (None, R), "dY")
+    T = dY.shape[0]
+    _shape(dX, (T, Cc), "dX")
+    _one_device((first, dY, W, dX))
+    args = (E, T, R, Cc, _dev(first, torch.int32), _dev(dY, torch.bfloat16), _dev(W, torch.bfloat16), _dev(dX),
+            _type(dX, "dX"))
+    return PreparedHere(lib().sft_expert_dx, args, (first, dY, W, dX))
+
+
+def sft_expert_dx(first, dY, W, dX, stream=None) -> None:
+    """Input gradients of sft_expert_forward: dX[t] = dY[t] W_e, dX [T x C]
+    bf16 or fp32 (async on the stream)."""
+    prepare_expert_dx(first, dY, W, dX)(stream)
+
+
+def prepare_expert_dw(first, dY, X, dW, accumulate: bool = False) -> PreparedHere:
+    """sft_expert_dw with its arguments built once."""
+    import torch
+    _shape(dW, (None, None, None), "dW")
+    E, R, Cc = dW.shape
+    _shape(first, (E + 1,), "first")
+    _shape(dY, (None, R), "dY")
+    T = dY.shape[0]
+    _shape(X, (T, Cc), "X")
+    _one_device((first, dY, X, dW))
+    args = (E, T, R, Cc, _dev(first, torch.int32), _dev(dY, torch.bfloat16), _dev(X, torch.bfloat16), _dev(dW),
+            _type(dW, "dW"), int(bool(accumulate)))
+    return PreparedHere(lib().sft_expert_dw, args, (first, dY, X, dW))
+
+
+def sft_expert_dw(first, dY, X, dW, accumulate: bool = False, stream=None) -> None:
+    """Weight gradients of sft_expert_forward: dW_e = dY_e^T X_e, dW [E x R x
+    C] bf16 or fp32, zero for experts without rows; with accumulate (fp32)
+    they are added to dW (async on the stream)."""
+    prepare_expert_dw(first, dY, X, dW, accumulate)(stream)
+
+
+# ------------------------------------------------------------------ dense optimizer step
 def _grad_arr(grads):
     arr = (CGradVec * max(len(grads), 1))(*[CGradVec(g.numel(), _dev(g), _type(g, f"gradient {i}"))
                                             for i, g in enumerate(grads)])

@@ -1,0 +1,45 @@
+"""CPU tests of the products grouped by expert (sft_expert_forward, _dx, _dw):
+what they refuse, before anything is launched."""
+import numpy as np
+import pytest
+
+from sparse_full_weight_amd import _lib
+
+BUF = np.zeros(1 << 12, np.uint8)
+BASE = (BUF.ctypes.data + 255) // 256 * 256
+GOOD = dict(E=2, T=3, R=8, C=16, first=BASE, a=BASE + 256, b=BASE + 512, out=BASE + 1024, type=0)
+
+
+def _call(op, **kw):
+    k = {**GOOD, **kw}
+    args = [k["E"], k["T"], k["R"], k["C"], k["first"], k["a"], k["b"], k["out"], k["type"]]
+    if op == "dw":
+        args.append(k.get("accumulate", 0))
+    return getattr(_lib.lib(), "sft_expert_" + op)(*args, None)
+
+
+@pytest.mark.parametrize("op", ["forward", "dx", "dw"])
+@pytest.mark.parametrize("kw,code", [
+    (dict(E=-1), _lib.SFT_EINVAL), (dict(T=-1), _lib.SFT_EINVAL), (dict(R=-8), _lib.SFT_EINVAL),
+    (dict(C=-8), _lib.SFT_EINVAL), (dict(type=2), _lib.SFT_EINVAL), (dict(type=-1), _lib.SFT_EINVAL),
+    (dict(R=12), _lib.SFT_ESHAPE), (dict(C=4), _lib.SFT_ESHAPE),
+    (dict(T=1 << 31), _lib.SFT_ENOTSUP), (dict(E=65537), _lib.SFT_ENOTSUP),
+    (dict(R=(1 << 20) + 8), _lib.SFT_ENOTSUP), (dict(C=(1 << 20) + 8), _lib.SFT_ENOTSUP),
+    (dict(first=None), _lib.SFT_EINVAL), (dict(a=None), _lib.SFT_EINVAL), (dict(b=None), _lib.SFT_EINVAL),
+    (dict(out=None), _lib.SFT_EINVAL), (dict(first=BASE + 2), _lib.SFT_EALIGN), (dict(a=BASE + 8), _lib.SFT_EALIGN),
+    (dict(b=BASE + 2), _lib.SFT_EALIGN), (dict(out=BASE + 4), _lib.SFT_EALIGN),
+    (dict(E=65536, T=(1 << 31) - 1, R=1 << 20, C=1 << 20), _lib.SFT_ENOTSUP),     # 2^31 tiles
+])
+def test_refuses(op, kw, code):
+    assert _call(op, **kw) == code
+    assert _lib.lib().sft_last_error()
+
+
+def test_dw_accumulates_only_fp32():
+    assert _call("dw", type=1, accumulate=1) == _lib.SFT_EINVAL
+
+
+@pytest.mark.parametrize("op,empty", [("forward", "ETR"), ("dx", "ETC"), ("dw", "ERC")])
+def test_nothing_to_write_is_nothing(op, empty):
+    for name in empty:
+        assert _call(op, **{name: 0}, first=None, a=None, b=None, out=None) == _lib.SFT_OK

@@ -1,0 +1,345 @@
+"""GPU tests of the products grouped by expert (sft_expert_forward, _dx, _dw)
+against fp64 products of the same inputs, at ragged groups, odd sizes and
+sizes around the kernels' tiles."""
+import numpy as np
+import pytest
+import torch
+
+from sparse_full_weight_amd import _lib
+from tests.gpu_helpers import adam_dev
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+U = 2.0 ** -24                     # half a step of fp32
+
+
+def _normal(shape, std, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * std).bfloat16()
+
+
+def _first(counts, start=0):
+    return torch.from_numpy(np.concatenate([[start], start + np.cumsum(counts)]).astype(np.int32)).cuda()
+
+
+def _check(got, a, b, what):
+    """got = a @ b in fp32 sums of exact products: each of the K additions and the joining of partial sums rounds
+    by U of a partial sum, which the sum of magnitudes bounds; (K + 4) U of it in all, and half a step of the
+    output's type."""
+    want = a.double() @ b.double()
+    bound = (a.shape[1] + 4) * U * (a.double().abs() @ b.double().abs())
+    if got.dtype == BF16:
+        bound = bound + 2.0 ** -8 * (want.abs() + bound)
+    off = ((got.double() - want).abs() - bound)
+    assert off.numel() == 0 or off.max().item() <= 0, f"{what}: {off.max().item()} beyond the bound"
+
+
+MARK = -77.0
+
+
+def _run(op, counts, R, C, out, seed=0, start=0, behind=0, integer=False, add=False):
+    """One call with the inputs' and outputs' rows that belong to no expert marked; checks all of it."""
+    E, T = len(counts), start + int(sum(counts)) + behind
+    first = _first(counts, start)
+    X, dY, W = _normal((T, C), 1.0, seed), _normal((T, R), 0.1, seed + 1), _normal((E, R, C), 0.1, seed + 2)
+    if integer:
+        X, dY, W = ((x * s).round().clamp(-3, 3) for x, s in ((X, 1.0), (dY, 10.0), (W, 10.0)))
+    for x in (X, dY):                       # rows of no expert must not reach any result
+        x[:start] = float("nan")
+        x[T - behind:] = float("nan")
+    bounds = first.tolist()
+    if op == "dw":
+        D = torch.full((E, R, C), MARK, dtype=out, device="cuda")
+        if add:
+            D = torch.randn((E, R, C), device="cuda", generator=torch.Generator(device="cuda").manual_seed(seed + 3))
+        before = D.clone()
+        _lib.sft_expert_dw(first, dY, X, D, accumulate=add)
+        for e, (lo, hi) in enumerate(zip(bounds, bounds[1:])):
+            a, b = dY[lo:hi].t(), X[lo:hi]
+            if add:                         # the old value is one more term of the sum
+                a = torch.cat([a.double(), before[e].double()], 1)
+                b = torch.cat([b.double(), torch.eye(C, device="cuda", dtype=torch.float64)])
+            elif integer:
+                assert torch.equal(D[e].double(), a.double() @ b.double())
+            _check(D[e], a, b, f"dW of expert {e}, {hi - lo} rows")
+        return D
+    N = R if op == "forward" else C
+    Y = torch.full((T, N), MARK, dtype=out, device="cuda")
+    if op == "forward":
+        _lib.sft_expert_forward(first, X, W, Y)
+    else:
+        _lib.sft_expert_dx(first, dY, W, Y)
+    for e, (lo, hi) in enumerate(zip(bounds, bounds[1:])):
+        a, b = (X[lo:hi], W[e].t()) if op == "forward" else (dY[lo:hi], W[e])
+        if integer and out == F32:
+            assert torch.equal(Y[lo:hi].double(), a.double() @ b.double())
+        _check(Y[lo:hi], a, b, f"{op} of expert {e}, {hi - lo} rows")
+    assert bool((Y[:start] == MARK).all()) and bool((Y[T - behind:] == MARK).all())
+    return Y
+
+
+OPS = ["forward", "dx", "dw"]
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("counts", [[1], [0, 1, 0], [3, 0, 5, 1, 0], [15, 16, 17, 0, 33], [63, 64, 65], [127, 1, 130],
+                                    [255, 0, 257], [300, 0, 0, 511]])
+def test_ragged_groups(gpu_lib, op, out, counts):
+    _run(op, counts, 72, 136, out, start=2, behind=3)
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("R,C", [(8, 8), (8, 4096), (4096, 8), (56, 64), (64, 72), (120, 248), (128, 128), (136, 264),
+                                 (256, 256), (264, 520), (1000, 520), (512, 1032)])
+def test_odd_sizes(gpu_lib, op, R, C):
+    _run(op, [70, 0, 5, 201], R, C, F32)
+    _run(op, [2, 1, 0, 7], R, C, BF16, behind=1)
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_integer_inputs_are_exact(gpu_lib, op):
+    # lanes, tiles and steps that were mixed up would show: every product and sum of these is exact in fp32
+    _run(op, [300, 17, 0, 140], 328, 392, F32, integer=True)
+    _run(op, [9, 16, 1, 2], 328, 392, F32, integer=True)
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("E", [1, 63, 64, 65, 200])
+def test_numbers_of_experts(gpu_lib, op, E):
+    rs = np.random.RandomState(E)
+    _run(op, list(rs.randint(0, 6, E) * (rs.rand(E) < 0.7)), 40, 72, F32, seed=E)
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_wide_training_shape(gpu_lib, op):
+    _run(op, [700, 129, 0, 1219], 1376, 4096, BF16)
+
+
+@pytest.mark.parametrize("counts", [[5, 0, 300], [0, 0, 0], [1, 1, 1]])
+def test_dw_accumulates(gpu_lib, counts):
+    _run("dw", counts, 136, 264, F32, add=True)
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_no_rows_at_all(gpu_lib, op):
+    _run(op, [0, 0], 16, 24, F32, behind=4)
+    _run(op, [0, 0], 16, 24, BF16)
+
+
+def test_empty_sums_are_zero(gpu_lib):
+    first = _first([2, 3])
+    Y = torch.full((5, 16), MARK, device="cuda")
+    _lib.sft_expert_forward(first, torch.empty((5, 0), dtype=BF16, device="cuda"),
+                            torch.empty((2, 16, 0), dtype=BF16, device="cuda"), Y)
+    assert not Y.any()
+    dX = torch.full((5, 24), MARK, device="cuda")
+    _lib.sft_expert_dx(first, torch.empty((5, 0), dtype=BF16, device="cuda"),
+                       torch.empty((2, 0, 24), dtype=BF16, device="cuda"), dX)
+    assert not dX.any()
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_values_outside_a_group_do_not_reach_it(gpu_lib, op):
+    # infinities and NaN in one expert's tokens and weights, at tile and stage ends that its neighbours share
+    counts, R, C = [37, 21, 100], 200, 136
+    first, T = _first(counts), sum(counts)
+    X, dY, W = _normal((T, C), 1.0, 1), _normal((T, R), 0.1, 2), _normal((3, R, C), 0.1, 3)
+    X[37:58], dY[37:58], W[1] = float("nan"), float("inf"), float("nan")
+    shape = {"forward": (T, R), "dx": (T, C), "dw": (3, R, C)}[op]
+    Y = torch.zeros(shape, device="cuda")
+    {"forward": lambda: _lib.sft_expert_forward(first, X, W, Y), "dx": lambda: _lib.sft_expert_dx(first, dY, W, Y),
+     "dw": lambda: _lib.sft_expert_dw(first, dY, X, Y)}[op]()
+    bad = torch.isnan(Y)
+    part = bad[1] if op == "dw" else bad[37:58]
+    assert bool(part.all())
+    assert int(bad.sum()) == part.numel()
+
+
+@pytest.mark.parametrize("op", ["forward", "dx"])
+def test_a_token_does_not_depend_on_its_group(gpu_lib, op):
+    # the same row alone, in a short group and in a long one, at the same launch sizes
+    R, C, T = 264, 200, 320
+    W = _normal((2, R, C), 0.1, 1)
+    row = _normal((1, C if op == "forward" else R), 1.0, 2)
+    seen = []
+    for at, counts in ((0, [1, 319]), (130, [200, 120]), (40, [41, 279])):
+        x = _normal((T, row.shape[1]), 1.0, 3 + at)
+        x[at] = row
+        Y = torch.zeros((T, R if op == "forward" else C), device="cuda")
+        (_lib.sft_expert_forward if op == "forward" else _lib.sft_expert_dx)(_first(counts), x, W, Y)
+        seen.append(Y[at].clone())
+    assert torch.equal(seen[0], seen[1]) and torch.equal(seen[0], seen[2])
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("first", [[5, 2, 9], [-3, 4, 4], [0, 99, 7], [50, 60, 70], [2**31 - 1, -2**31, 6]])
+def test_first_out_of_range_stays_inside(gpu_lib, op, first):
+    # clipped into [0, T]; a group that ends before it starts is empty
+    T, R, C = 8, 16, 24
+    f = torch.tensor(first, dtype=torch.int64).to(torch.int32).cuda()
+    X, dY, W = _normal((T, C), 1.0, 1), _normal((T, R), 0.1, 2), _normal((2, R, C), 0.1, 3)
+    n = {"forward": T * R, "dx": T * C, "dw": 2 * R * C}[op]
+    whole = torch.full((n + 1024,), MARK, device="cuda")
+    Y = whole[512:512 + n].view({"forward": (T, R), "dx": (T, C), "dw": (2, R, C)}[op])
+    {"forward": lambda: _lib.sft_expert_forward(f, X, W, Y), "dx": lambda: _lib.sft_expert_dx(f, dY, W, Y),
+     "dw": lambda: _lib.sft_expert_dw(f, dY, X, Y)}[op]()
+    assert bool((whole[:512] == MARK).all()) and bool((whole[512 + n:] == MARK).all())
+    for e in range(2):
+        lo = min(max(first[e], 0), T)
+        hi = min(max(first[e + 1], lo), T)
+        if op == "dw":
+            _check(Y[e], dY[lo:hi].t(), X[lo:hi], "dW")
+        elif e == 1 or first[2] >= first[1]:
+            a, b = (X, W[e].t()) if op == "forward" else (dY, W[e])
+            _check(Y[lo:hi], a[lo:hi], b, op)
+
+
+def test_weights_past_32_bits(gpu_lib):
+    # the last of the experts starts beyond 2^32 bytes into W and dW
+    E, R, C, T = 9, 16384, 16384, 40
+    counts = [0] * 7 + [3, 37]
+    W = torch.zeros((E, R, C), dtype=BF16, device="cuda")
+    W[7], W[8] = _normal((R, C), 0.1, 1), _normal((R, C), 0.1, 2)
+    X, dY, first = _normal((T, C), 1.0, 3), _normal((T, R), 0.1, 4), _first(counts)
+    Y, dX = torch.zeros((T, R), device="cuda"), torch.zeros((T, C), device="cuda")
+    _lib.sft_expert_forward(first, X, W, Y)
+    _lib.sft_expert_dx(first, dY, W, dX)
+    for e, lo, hi in ((7, 0, 3), (8, 3, 40)):
+        _check(Y[lo:hi], X[lo:hi], W[e].t(), "forward")
+        _check(dX[lo:hi], dY[lo:hi], W[e], "dx")
+    _lib.sft_expert_dw(first, dY, X, W)
+    for e, lo, hi in ((6, 0, 0), (7, 0, 3), (8, 3, 40)):
+        _check(W[e][-300:], dY[lo:hi, -300:].t(), X[lo:hi], "dw")
+
+
+def test_tokens_past_32_bits(gpu_lib):
+    # a token array of more than 2^32 bytes, groups at its end
+    T, R, C = 1_100_000, 2048, 64
+    counts = [1_099_000, 700, 300]
+    first, W = _first(counts), _normal((3, R, C), 0.1, 2)
+    X, Y = _normal((T, C), 1.0, 3), torch.zeros((T, R), dtype=BF16, device="cuda")
+    _lib.sft_expert_forward(first, X, W, Y)
+    for e, lo, hi in ((0, 1_098_900, 1_099_000), (1, 1_099_000, 1_099_700), (2, 1_099_700, T)):
+        _check(Y[lo:hi], X[lo:hi], W[e].t(), "forward")
+    dX = torch.zeros((T, C), device="cuda")
+    _lib.sft_expert_dx(first, Y, W, dX)
+    for e, lo, hi in ((0, 1_098_900, 1_099_000), (1, 1_099_000, 1_099_700), (2, 1_099_700, T)):
+        _check(dX[lo:hi], Y[lo:hi], W[e], "dx")
+    dW = torch.zeros((3, R, C), device="cuda")
+    _lib.sft_expert_dw(first, Y, X, dW)
+    for e, lo, hi in ((1, 1_099_000, 1_099_700), (2, 1_099_700, T)):
+        _check(dW[e], Y[lo:hi].t(), X[lo:hi], "dw")
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("wrong", ["first", "T", "R", "strided", "out", "in type", "host"])
+def test_python_refuses(gpu_lib, op, wrong):
+    E, T, R, C = 2, 6, 16, 24
+    first, X, dY, W = _first([3, 3]), _normal((T, C), 1.0, 1), _normal((T, R), 1.0, 2), _normal((E, R, C), 1.0, 3)
+    a, b, call = {"forward": (X, W, _lib.sft_expert_forward), "dx": (dY, W, _lib.sft_expert_dx),
+                  "dw": (dY, X, _lib.sft_expert_dw)}[op]
+    out = torch.zeros({"forward": (T, R), "dx": (T, C), "dw": (E, R, C)}[op], device="cuda")
+    if wrong == "first":
+        first = first[:-1]
+    elif wrong == "T":
+        if op == "dw":
+            b = b[:-1]
+        else:
+            out = out[:-1]
+    elif wrong == "R":
+        a = a[:, :8].contiguous()
+    elif wrong == "strided":
+        a = torch.cat([a, a], 1)[:, :a.shape[1]]
+    elif wrong == "out":
+        out = out.half()
+    elif wrong == "in type":
+        a = a.float()
+    else:
+        b = b.cpu()
+    with pytest.raises((TypeError, ValueError)):
+        call(first, a, b, out)
+
+
+def _layer_step(first, X, W, dY, p, vec, hp, ws, clip, norm, Y, dX, dW, step):
+    return [_lib.prepare_expert_forward(first, X, W, Y), _lib.prepare_expert_dx(first, dY, W, dX),
+            _lib.prepare_expert_dw(first, dY, X, dW), _lib.prepare_grad_clip([dW], 0.5, clip, norm, ws),
+            _lib.prepare_adamw([vec], step, hp, clip)]
+
+
+@pytest.mark.parametrize("held", [False, True])
+def test_training_steps_of_an_expert_layer(gpu_lib, held):
+    # forward, gradients, clip and update as a training step uses them, captured once and replayed with other routings and
+    # tokens, against the formulas step by step
+    E, T, R, C = 5, 300, 136, 200
+    X, dY, W = _normal((T, C), 1.0, 1), _normal((T, R), 0.1, 2), _normal((E, R, C), 0.1, 3)
+    p = W.float()
+    first = _first([0] * E)
+    Y, dX, dW = (torch.zeros(s, dtype=t, device="cuda") for s, t in (((T, R), BF16), ((T, C), BF16), ((E, R, C), F32)))
+    vec = _lib.AdamwVec.alloc8(p, dW, W) if held else _lib.AdamwVec(p, dW, torch.zeros_like(p), torch.zeros_like(p),
+                                                                    None, W)
+    hp = adam_dev(lr=1e-2, weight_decay=0.1)
+    clip, norm = torch.zeros(1, device="cuda"), torch.zeros(1, device="cuda")
+    ws = torch.empty(_lib.sft_grad_clip_workspace([dW]), dtype=torch.uint8, device="cuda")
+    step = torch.zeros(1, dtype=torch.int32, device="cuda")
+    calls = _layer_step(first, X, W, dY, p, vec, hp, ws, clip, norm, Y, dX, dW, step)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step += 1
+        for c in calls:
+            c()
+    rs = np.random.RandomState(0)
+    m = v = torch.zeros((E, R, C), dtype=torch.float64, device="cuda")
+    for t in range(1, 5):
+        counts = rs.multinomial(T - 7, rs.dirichlet(np.ones(E)))
+        first.copy_(_first(counts))
+        X.copy_(_normal((T, C), 1.0, 10 * t))
+        dY.copy_(_normal((T, R), 0.1, 10 * t + 1))
+        W0, p0 = W.clone(), p.double()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        bounds = first.tolist()
+        for e, (lo, hi) in enumerate(zip(bounds, bounds[1:])):
+            _check(Y[lo:hi], X[lo:hi], W0[e].t(), "forward")
+            _check(dX[lo:hi], dY[lo:hi], W0[e], "dx")
+            _check(dW[e], dY[lo:hi].t(), X[lo:hi], "dw")
+        true = dW.double().square().sum().sqrt().item()
+        assert norm.item() == pytest.approx(true, rel=2 * U) and clip.item() == pytest.approx(0.5 / true, rel=2 * U)
+        if not held:
+            g = dW.double() * clip.double()
+            m, v = 0.9 * m + 0.1 * g, 0.999 * v + 0.001 * g * g
+            u = 1e-2 * (m / (1 - 0.9 ** t)) / ((v / (1 - 0.999 ** t)).sqrt() + 1e-8)
+            want = p0 * (1 - 1e-3) - u
+            # betas and rates are fp32 numbers and the moments' cancellations stay small against the step's size 1e-2
+            assert (p.double() - want).abs().max().item() <= 1e-2 * 1e-4
+        else:
+            assert (p.double() - p0).abs().max().item() <= 1.2e-2
+        assert torch.equal(W, p.bfloat16())
+
+
+@pytest.mark.parametrize("op", ["forward", "dw"])
+def test_gradients_agree_with_differences(gpu_lib, op):
+    # <dY, Y> is linear in X and in W: a change of one of them changes it by exactly <gradient, change>
+    counts, R, C = [40, 0, 25], 72, 56
+    T = sum(counts)
+    first = _first(counts)
+    X, dY, W = _normal((T, C), 1.0, 1), _normal((T, R), 1.0, 2), _normal((3, R, C), 1.0, 3)
+
+    def loss(x, w):
+        Y = torch.zeros((T, R), device="cuda")
+        _lib.sft_expert_forward(first, x, w, Y)
+        return (Y.double() * dY.double()).sum().item()
+
+    if op == "forward":
+        other, grad = _normal((T, C), 1.0, 4), torch.zeros((T, C), device="cuda")
+        _lib.sft_expert_dx(first, dY, W, grad)
+        change, got = loss(other, W) - loss(X, W), (grad.double() * (other.double() - X.double())).sum().item()
+    else:
+        other, grad = _normal((3, R, C), 1.0, 4), torch.zeros((3, R, C), device="cuda")
+        _lib.sft_expert_dw(first, dY, X, grad)
+        change, got = loss(X, other) - loss(X, W), (grad.double() * (other.double() - W.double())).sum().item()
+    # both sides are sums of T*R*C products in fp32 pieces of at most 72 terms
+    assert abs(change - got) <= 4 * (72 + 4) * U * T * R * C ** 0.5 * 4
