@@ -27,9 +27,9 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short short4v __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kBK = 64;                       // k of one stage: four matrix steps of 16
+constexpr int kThreads = 256;                 // 2 x 2 waves
 constexpr uint32_t kOutside = 0x80000000u;    // an offset beyond every buffer's size: reads as zero
 constexpr int kGroupM = 8;                    // m-tiles that are walked together along n
 
@@ -41,7 +41,8 @@ struct ExpertParams {
     const int32_t *first;
     int64_t T, R, C;
     int32_t E;
-    int32_t chunk;          // consecutive tiles that one XCD takes
+    int32_t chunk;          // consecutive units that one XCD takes
+    int32_t cus;            // compute units: a launch that ends in a short round cuts its tiles in half
 };
 
 // s_waitcnt vmcnt(n) alone, and lgkmcnt(0) alone (gfx9 encoding).
@@ -59,9 +60,10 @@ __device__ __forceinline__ uint64_t uniform64(uint64_t x) {
 }
 
 // ------------------------------------------------------------------ tiles
-// One output tile: expert e, its token rows [lo, lo + n), tile position.
+// One output tile of an expert's product: its token rows [lo, lo + n), the
+// tile's position, and which half of its columns (-1: all).
 struct Tile {
-    int32_t e, lo, n, mt, nt;
+    int32_t e, lo, n, mt, nt, half;
 };
 
 // Expert e's rows, whatever first[] holds: inside [0, T], never negative.
@@ -72,10 +74,19 @@ __device__ __forceinline__ int2 rows_of(const ExpertParams &p, int32_t e) {
 }
 
 // Workgroups are dealt to the 8 XCDs in turn; an XCD takes runs of `chunk`
-// neighbouring tiles, which share operand panels in its L2.
-__device__ __forceinline__ int32_t tile_index(const ExpertParams &p) {
+// neighbouring units, which share operand panels in its L2.
+__device__ __forceinline__ int32_t unit_index(const ExpertParams &p) {
     const int32_t b = blockIdx.x, x = b & 7, i = b >> 3;
     return ((i / p.chunk) * 8 + x) * p.chunk + i % p.chunk;
+}
+
+// Unit u of a launch of `tiles` tiles: whole tiles, and where the last round
+// of workgroups would fill half of the CUs or less, that round's tiles as two
+// halves along n.
+__device__ __forceinline__ int32_t tile_of_unit(const ExpertParams &p, int32_t u, int32_t tiles, int32_t &half) {
+    const int32_t last = tiles % p.cus, whole = tiles - (2 * last <= p.cus ? last : 0);
+    half = u < whole ? -1 : (u - whole) & 1;
+    return u < whole ? u : whole + ((u - whole) >> 1);
 }
 
 // Tiles of an expert in walking order: groups of kGroupM m-tiles, n outside,
@@ -89,11 +100,20 @@ __device__ __forceinline__ void place(Tile &t, int32_t i, int32_t m_tiles, int32
 
 // The tile of this workgroup, or false where there is none: the host only
 // knows how many tiles there can be at most.  64 experts at a time, a lane
-// each: their tile counts, the running sum, and the lane whose range holds
-// the index.
-template <int BM, int BN>
+// each: their tile counts, and the running sum whose range holds the index.
+template <int BM, bool kHalves>
 __device__ __forceinline__ bool token_tile(const ExpertParams &p, int32_t n_tiles, Tile &t) {
-    const int32_t v = tile_index(p), lane = threadIdx.x & 63;
+    const int32_t u = unit_index(p), lane = threadIdx.x & 63;
+    int32_t v = u;
+    t.half = -1;
+    if constexpr (kHalves) {
+        int32_t tiles = 0;
+        for (int32_t e0 = 0; e0 < p.E; e0 += 64)
+            tiles += e0 + lane < p.E ? (rows_of(p, e0 + lane).y + BM - 1) / BM : 0;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) tiles += __shfl_xor(tiles, d);
+        v = tile_of_unit(p, u, uniform(tiles) * n_tiles, t.half);
+    }
     int32_t before = 0;
     for (int32_t e0 = 0; e0 < p.E; e0 += 64) {
         const int32_t e = e0 + lane;
@@ -124,34 +144,44 @@ __device__ __forceinline__ bool token_tile(const ExpertParams &p, int32_t n_tile
 }
 
 // ------------------------------------------------------------------ operands
-__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, void *lds) {
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
+typedef __attribute__((address_space(3))) short4v lds_short4v;
+
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, lds_u8 *lds) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)(lds), 16, voff, 0, 0, 0);
-}
-__device__ __forceinline__ short4v lds_tr16(const uint8_t *p) {
-    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) short4v *)(p));
 }
 
 // One operand of a tile: how its stages of kBK k-values get into LDS and how
-// a wave reads matrix fragments from there.  W: rows (m or n) of the tile, NW:
-// waves of the workgroup.  A stage is copied by pieces of 1 KB, 16 bytes a
-// lane, of which a wave takes every NW-th.
+// a wave reads matrix fragments from there.  W: rows (m or n) of the tile.  A
+// stage is copied by pieces of 1 KB, 16 bytes a lane, of which a wave takes
+// every NW-th.
 //
-// kTr false (k contiguous): LDS row = one m, 128 bytes, 8 groups of 16 bytes;
-// group g sits in slot g ^ (row % 8), so that 8 lanes reading one group of 8
-// rows hit all banks.  kTr true (m contiguous): LDS row = one k, 2W bytes;
-// group g sits in slot g ^ 2*(row % 4), so that the four rows of a transposing
-// read hit distinct banks.
-template <bool kTr, int W, int NW>
+// kTr false (k contiguous): LDS row = one m, kBK values in groups of 16 bytes,
+// each group in slot g ^ (row/2 % 8), or g ^ (row/4 % 4) of the shorter rows,
+// so that 16 lanes reading one group of 16 rows hit all 64 banks.  kTr true (m
+// contiguous): LDS row = one k, 2W bytes; a transposing read takes, by 32
+// lanes, 64 bytes of four rows: group g sits in slot g ^ 4*(row % 4) where
+// rows are whole multiples of 256 bytes, and in g ^ 4*(row/2 % 2) where every
+// second row starts 128 bytes on, so that these hit all banks too.
+template <bool kTr, int W, int kBK>
 struct Operand {
+    static constexpr int NW = kThreads / 64;
     static constexpr int kBytes = W * kBK * 2;
     static constexpr int kLoads = kBytes / 1024 / NW;
     static_assert(kLoads * 1024 * NW == kBytes, "a stage is its waves' pieces");
-    static constexpr int kRowLanes = kTr ? W / 8 : 8;     // lanes of a piece that share an LDS row
+    static constexpr int kShift = kBK == 32 ? 2 : 1;
+    static __device__ __forceinline__ int turn(int row) {
+        if constexpr (!kTr) return row >> kShift & (kBK / 8 - 1);
+        else return W % 128 ? 4 * (row >> 1 & 1) : 4 * (row & 3);
+    }
+    static constexpr int kRowLanes = kTr ? W / 8 : kBK / 8;     // groups of 16 bytes in an LDS row
 
     const uint8_t *base;      // of the next stage's first byte (wave-uniform)
     int64_t left;             // bytes from there to the end of what is valid
     int64_t step;             // bytes from one stage to the next
     uint32_t voff[kLoads];
+    int32_t from[kTr ? 4 : 1];
     int32_t kgrp;             // k of the lane's 16 bytes inside a stage (k contiguous)
 
     // mem: first row of the tile (k contiguous) or first column (m contiguous)
@@ -165,20 +195,18 @@ struct Operand {
         step = static_cast<int64_t>(uniform64(static_cast<uint64_t>(kTr ? kBK * ld * 2 : kBK * 2)));
 #pragma unroll
         for (int k = 0; k < kLoads; ++k) {
-            const int row = (64 / kRowLanes) * (wave + NW * k) + lane / kRowLanes;
-            const int slot = lane % kRowLanes;
-            const int grp = kTr ? slot ^ (2 * (row & 3)) : slot ^ (row & 7);
+            const int at = 64 * (wave + NW * k) + lane, row = at / kRowLanes, grp = at % kRowLanes ^ turn(row);
             if constexpr (kTr) {
                 voff[k] = 8 * grp < cols ? static_cast<uint32_t>((row * ld + 8 * grp) * 2) : kOutside;
             } else {
                 voff[k] = row < valid ? static_cast<uint32_t>((row * ld + 8 * grp) * 2) : kOutside;
-                kgrp = 8 * grp;   // row % 8 is the same for every piece of the lane
+                kgrp = 8 * grp;   // the turn is the same for every piece of the lane
             }
         }
     }
 
     // Copies the next stage; k_left = valid k-values from it on.
-    __device__ __forceinline__ void issue(uint8_t *lds, int32_t k_left) {
+    __device__ __forceinline__ void issue(lds_u8 *lds, int32_t k_left) {
         const int wave = uniform(threadIdx.x >> 6);
         const int32_t size = static_cast<int32_t>(left <= 0 ? 0 : left > 0x7fffffff ? 0x7fffffff : left);
         const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base),
@@ -194,82 +222,84 @@ struct Operand {
         left -= step;
     }
 
-    // Fragments: 32 rows (m) of matrix step kk; lane l holds row l % 32,
-    // k = 8 * (l / 32) + 0..7.  at: first row of the wave's part of the tile.
-    template <int F>
-    __device__ __forceinline__ void read(const uint8_t *lds, int at, int kk, bf16x8 (&f)[F]) const {
+    // Where a wave reads its part of the tile, `at` = its first row.  The
+    // empty asm keeps the compiler from taking the offset apart again: behind
+    // a chain of pointer sums it loses track of which stage a read is from,
+    // and waits for every copy in flight.
+    __device__ __forceinline__ void read_from(int at) {
         const int lane = threadIdx.x & 63;
         if constexpr (kTr) {
-            const int s = lane & 15, row = 16 * kk + 8 * (lane >> 5) + (s >> 2);
-            const int col = ((lane >> 4) & 1) * 16 + 4 * (s & 3);
+            const int s = lane & 15, col = ((lane >> 4) & 1) * 16 + 4 * (s & 3);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int grp = (at + 32 * i) / 8 + (col >> 3);
+                from[i] = (8 * (lane >> 5) + (s >> 2)) * (2 * W) + 16 * (grp ^ turn(s >> 2)) + 2 * (col & 7);
+                asm volatile("" : "+v"(from[i]));
+            }
+        } else {
+            from[0] = at + (lane & 31);
+        }
+    }
+
+    // Fragments: 32 rows (m) of matrix step kk; lane l holds row l % 32,
+    // k = 8 * (l / 32) + 0..7.
+    template <int F>
+    __device__ __forceinline__ void read(lds_u8 *lds, int kk, bf16x8 (&f)[F]) const {
+        const int lane = threadIdx.x & 63;
+        if constexpr (kTr) {
 #pragma unroll
             for (int i = 0; i < F; ++i) {
-                const int grp = (at + 32 * i) / 8 + (col >> 3);
-                const uint8_t *q = lds + row * (2 * W) + 16 * (grp ^ (2 * (s >> 2))) + 2 * (col & 7);
-                const short4v lo = lds_tr16(q), hi = lds_tr16(q + 4 * 2 * W);
+                lds_u8 *q = lds + from[i];
+                const short4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4v *)(q + 16 * kk * 2 * W));
+                const short4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4v *)(q + (16 * kk + 4) * 2 * W));
                 f[i] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
             }
         } else {
-            const int row = at + (lane & 31);
+            const int row = from[0];
 #pragma unroll
             for (int i = 0; i < F; ++i)
-                f[i] = *reinterpret_cast<const bf16x8 *>(lds + (row + 32 * i) * 128 +
-                                                         16 * ((2 * kk + (lane >> 5)) ^ (lane & 7)));
+                f[i] = *(lds_bf16x8 *)(lds + ((row + 32 * i) * (2 * kBK) + 16 * ((2 * kk + (lane >> 5)) ^ turn(lane))));
         }
     }
 };
 
-// Two stages of each operand, as LDS variables of their own so that the
-// compiler can tell copies into one from reads of the other.
-template <int BM, int BN, int S>
-struct Stage {
-    static __device__ __forceinline__ uint8_t *a() {
-        __shared__ __attribute__((aligned(1024))) uint8_t m[BM * kBK * 2];
-        return m;
-    }
-    static __device__ __forceinline__ uint8_t *b() {
-        __shared__ __attribute__((aligned(1024))) uint8_t m[BN * kBK * 2];
-        return m;
-    }
-};
-
-// ------------------------------------------------------------------ the product
-template <class Out, bool kAdd>
-__device__ __forceinline__ void store4(Out *o, f32x4 x) {
-    if constexpr (std::is_same<Out, float>::value) {
-        f32x4 *q = reinterpret_cast<f32x4 *>(o);
-        *q = kAdd ? *q + x : x;
-    } else {
-        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-        *reinterpret_cast<u32x2 *>(o) = __builtin_bit_cast(
-            u32x2, bf16x4{static_cast<__bf16>(x.x), static_cast<__bf16>(x.y), static_cast<__bf16>(x.z),
-                          static_cast<__bf16>(x.w)});
-    }
+// The stages of each operand, as LDS variables of their own so that the
+// compiler can tell copies into one from reads of the other; W: rows of the
+// largest tile of the kernel.
+template <int kBytes, int kOperand, int S>
+__device__ __forceinline__ lds_u8 *stage() {
+    __shared__ __attribute__((aligned(1024))) uint8_t m[kBytes];
+    return (lds_u8 *)m;
 }
 
-// WM x WN waves; each takes (BM/WM) x (BN/WN) of the tile in blocks of 32 x 32.
-template <int kOp, int BM, int BN, int WM, int WN, class Out, bool kAdd>
-__global__ __launch_bounds__(WM *WN * 64, 2) void k_expert(const ExpertParams p) {
-    constexpr int NW = WM * WN, FM = BM / WM / 32, FN = BN / WN / 32;
-    typedef Operand<kOp == kDw, BM, NW> A;
-    typedef Operand<kOp != kForward, BN, NW> B;
+// ------------------------------------------------------------------ the product
+// Two values rounded to bf16, nearest even.
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(a), static_cast<__bf16>(b)});
+}
+
+constexpr int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
+
+// A kernel's tiles: kM x kN, by stages of kBK along k, kStages of them in LDS;
+// kPerCu workgroups share a CU.
+template <int M_, int N_, int BK_, int STAGES_>
+struct Shape {
+    static constexpr int kM = M_, kN = N_, kBK = BK_, kStages = STAGES_;
+    static constexpr int kLds = (kM + kN) * kBK * 2 * kStages;
+    static constexpr int kPerCu = 160 * 1024 / kLds < 4 ? 160 * 1024 / kLds : 4;
+};
+
+// BM x BN from (m0, n0) on of expert t.e's product, by 2 x 2 waves, each
+// (BM/2) x (BN/2) in blocks of 32 x 32.
+template <int kOp, class S, int BM, int BN, class Out, bool kAdd>
+__device__ __forceinline__ void multiply_part(const ExpertParams &p, const Tile &t, int64_t m0, int64_t n0) {
+    constexpr int FM = BM / 64, FN = BN / 64, kBK = S::kBK, kStages = S::kStages, KK = kBK / 16;
+    constexpr int SA = S::kM * kBK * 2, SB = S::kN * kBK * 2;
+    typedef Operand<kOp == kDw, BM, kBK> A;
+    typedef Operand<kOp != kForward, BN, kBK> B;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int64_t N = kOp == kForward ? p.R : p.C;
-    const int32_t n_tiles = static_cast<int32_t>((N + BN - 1) / BN);
-
-    Tile t;
-    if constexpr (kOp == kDw) {
-        const int32_t m_tiles = static_cast<int32_t>((p.R + BM - 1) / BM), v = tile_index(p);
-        t.e = v / (m_tiles * n_tiles);
-        if (t.e >= p.E) return;
-        const int2 r = rows_of(p, t.e);
-        t.lo = r.x;
-        t.n = r.y;
-        place(t, v - t.e * m_tiles * n_tiles, m_tiles, n_tiles);
-    } else {
-        if (!token_tile<BM, BN>(p, n_tiles, t)) return;
-    }
-    const int64_t m0 = static_cast<int64_t>(t.mt) * BM, n0 = static_cast<int64_t>(t.nt) * BN;
     const int64_t K = kOp == kForward ? p.C : kOp == kDx ? p.R : t.n;
     const int64_t M = kOp == kDw ? p.R : t.n;
 
@@ -295,62 +325,161 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void k_expert(const ExpertParams p)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-    const int am = (wave / WN) * (BM / WM), bn = (wave % WN) * (BN / WN);
-    const int32_t KT = static_cast<int32_t>((K + kBK - 1) / kBK), k32 = static_cast<int32_t>(K);
+    const int am = (wave >> 1) * (BM / 2), bn = (wave & 1) * (BN / 2);
+    a.read_from(am);
+    b.read_from(bn);
+    const int32_t k32 = static_cast<int32_t>(K), KT = (k32 + kBK - 1) / kBK;
     auto issue = [&](auto s, int32_t kt) __attribute__((always_inline)) {
-        constexpr int S = decltype(s)::value;
-        a.issue(Stage<BM, BN, S>::a(), k32 - kt * kBK);
-        b.issue(Stage<BM, BN, S>::b(), k32 - kt * kBK);
+        constexpr int I = decltype(s)::value;
+        a.issue(stage<SA, 0, I>(), k32 - kt * kBK);
+        b.issue(stage<SB, 1, I>(), k32 - kt * kBK);
     };
-    // One stage: its copies have landed for this wave (and, behind the
-    // barrier, for all); the next stage's are on their way while it is used.
-    auto use = [&](auto s, int32_t kt) __attribute__((always_inline)) {
-        constexpr int S = decltype(s)::value;
-        if (kt + 1 < KT) {
-            issue(ic<1 - S>{}, kt + 1);
-            SFT_WAIT_VMCNT(A::kLoads + B::kLoads);
-        } else {
-            SFT_WAIT_VMCNT(0);
+    auto read = [&](auto s, int kk, bf16x8 (&fa)[FM], bf16x8 (&fb)[FN]) __attribute__((always_inline)) {
+        constexpr int I = decltype(s)::value;
+        a.read(stage<SA, 0, I>(), kk, fa);
+        b.read(stage<SB, 1, I>(), kk, fb);
+    };
+    auto multiply = [&](const bf16x8 (&fa)[FM], const bf16x8 (&fb)[FN]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+    };
+    // The fragments of a matrix step are read while the step before is
+    // multiplied, across stages too: a stage's last step needs nothing from
+    // LDS, so the wait for the next stage and the barrier stand before it.
+    // Behind the barrier every wave has read this stage whole, and the copies
+    // of the stage kStages ahead go into its place.  Stages past K are copied
+    // as zeros from an empty buffer, so every wave has the same copies in
+    // flight at every wait.  The compiler would sink each read to its use:
+    // the groups below spread reads and copies evenly between the products
+    // (forward at 256 x 256: 742 us, 885 us as the compiler orders them).
+    constexpr int kReads = FM * (kOp == kDw ? 2 : 1) + FN * (kOp == kForward ? 1 : 2), kMul = FM * FN;
+    constexpr int kGroups = gcd(kReads, kMul), kCopies = (A::kLoads + B::kLoads + kGroups - 1) / kGroups;
+    auto weave = [&](auto copies) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x100, kReads / kGroups, 0);                        // LDS reads
+            if constexpr (decltype(copies)::value) __builtin_amdgcn_sched_group_barrier(0x020, kCopies, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, kMul / kGroups, 0);                          // MFMA
         }
-        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    constexpr int kInFlight = (kStages - 2) * (A::kLoads + B::kLoads);
+    bf16x8 fa[2][FM], fb[2][FN];
+    auto use = [&](auto s, int32_t kt) __attribute__((always_inline)) {
+        constexpr int I = decltype(s)::value;
 #pragma unroll
-        for (int kk = 0; kk < kBK / 16; ++kk) {
-            bf16x8 fa[FM], fb[FN];
-            a.read(Stage<BM, BN, S>::a(), am, kk, fa);
-            b.read(Stage<BM, BN, S>::b(), bn, kk, fb);
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int j = 0; j < FN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+        for (int kk = 0; kk + 1 < KK; ++kk) {
+            read(s, kk + 1, fa[(kk + 1) & 1], fb[(kk + 1) & 1]);
+            multiply(fa[kk & 1], fb[kk & 1]);
+            weave(ic<0>{});
         }
         SFT_WAIT_LGKM0();
+        SFT_WAIT_VMCNT(kInFlight);
         __builtin_amdgcn_s_barrier();
+        issue(s, kt + kStages);
+        read(ic<(I + 1) % kStages>{}, 0, fa[0], fb[0]);
+        multiply(fa[1], fb[1]);
+        weave(ic<1>{});
     };
-    if (KT > 0) issue(ic<0>{}, 0);
-    for (int32_t kt = 0; kt < KT; kt += 2) {
-        use(ic<0>{}, kt);
-        if (kt + 1 < KT) use(ic<1>{}, kt + 1);
+    auto each = [&](auto f) __attribute__((always_inline)) {
+        f(ic<0>{});
+        f(ic<1>{});
+        if constexpr (kStages > 2) f(ic<2>{});
+        if constexpr (kStages > 3) f(ic<3>{});
+    };
+    static_assert(kStages >= 2 && kStages <= 4 && KK % 2 == 0, "stages");
+    if (KT > 0) {
+        each([&](auto s) __attribute__((always_inline)) { issue(s, decltype(s)::value); });
+        SFT_WAIT_VMCNT((kStages - 1) * (A::kLoads + B::kLoads));
+        __builtin_amdgcn_s_barrier();
+        read(ic<0>{}, 0, fa[0], fb[0]);
+        for (int32_t kt = 0; kt < KT; kt += kStages)
+            each([&](auto s) __attribute__((always_inline)) { use(s, kt + decltype(s)::value); });
     }
+    SFT_WAIT_VMCNT(0);   // no copy may land in LDS that is another workgroup's by then
 
     // Lane l holds, for row l % 32 of block (i, j), the columns
     // 8*(r/4) + 4*(l/32) + r%4 of register r: four neighbours a register quad.
+    // For bf16 the halves of the wave trade quads, after which a lane holds
+    // eight neighbours: 16-byte stores.
     Out *out = static_cast<Out *>(p.out) +
                (kOp == kDw ? static_cast<int64_t>(t.e) * p.R * p.C : static_cast<int64_t>(t.lo) * N);
+    const int half = lane >> 5;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const int64_t m = m0 + am + 32 * i + (lane & 31);
-        if (m >= M) continue;
+        Out *row = out + m * N;
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
+        for (int j = 0; j < FN; ++j) {
+            const int64_t n = n0 + bn + 32 * j;
+            const floatx16 &x = acc[i][j];
+            if constexpr (std::is_same<Out, float>::value) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int64_t n = n0 + bn + 32 * j + 8 * q + 4 * (lane >> 5);
-                if (n < N)
-                    store4<Out, kAdd>(out + m * N + n, f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1],
-                                                            acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]});
+                for (int q = 0; q < 4; ++q) {
+                    f32x4 *o = reinterpret_cast<f32x4 *>(row + n + 8 * q + 4 * half);
+                    f32x4 v{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
+                    if (m < M && n + 8 * q + 4 * half < N) *o = kAdd ? *o + v : v;
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; q += 2) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) w[c] = pack2(x[4 * q + 2 * c], x[4 * q + 2 * c + 1]);
+                    const auto lo = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+                    const auto hi = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+                    const int64_t c = n + 8 * (q + half);
+                    if (m < M && c < N)
+                        *reinterpret_cast<u32x4 *>(row + c) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+                }
             }
+        }
     }
+}
+
+// The last rows of an expert take a tile of the height that they need, in
+// steps of 64.
+template <int kOp, class S, int BM, int BN, class Out, bool kAdd>
+__device__ __forceinline__ void multiply_rows(const ExpertParams &p, const Tile &t, int64_t m0, int64_t n0,
+                                              int64_t rows) {
+    if constexpr (kOp != kDw && BM > 64) {
+        if (rows <= BM - 64) return multiply_rows<kOp, S, BM - 64, BN, Out, kAdd>(p, t, m0, n0, rows);
+    }
+    multiply_part<kOp, S, BM, BN, Out, kAdd>(p, t, m0, n0);
+}
+
+template <int kOp, class S, class Out, bool kAdd>
+__global__ __launch_bounds__(kThreads, S::kPerCu) void k_expert(const ExpertParams p) {
+    constexpr bool kHalves = S::kPerCu == 1;
+    const int64_t N = kOp == kForward ? p.R : p.C;
+    const int32_t n_tiles = static_cast<int32_t>((N + S::kN - 1) / S::kN);
+    Tile t;
+    if constexpr (kOp == kDw) {
+        const int32_t m_tiles = static_cast<int32_t>((p.R + S::kM - 1) / S::kM), each = m_tiles * n_tiles;
+        const int32_t v = unit_index(p);
+        t.e = v / each;
+        if (t.e >= p.E) return;
+        const int2 r = rows_of(p, t.e);
+        t.lo = r.x;
+        t.n = r.y;
+        t.half = -1;
+        place(t, v - t.e * each, m_tiles, n_tiles);
+    } else {
+        if (!token_tile<S::kM, kHalves>(p, n_tiles, t)) return;
+    }
+    const int64_t m0 = static_cast<int64_t>(t.mt) * S::kM, n0 = static_cast<int64_t>(t.nt) * S::kN;
+    const int64_t rows = kOp == kDw ? S::kM : t.n - m0;
+    if constexpr (kHalves && kOp != kDw) {
+        if (t.half >= 0) {
+            const int64_t n = n0 + t.half * (S::kN / 2);
+            if (n < N) multiply_rows<kOp, S, S::kM, S::kN / 2, Out, kAdd>(p, t, m0, n, rows);
+            return;
+        }
+    }
+    multiply_rows<kOp, S, S::kM, S::kN, Out, kAdd>(p, t, m0, n0, rows);
 }
 
 // ------------------------------------------------------------------ host
@@ -370,34 +499,80 @@ int check(const char *who, int64_t E, int64_t T, int64_t R, int64_t C, const voi
     return SFT_OK;
 }
 
-template <int kOp, int BM, int BN, int WM, int WN>
+// Output tiles of a shape at most: the counts of the experts are on the device.
+template <int kOp>
+int64_t tiles_of(const ExpertParams &p, int64_t kM, int64_t kN) {
+    const int64_t N = kOp == kForward ? p.R : p.C;
+    const int64_t m = kOp == kDw ? p.E * ((p.R + kM - 1) / kM) : p.T / kM + std::min<int64_t>(p.E, p.T);
+    return m * ((N + kN - 1) / kN);
+}
+
+template <int kOp, class S>
 int launch(const char *who, ExpertParams p, int32_t out_type, bool add, hipStream_t st) {
-    const int64_t N = kOp == kForward ? p.R : p.C, n_tiles = (N + BN - 1) / BN;
-    const int64_t m_tiles = kOp == kDw ? p.E * ((p.R + BM - 1) / BM) : p.T / BM + std::min<int64_t>(p.E, p.T);
-    const int64_t tiles = m_tiles * n_tiles;
-    if (tiles == 0) return SFT_OK;
-    // runs of a whole round of workgroups (one or two on each of an XCD's 32
-    // CUs), fewer where the launch has less than a round
-    const int64_t round = 32 * (8 / (WM * WN));
-    p.chunk = static_cast<int32_t>(std::min<int64_t>(round, (tiles + 7) / 8));
-    const int64_t run = 8 * int64_t(p.chunk), groups = (tiles + run - 1) / run * run;
+    p.cus = sft::num_cus();
+    const int64_t units = tiles_of<kOp>(p, S::kM, S::kN) + (kOp != kDw && S::kPerCu == 1 ? p.cus / 2 : 0);
+    // runs of a whole round of workgroups (kPerCu on each of an XCD's 32 CUs),
+    // fewer where the launch has less than a round
+    p.chunk = static_cast<int32_t>(std::min<int64_t>(32 * S::kPerCu, (units + 7) / 8));
+    const int64_t run = 8 * int64_t(p.chunk), groups = (units + run - 1) / run * run;
     SFT_CHECK(groups < (int64_t(1) << 31), SFT_ENOTSUP, "%s: 2^31 output tiles or more", who);
-    const dim3 grid(static_cast<uint32_t>(groups)), block(WM * WN * 64);
+    const dim3 grid(static_cast<uint32_t>(groups)), block(kThreads);
     if (out_type == SFT_BF16)
-        hipLaunchKernelGGL((k_expert<kOp, BM, BN, WM, WN, uint16_t, false>), grid, block, 0, st, p);
+        hipLaunchKernelGGL((k_expert<kOp, S, uint16_t, false>), grid, block, 0, st, p);
     else if (!add)
-        hipLaunchKernelGGL((k_expert<kOp, BM, BN, WM, WN, float, false>), grid, block, 0, st, p);
+        hipLaunchKernelGGL((k_expert<kOp, S, float, false>), grid, block, 0, st, p);
     else if constexpr (kOp == kDw)
-        hipLaunchKernelGGL((k_expert<kOp, BM, BN, WM, WN, float, true>), grid, block, 0, st, p);
+        hipLaunchKernelGGL((k_expert<kOp, S, float, true>), grid, block, 0, st, p);
     const hipError_t e = hipGetLastError();
     SFT_CHECK(e == hipSuccess, SFT_EHIP, "%s: launch failed: %s", who, hipGetErrorString(e));
     return SFT_OK;
 }
 
+// The shape of a product's tiles, by how much there is to fill the GPU with.
+// Times in us on one MI355X, experts x R x C at T tokens, groups uneven:
+//   256 x 256, one workgroup a CU: least traffic between L2 and LDS.
+//     Forward, stages of 64 (whole cache lines of k): 8 x 11008 x 4096 at T =
+//     4096 / 16384: 382 / 1309, 128 x 192 413 / 1408, 128 x 128 438 / 1520.
+//     Input gradient, stages of 32, four of them: 103 / 468 / 1306 at 16 /
+//     4096 / 16384, 128 x 192 171 / 479 / 1495; its weight rows are long
+//     runs, so it also streams them best for few tokens.
+//   128 x 192, two workgroups a CU, one stores while the other multiplies:
+//     shorter sums or groups (64 x 1376 x 4096 at 16384, forward 275, 256 x
+//     256 299; input gradient 265, 256 x 256 272, at 4096 143 and 162)
+//   128 x 128: forward of groups about that long (8 x 11008 x 4096 at 1024:
+//     177, 128 x 192 207, 256 x 256 202)
+//   128 x 256, stages of 32: the weight gradient, whose operands are both
+//     read in long rows (8 x 11008 x 4096 at 64 / 4096 / 16384: 259 / 599 /
+//     1412; 128 x 192 287 / 632 / 1553, 256 x 256 449 / 639 / 1409)
+//   64 x 128 and 64 x 64: few tiles (16 x 1024 x 1024 forward at 4096: 64 x
+//     128 20.2, 128 x 192 26.1, 64 x 64 26.8; at 1024: 13.9, 17.8, 12.0)
+//   64 x 64 with four stages, forward: weights streamed for a few tokens (64 x
+//     1376 x 4096 at 8 tokens: 20, every other shape 34 to 62)
 template <int kOp>
 int product(const char *who, const ExpertParams &p, int32_t out_type, bool add, void *stream) {
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    return launch<kOp, 256, 256, 2, 4>(who, p, out_type, add, st);
+    if constexpr (kOp == kDw) {
+        if (tiles_of<kOp>(p, 128, 256) >= 256)
+            return launch<kOp, Shape<128, 256, 32, 3>>(who, p, out_type, add, st);
+        if (tiles_of<kOp>(p, 128, 128) >= 256)
+            return launch<kOp, Shape<128, 128, 64, 2>>(who, p, out_type, add, st);
+    } else {
+        const int64_t rows = p.T / p.E;      // of an expert on average
+        if constexpr (kOp == kForward) {
+            if (rows >= 512 && tiles_of<kOp>(p, 256, 256) >= 1024)
+                return launch<kOp, Shape<256, 256, 64, 2>>(who, p, out_type, add, st);
+            if (rows >= 48 && rows <= 192 && tiles_of<kOp>(p, 128, 128) >= 512)
+                return launch<kOp, Shape<128, 128, 64, 2>>(who, p, out_type, add, st);
+        } else {
+            if (p.R >= 4096 && tiles_of<kOp>(p, 256, 256) >= 128)
+                return launch<kOp, Shape<256, 256, 32, 4>>(who, p, out_type, add, st);
+        }
+        if (tiles_of<kOp>(p, 128, 192) >= 320 && (kOp == kDx || rows > 4))
+            return launch<kOp, Shape<128, 192, 64, 2>>(who, p, out_type, add, st);
+        if (tiles_of<kOp>(p, 64, 128) >= 256 && rows >= 128)
+            return launch<kOp, Shape<64, 128, 64, 2>>(who, p, out_type, add, st);
+    }
+    return launch<kOp, Shape<64, 64, 64, 4>>(who, p, out_type, add, st);
 }
 
 }  // namespace
@@ -411,7 +586,7 @@ int sft_expert_forward(int64_t E, int64_t T, int64_t R, int64_t C, const int32_t
                        out_type))
         return rc;
     if (E == 0 || T == 0 || R == 0) return SFT_OK;
-    return product<kForward>("sft_expert_forward", ExpertParams{X, W, Y, first, T, R, C, int32_t(E), 0}, out_type,
+    return product<kForward>("sft_expert_forward", ExpertParams{X, W, Y, first, T, R, C, int32_t(E), 0, 0}, out_type,
                              false, stream);
 }
 
@@ -421,7 +596,7 @@ int sft_expert_dx(int64_t E, int64_t T, int64_t R, int64_t C, const int32_t *fir
     if (int rc = check("sft_expert_dx", E, T, R, C, first, dY, T && R, W, E && R && C, dX, E && T && C, out_type))
         return rc;
     if (E == 0 || T == 0 || C == 0) return SFT_OK;
-    return product<kDx>("sft_expert_dx", ExpertParams{dY, W, dX, first, T, R, C, int32_t(E), 0}, out_type, false,
+    return product<kDx>("sft_expert_dx", ExpertParams{dY, W, dX, first, T, R, C, int32_t(E), 0, 0}, out_type, false,
                         stream);
 }
 
@@ -432,7 +607,7 @@ int sft_expert_dw(int64_t E, int64_t T, int64_t R, int64_t C, const int32_t *fir
         return rc;
     SFT_CHECK(!accumulate || out_type == SFT_F32, SFT_EINVAL, "sft_expert_dw: only fp32 gradients accumulate");
     if (E == 0 || R == 0 || C == 0) return SFT_OK;
-    return product<kDw>("sft_expert_dw", ExpertParams{dY, X, dW, first, T, R, C, int32_t(E), 0}, out_type,
+    return product<kDw>("sft_expert_dw", ExpertParams{dY, X, dW, first, T, R, C, int32_t(E), 0, 0}, out_type,
                         accumulate != 0, stream);
 }
 

@@ -105,6 +105,25 @@ def test_integer_inputs_are_exact(gpu_lib, op):
     _run(op, [9, 16, 1, 2], 328, 392, F32, integer=True)
 
 
+@pytest.mark.parametrize("integer", [False, True])
+@pytest.mark.parametrize("op,counts,R,C", [
+    ("forward", [8192 - 3, 70], 8000, 72), ("forward", [7700, 0, 530], 8192, 40),        # 256 x 256
+    ("dx", [8192 - 3, 70], 4104, 1032), ("dx", [7700, 0, 530], 4096, 1024), ("dx", [3, 1, 0] * 11, 4160, 1288),
+    ("forward", [90, 200, 0, 129] * 10, 1160, 72),                                             # 128 x 128
+    ("forward", [5000, 61, 131, 3000], 2056, 136), ("dx", [5000, 61, 131, 3000], 136, 2056),   # 128 x 192
+    ("dx", [1, 0, 2, 0, 1] * 12, 72, 1160), ("dx", [200, 130] * 8, 200, 584),
+    ("forward", [2000, 129, 65], 1032, 72), ("dx", [2000, 129, 65], 72, 1032),                   # 64 x 128
+    ("forward", [2, 0, 1, 70], 520, 328), ("dx", [2, 0, 1, 70], 328, 520),                     # 64 x 64
+    ("dw", [300, 0, 65, 1], 1096, 2056), ("dw", [33, 31, 97, 0], 1096, 1032), ("dw", [70, 0, 129], 328, 264),
+])
+def test_every_shape_of_tiles(gpu_lib, op, counts, R, C, integer):
+    # sizes that take each of the kernels' tiles, with rows and columns that end inside them; the last launch round of
+    # the 256 x 256 tiles is cut in halves in one of the two cases
+    _run(op, counts, R, C, F32, start=1, behind=2, integer=integer)
+    if not integer:
+        _run(op, counts, R, C, BF16)
+
+
 @pytest.mark.parametrize("op", OPS)
 @pytest.mark.parametrize("E", [1, 63, 64, 65, 200])
 def test_numbers_of_experts(gpu_lib, op, E):
