@@ -945,13 +945,25 @@ def _type(t, what) -> int:
     raise TypeError(f"{what}: expected float32 or bfloat16, got {t.dtype}")
 
 
-def _one_device(tensors) -> None:
-    """The kernels run on the current device: every tensor has to be there."""
+def _here(t, dtype=None):
+    """Device pointer of a contiguous tensor on the current GPU (None -> NULL)."""
     import torch
-    here = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != here:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{here}")
+    if t is not None and t.get_device() != torch.cuda.current_device() and t.is_cuda:
+        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return _dev(t, dtype)
+
+
+def _raw_stream(device: int) -> int:
+    """Torch's current stream of a device as a hipStream_t, without the Python
+    stream object (which takes longer to make than a short kernel to run)."""
+    global _raw
+    if _raw is None:
+        import torch
+        _raw = getattr(torch._C, "_cuda_getCurrentRawStream", lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw(device)
+
+
+_raw = None
 
 
 class PreparedHere(Prepared):
@@ -965,16 +977,17 @@ class PreparedHere(Prepared):
 
     def __call__(self, stream=None) -> None:
         import torch
-        if torch.cuda.current_device() != self._device:
-            raise ValueError(f"prepared on cuda:{self._device}, called with cuda:{torch.cuda.current_device()} current")
-        super().__call__(stream)
+        here = torch.cuda.current_device()
+        if here != self._device:
+            raise ValueError(f"prepared on cuda:{self._device}, called with cuda:{here} current")
+        _check(self._fn(*self._args, _raw_stream(here) if stream is None else _stream(stream)))
 
 
 def _scalar(t, dtype, what):
     """Device pointer of a tensor's single value (None -> NULL)."""
     if t is not None and t.numel() != 1:
         raise ValueError(f"{what}: {t.numel()} elements, expected 1")
-    return _dev(t, dtype)
+    return _here(t, dtype)
 
 
 def prepare_expert_forward(first, X, W, Y) -> PreparedHere:
@@ -986,8 +999,7 @@ def prepare_expert_forward(first, X, W, Y) -> PreparedHere:
     _shape(X, (None, Cc), "X")
     T = X.shape[0]
     _shape(Y, (T, R), "Y")
-    _one_device((first, X, W, Y))
-    args = (E, T, R, Cc, _dev(first, torch.int32), _dev(X, torch.bfloat16), _dev(W, torch.bfloat16), _dev(Y),
+    args = (E, T, R, Cc, _here(first, torch.int32), _here(X, torch.bfloat16), _here(W, torch.bfloat16), _here(Y),
             _type(Y, "Y"))
     return PreparedHere(lib().sft_expert_forward, args, (first, X, W, Y))
 
@@ -1009,8 +1021,7 @@ def prepare_expert_dx(first, dY, W, dX) -> PreparedHere:
     _shape(dY, (None, R), "dY")
     T = dY.shape[0]
     _shape(dX, (T, Cc), "dX")
-    _one_device((first, dY, W, dX))
-    args = (E, T, R, Cc, _dev(first, torch.int32), _dev(dY, torch.bfloat16), _dev(W, torch.bfloat16), _dev(dX),
+    args = (E, T, R, Cc, _here(first, torch.int32), _here(dY, torch.bfloat16), _here(W, torch.bfloat16), _here(dX),
             _type(dX, "dX"))
     return PreparedHere(lib().sft_expert_dx, args, (first, dY, W, dX))
 
@@ -1030,8 +1041,7 @@ def prepare_expert_dw(first, dY, X, dW, accumulate: bool = False) -> PreparedHer
     _shape(dY, (None, R), "dY")
     T = dY.shape[0]
     _shape(X, (T, Cc), "X")
-    _one_device((first, dY, X, dW))
-    args = (E, T, R, Cc, _dev(first, torch.int32), _dev(dY, torch.bfloat16), _dev(X, torch.bfloat16), _dev(dW),
+    args = (E, T, R, Cc, _here(first, torch.int32), _here(dY, torch.bfloat16), _here(X, torch.bfloat16), _here(dW),
             _type(dW, "dW"), int(bool(accumulate)))
     return PreparedHere(lib().sft_expert_dw, args, (first, dY, X, dW))
 
@@ -1045,10 +1055,7 @@ def sft_expert_dw(first, dY, X, dW, accumulate: bool = False, stream=None) -> No
 
 # ------------------------------------------------------------------ dense optimizer step
 def _grad_arr(grads):
-    arr = (CGradVec * max(len(grads), 1))(*[CGradVec(g.numel(), _dev(g), _type(g, f"gradient {i}"))
-                                            for i, g in enumerate(grads)])
-    _one_device(grads)
-    return arr
+    return (CGradVec * max(len(grads), 1))(*[CGradVec(g.numel(), _here(g), _type(g, "gradient")) for g in grads])
 
 
 def sft_grad_clip_workspace(grads) -> int:
@@ -1063,9 +1070,8 @@ def prepare_grad_clip(grads, max_norm: float, clip, norm, ws) -> PreparedHere:
     """sft_grad_clip with its arguments built once."""
     import torch
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _one_device((clip, norm, ws))
     args = (_grad_arr(grads), len(grads), float(max_norm), _scalar(clip, torch.float32, "clip"),
-            _scalar(norm, torch.float32, "norm"), _dev(ws), nbytes)
+            _scalar(norm, torch.float32, "norm"), _here(ws), nbytes)
     return PreparedHere(lib().sft_grad_clip, args, (list(grads), clip, norm, ws))
 
 
@@ -1093,15 +1099,15 @@ class AdamwVec:
     def c(self) -> CAdamwVec:
         import torch
         n = self.p.numel()
-        for t, what in ((self.grad, "grad"), (self.m, "m"), (self.v, "v"), (self.p_live, "p_live")):
+        for t in (self.grad, self.m, self.v, self.p_live):
             if t is not None and t.numel() != n:
-                raise ValueError(f"{what}: {t.numel()} elements, expected {n}")
-        state = torch.float32 if self.scale is None else torch.float8_e4m3fn
+                raise ValueError(f"a tensor of {t.numel()} elements among those of {n}")
+        state = torch.float32
         if self.scale is not None:
+            state = torch.float8_e4m3fn
             _shape(self.scale, ((n + 255) // 256, 2), "scale")
-        _one_device((self.p, self.grad, self.m, self.v, self.scale, self.p_live))
-        return CAdamwVec(n, _dev(self.p), _dev(self.grad), _dev(self.m, state), _dev(self.v, state),
-                         _dev(self.scale, torch.float8_e8m0fnu), _dev(self.p_live, torch.bfloat16),
+        return CAdamwVec(n, _here(self.p), _here(self.grad), _here(self.m, state), _here(self.v, state),
+                         _here(self.scale, torch.float8_e8m0fnu), _here(self.p_live, torch.bfloat16),
                          _type(self.p, "p"), _type(self.grad, "grad"))
 
     @staticmethod
@@ -1120,7 +1126,7 @@ def prepare_adamw(vecs: Sequence[AdamwVec], step, hp: Adam, clip=None) -> Prepar
     arr = (CAdamwVec * max(len(vecs), 1))(*[v.c() for v in vecs])
     h = hp.c()
     on_dev = isinstance(step, torch.Tensor)
-    _one_device((clip, hp.bc1, hp.bc2) + ((step,) if on_dev else ()))
+    _here(hp.bc1), _here(hp.bc2)
     args = (arr, len(vecs), 0 if on_dev else int(step), _scalar(step, torch.int32, "step") if on_dev else None,
             _scalar(clip, torch.float32, "clip"), C.byref(h))
     return PreparedHere(lib().sft_adamw, args, (arr, h, list(vecs), hp, step, clip))
