@@ -98,6 +98,17 @@ __device__ __forceinline__ void place(Tile &t, int32_t i, int32_t m_tiles, int32
     t.mt = g * kGroupM + (r - t.nt * gm);
 }
 
+// Sum over the lanes up to each lane's own, without going through LDS.
+__device__ __forceinline__ int32_t running_sum(int32_t x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, true);    // within 16 lanes: from 1, 2, 4, 8 lanes below
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);   // lane 15 to the next 16, 47 to the last
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);   // lane 31 to the upper half
+    return x;
+}
+
 // The tile of this workgroup, or false where there is none: the host only
 // knows how many tiles there can be at most.  64 experts at a time, a lane
 // each: their tile counts, and the running sum whose range holds the index.
@@ -110,35 +121,27 @@ __device__ __forceinline__ bool token_tile(const ExpertParams &p, int32_t n_tile
         int32_t tiles = 0;
         for (int32_t e0 = 0; e0 < p.E; e0 += 64)
             tiles += e0 + lane < p.E ? (rows_of(p, e0 + lane).y + BM - 1) / BM : 0;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) tiles += __shfl_xor(tiles, d);
-        v = tile_of_unit(p, u, uniform(tiles) * n_tiles, t.half);
+        v = tile_of_unit(p, u, __builtin_amdgcn_readlane(running_sum(tiles), 63) * n_tiles, t.half);
     }
     int32_t before = 0;
     for (int32_t e0 = 0; e0 < p.E; e0 += 64) {
         const int32_t e = e0 + lane;
         const int2 r = e < p.E ? rows_of(p, e) : int2{0, 0};
         const int32_t m_tiles = (r.y + BM - 1) / BM;
-        int32_t end = m_tiles;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int32_t o = __shfl_up(end, d);
-            end += lane >= d ? o : 0;
-        }
-        end = before + end * n_tiles;
+        const int32_t end = before + running_sum(m_tiles) * n_tiles;
         const uint64_t past = __ballot(v < end);
         if (past) {
-            const int at = __builtin_ctzll(past);
+            const int at = uniform(__builtin_ctzll(past));
             t.e = e0 + at;
-            t.lo = uniform(__shfl(r.x, at));
-            t.n = uniform(__shfl(r.y, at));
-            const int32_t mt = uniform(__shfl(m_tiles, at));
-            const int32_t i = v - (uniform(__shfl(end, at)) - mt * n_tiles);
+            t.lo = __builtin_amdgcn_readlane(r.x, at);
+            t.n = __builtin_amdgcn_readlane(r.y, at);
+            const int32_t mt = __builtin_amdgcn_readlane(m_tiles, at);
+            const int32_t i = v - (__builtin_amdgcn_readlane(end, at) - mt * n_tiles);
             if (i < 0 || i >= mt * n_tiles) return false;   // first[] does not ascend and the sums ran over
             place(t, i, mt, n_tiles);
             return true;
         }
-        before = uniform(__shfl(end, 63));
+        before = __builtin_amdgcn_readlane(end, 63);
     }
     return false;
 }
