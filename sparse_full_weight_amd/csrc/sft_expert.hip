@@ -82,7 +82,8 @@ __device__ __forceinline__ int32_t unit_index(const ExpertParams &p) {
 
 // Unit u of a launch of `tiles` tiles: whole tiles, and where the last round
 // of workgroups would fill half of the CUs or less, that round's tiles as two
-// halves along n.
+// halves along n (forward of 8 x 11008 x 4096 at 8192 tokens, 6.05 rounds: 692
+// us, with whole tiles to the end 705).
 __device__ __forceinline__ int32_t tile_of_unit(const ExpertParams &p, int32_t u, int32_t tiles, int32_t &half) {
     const int32_t last = tiles % p.cus, whole = tiles - (2 * last <= p.cus ? last : 0);
     half = u < whole ? -1 : (u - whole) & 1;
@@ -150,6 +151,7 @@ __device__ __forceinline__ bool token_tile(const ExpertParams &p, int32_t n_tile
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
 typedef __attribute__((address_space(3))) short4v lds_short4v;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, lds_u8 *lds) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)(lds), 16, voff, 0, 0, 0);
@@ -282,6 +284,14 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(a), static_cast<__bf16>(b)});
 }
 
+// Weight gradients are written past L2 (they are larger than every cache and
+// would push the operands out); results for the next layer are not.
+template <bool kStream, class V>
+__device__ __forceinline__ void put(V *p, V v) {
+    if constexpr (kStream) __builtin_nontemporal_store(v, p);
+    else *p = v;
+}
+
 constexpr int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
 // A kernel's tiles: kM x kN, by stages of kBK along k, kStages of them in LDS;
@@ -402,41 +412,67 @@ __device__ __forceinline__ void multiply_part(const ExpertParams &p, const Tile 
         for (int32_t kt = 0; kt < KT; kt += kStages)
             each([&](auto s) __attribute__((always_inline)) { use(s, kt + decltype(s)::value); });
     }
-    SFT_WAIT_VMCNT(0);   // no copy may land in LDS that is another workgroup's by then
+    // Behind this every copy has landed and every wave has read its last
+    // stage: LDS is free for the results.
+    SFT_WAIT_VMCNT(0);
+    __builtin_amdgcn_s_barrier();
 
     // Lane l holds, for row l % 32 of block (i, j), the columns
     // 8*(r/4) + 4*(l/32) + r%4 of register r: four neighbours a register quad.
-    // For bf16 the halves of the wave trade quads, after which a lane holds
-    // eight neighbours: 16-byte stores.
+    // A wave turns 32 rows of 128 bytes (one block of fp32, two of bf16, whose
+    // halves of the wave first trade quads for eight neighbours a lane) at a
+    // time through its own 4 KB of LDS, and stores whole cache lines: 16-byte
+    // group c of row r sits in slot c ^ (r/2 % 8), free of bank conflicts both
+    // ways.  Weight gradient of 8 x 11008 x 4096 at 8192 tokens, fp32: stored
+    // straight from the registers, 32 bytes a row, 871 us; so 834; and past
+    // L2 803 (64 x 1376 x 4096 at 4099 tokens, bf16: 226, 211, 158).
+    constexpr bool kF32 = std::is_same<Out, float>::value;
+    constexpr int kJ = kF32 ? 1 : 2, kLane = kF32 ? 4 : 8;    // blocks at a time, values in 16 bytes
+    static_assert(SA >= 8192 && SB >= 8192, "4 KB for each of 4 waves");
+    lds_u8 *turn = (wave & 2 ? stage<SB, 1, 0>() : stage<SA, 0, 0>()) + 4096 * (wave & 1);
     Out *out = static_cast<Out *>(p.out) +
                (kOp == kDw ? static_cast<int64_t>(t.e) * p.R * p.C : static_cast<int64_t>(t.lo) * N);
-    const int half = lane >> 5;
+    const int half = lane >> 5, row = lane & 31;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-        const int64_t m = m0 + am + 32 * i + (lane & 31);
-        Out *row = out + m * N;
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            const int64_t n = n0 + bn + 32 * j;
-            const floatx16 &x = acc[i][j];
-            if constexpr (std::is_same<Out, float>::value) {
+        for (int j = 0; j < FN; j += kJ) {
+            const int groups = (FN - j < kJ ? FN - j : kJ) * (32 / kLane);     // of 16 bytes in a row: 8, or 4
+            auto slot = [&](int r, int c) __attribute__((always_inline)) {
+                return (lds_u32x4 *)(turn + (128 * r + 16 * (c ^ (r >> 1 & 7))));
+            };
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    f32x4 *o = reinterpret_cast<f32x4 *>(row + n + 8 * q + 4 * half);
-                    f32x4 v{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
-                    if (m < M && n + 8 * q + 4 * half < N) *o = kAdd ? *o + v : v;
+            for (int b = j; b < j + kJ && b < FN; ++b) {
+                const floatx16 &x = acc[i][b];
+                if constexpr (kF32) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        *slot(row, 2 * q + half) = __builtin_bit_cast(
+                            u32x4, f32x4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]});
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; q += 2) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) w[c] = pack2(x[4 * q + 2 * c], x[4 * q + 2 * c + 1]);
+                        const auto lo = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+                        const auto hi = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+                        *slot(row, 4 * (b - j) + q + half) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+                    }
                 }
-            } else {
+            }
+            const int rows = 64 / groups, c = lane % groups;                   // of one store
+            const int64_t n = n0 + bn + 32 * j + kLane * c;
 #pragma unroll
-                for (int q = 0; q < 4; q += 2) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) w[c] = pack2(x[4 * q + 2 * c], x[4 * q + 2 * c + 1]);
-                    const auto lo = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-                    const auto hi = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-                    const int64_t c = n + 8 * (q + half);
-                    if (m < M && c < N)
-                        *reinterpret_cast<u32x4 *>(row + c) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+            for (int r0 = 0; r0 < 32; r0 += rows) {
+                const int r = r0 + lane / groups;
+                const int64_t m = m0 + am + 32 * i + r;
+                u32x4 v = *slot(r, c);
+                if (m < M && n < N) {
+                    u32x4 *o = reinterpret_cast<u32x4 *>(out + m * N + n);
+                    if constexpr (kAdd)
+                        v = __builtin_bit_cast(u32x4, __builtin_bit_cast(f32x4, *o) + __builtin_bit_cast(f32x4, v));
+                    put<kOp == kDw>(o, v);
                 }
             }
         }
