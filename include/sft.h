@@ -879,7 +879,10 @@ typedef struct sft_adamw_vec {
  *   g = clip * grad,  m = beta1*m + (1-beta1)*g,  v = beta2*v + (1-beta2)*g^2
  *   p = p*(1 - lr*weight_decay) - (k1*m) / (sqrt(v)*k2 + eps)
  * with k1 = lr/bc1[t], k2 = 1/sqrt(bc2[t]) (entry min(t, t_max) of the
- * tables), in fp32 with every operation rounded on its own.
+ * tables), in fp32 with every operation rounded on its own (with 8-bit states
+ * the quotient is a product with a reciprocal that is off by at most one unit
+ * in the last place).  With eps = 0 a parameter whose gradients were all zero
+ * becomes NaN, as the formula has it.
  *   step      t, where step_dev is NULL
  *   step_dev  device int32, 4-byte aligned: t is read when the step runs, so
  *             that a captured call can be replayed for the next steps (the
@@ -888,7 +891,8 @@ typedef struct sft_adamw_vec {
  *   clip      device float, 4-byte aligned, or NULL for 1.  Where it is not a
  *             positive finite number the step is left out: no tensor changes.
  * Arrays that the step writes must not overlap.
- * Errors: SFT_EINVAL (null pointers, bad sizes, types, betas, eps or step,
+ * Errors: SFT_EINVAL (null pointers, bad sizes, types, betas, eps (negative or
+ * subnormal) or step,
  * overlapping arrays), SFT_EALIGN, SFT_ENOTSUP (2^42 values in a tensor, or
  * 2^31 chunks in a launch), SFT_EHIP; a failed argument check launches
  * nothing.

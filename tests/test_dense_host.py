@@ -45,6 +45,7 @@ def _hp(**kw):
     (dict(vecs=[_vec()], hp=_hp(beta1=1.0)), _lib.SFT_EINVAL),
     (dict(vecs=[_vec()], hp=_hp(beta2=float("nan"))), _lib.SFT_EINVAL),
     (dict(vecs=[_vec()], hp=_hp(eps=-1.0)), _lib.SFT_EINVAL),
+    (dict(vecs=[_vec()], hp=_hp(eps=1e-40)), _lib.SFT_EINVAL),
     (dict(vecs=[_vec()], hp=_hp(t_max=0)), _lib.SFT_EINVAL),
     (dict(vecs=[_vec()], hp=_hp(bc1=None)), _lib.SFT_EINVAL),
 ])

@@ -57,8 +57,9 @@ def _formula(p, g, m, v, step, hp, clip=1.0):
     ev = 5 * U * v1                                      # clip twice, square, products, sum: all terms positive
     den = (v1 / bc2).sqrt() + eps
     u = lr / bc1 * m1 / den
-    # k1, its product, the division: 3; k2 (root, quotient), its product, the sum and the root of v: 5.5 + 2.5 of v
-    eu = 11 * U * u.abs() + lr / bc1 / den * em
+    # k1 and its product: 2; k2 (root, quotient), its product, the sum, the root of v and half of v's 5: 7.5; the
+    # quotient 1, or as a product with a reciprocal off by one unit in the last place (2 U) 3
+    eu = 12.5 * U * u.abs() + lr / bc1 / den * em
     p1 = p * (1 - lr * decay) - u
     ep = 3 * U * p.abs() + eu + U * p1.abs()           # lr*decay, 1 - it, the product; the difference
     return (p1, m1, v1), (1.01 * ep + 1e-45, 1.01 * em + 1e-45, 1.01 * ev + 1e-45)
