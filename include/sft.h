@@ -771,7 +771,9 @@ enum { SFT_F32 = 0, SFT_BF16 = 1 };
  *   first  device int32 [E + 1], ascending, 4-byte aligned.  It is read on
  *          the device only, so that a router's counts never come back to the
  *          host; values are clipped into [0, T], and a group that would end
- *          before it starts is empty.  Experts may have no rows; rows before
+ *          before it starts is empty (the results of groups that overlap, in
+ *          a list that does not ascend, are not defined, but stay inside the
+ *          arrays).  Experts may have no rows; rows before
  *          first[0] and from first[E] on belong to none, and what a call
  *          would write there stays as it was.
  *   X bf16 [T x C], W bf16 [E x R x C], dY bf16 [T x R]
@@ -779,7 +781,7 @@ enum { SFT_F32 = 0, SFT_BF16 = 1 };
  * Sums are in fp32 on the matrix cores, in an order that depends only on the
  * sizes: results are deterministic, and a token's do not depend on the other
  * tokens of its group.  No workspace, nothing allocated.
- * Limits: R and C multiples of 8 and at most 2^20, T < 2^31, E <= 65536,
+ * Limits: R and C multiples of 8 and at most 2^20, T < 2^30, E <= 65536,
  * fewer than 2^31 output tiles.
  * Errors: SFT_EINVAL (null pointers, negative sizes, bad out_type),
  * SFT_ESHAPE (R or C), SFT_EALIGN, SFT_ENOTSUP (beyond the limits), SFT_EHIP.

@@ -149,8 +149,14 @@ __device__ __forceinline__ void norm_chunk(const typename G::type *g, int64_t n,
             for (int i = 0; i < kStep; ++i) sum = __builtin_fma(static_cast<double>(x[i]), static_cast<double>(x[i]), sum);
         }
     } else {
-        const int end = static_cast<int>(n < kNormChunk ? n : kNormChunk);
-        for (int i = threadIdx.x; i < end; i += kThreads) {
+        const int end = static_cast<int>(n < kNormChunk ? n : kNormChunk), runs = vec ? end / kStep * kStep : 0;
+        for (int i = threadIdx.x * kStep; i < runs; i += kThreads * kStep) {
+            float x[kStep];
+            G::load(g + i, x);
+#pragma unroll
+            for (int j = 0; j < kStep; ++j) sum = __builtin_fma(static_cast<double>(x[j]), static_cast<double>(x[j]), sum);
+        }
+        for (int i = runs + threadIdx.x; i < end; i += kThreads) {
             const double x = G::one(g + i);
             sum = __builtin_fma(x, x, sum);
         }
@@ -680,17 +686,22 @@ int adamw(const sft_adamw_vec *vecs, int32_t n_vecs, int32_t step, const int32_t
     h.step = step;
     h.t_max = hp->t_max;
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    Launch32 l32;
-    Launch8 l8;
-    l32.a.h = h;
-    l8.a.h = h;
+    const auto kind_of = [](const sft_adamw_vec &v) { return v.p_type | v.g_type << 1 | int(v.scale != nullptr) << 2; };
+    uint32_t kinds = 0;
+    for (int32_t i = 0; i < n_vecs; ++i)
+        if (vecs[i].n) kinds |= 1u << kind_of(vecs[i]);
     // one launch for the tensors of each kind
     for (int kind = 0; kind < 8; ++kind) {
+        if (!(kinds >> kind & 1u)) continue;
         const int p_type = kind & 1, g_type = kind >> 1 & 1;
         const bool held = kind >> 2;
+        Launch32 l32;
+        Launch8 l8;
+        l32.a.h = h;
+        l8.a.h = h;
         for (int32_t i = 0; i < n_vecs; ++i) {
             const sft_adamw_vec &v = vecs[i];
-            if (v.n == 0 || v.p_type != p_type || v.g_type != g_type || (v.scale != nullptr) != held) continue;
+            if (v.n == 0 || kind_of(v) != kind) continue;
             const bool vec = sft::aligned16(v.p) && sft::aligned16(v.grad) && sft::aligned16(v.m) &&
                              sft::aligned16(v.v) && sft::aligned16(v.p_live);
             if (held) {

@@ -528,8 +528,8 @@ int check(const char *who, int64_t E, int64_t T, int64_t R, int64_t C, const voi
     SFT_CHECK(E >= 0 && T >= 0 && R >= 0 && C >= 0, SFT_EINVAL, "%s: a size is negative", who);
     SFT_CHECK(out_type == SFT_F32 || out_type == SFT_BF16, SFT_EINVAL, "%s: bad out_type %d", who, out_type);
     SFT_CHECK(R % 8 == 0 && C % 8 == 0, SFT_ESHAPE, "%s: R and C must be multiples of 8", who);
-    SFT_CHECK(T < (int64_t(1) << 31) && E <= 65536 && R <= (int64_t(1) << 20) && C <= (int64_t(1) << 20), SFT_ENOTSUP,
-              "%s: T >= 2^31, E > 65536, or R or C > 2^20", who);
+    SFT_CHECK(T < (int64_t(1) << 30) && E <= 65536 && R <= (int64_t(1) << 20) && C <= (int64_t(1) << 20), SFT_ENOTSUP,
+              "%s: T >= 2^30, E > 65536, or R or C > 2^20", who);
     if (!out_values) return SFT_OK;
     SFT_CHECK(first && out && (a || !a_values) && (b || !b_values), SFT_EINVAL, "%s: null pointer", who);
     SFT_CHECK(sft::aligned16(a) && sft::aligned16(b) && sft::aligned16(out), SFT_EALIGN,

@@ -23,12 +23,12 @@ def _call(op, **kw):
     (dict(E=-1), _lib.SFT_EINVAL), (dict(T=-1), _lib.SFT_EINVAL), (dict(R=-8), _lib.SFT_EINVAL),
     (dict(C=-8), _lib.SFT_EINVAL), (dict(type=2), _lib.SFT_EINVAL), (dict(type=-1), _lib.SFT_EINVAL),
     (dict(R=12), _lib.SFT_ESHAPE), (dict(C=4), _lib.SFT_ESHAPE),
-    (dict(T=1 << 31), _lib.SFT_ENOTSUP), (dict(E=65537), _lib.SFT_ENOTSUP),
+    (dict(T=1 << 30), _lib.SFT_ENOTSUP), (dict(E=65537), _lib.SFT_ENOTSUP),
     (dict(R=(1 << 20) + 8), _lib.SFT_ENOTSUP), (dict(C=(1 << 20) + 8), _lib.SFT_ENOTSUP),
     (dict(first=None), _lib.SFT_EINVAL), (dict(a=None), _lib.SFT_EINVAL), (dict(b=None), _lib.SFT_EINVAL),
     (dict(out=None), _lib.SFT_EINVAL), (dict(first=BASE + 2), _lib.SFT_EALIGN), (dict(a=BASE + 8), _lib.SFT_EALIGN),
     (dict(b=BASE + 2), _lib.SFT_EALIGN), (dict(out=BASE + 4), _lib.SFT_EALIGN),
-    (dict(E=65536, T=(1 << 31) - 1, R=1 << 20, C=1 << 20), _lib.SFT_ENOTSUP),     # 2^31 tiles
+    (dict(E=65536, T=(1 << 30) - 1, R=1 << 20, C=1 << 20), _lib.SFT_ENOTSUP),     # 2^31 tiles
 ])
 def test_refuses(op, kw, code):
     assert _call(op, **kw) == code

@@ -339,6 +339,39 @@ def test_training_steps_of_an_expert_layer(gpu_lib, held):
         assert torch.equal(W, p.bfloat16())
 
 
+def test_two_streams_at_once(gpu_lib):
+    # the calls share nothing: layers stepped on two streams at a time end as they do one after the other
+    def layer(seed):
+        counts, R, C = [300, 0, 129, 71], 264, 392
+        T = sum(counts)
+        first, W = _first(counts), _normal((4, R, C), 0.1, seed)
+        X, dY = _normal((T, C), 1.0, seed + 1), _normal((T, R), 0.1, seed + 2)
+        Y, dX = torch.zeros((T, R), dtype=BF16, device="cuda"), torch.zeros((T, C), dtype=BF16, device="cuda")
+        dW, p = torch.zeros((4, R, C), device="cuda"), W.float()
+        vec = _lib.AdamwVec.alloc8(p, dW, W)
+        clip = torch.zeros(1, device="cuda")
+        ws = torch.empty(_lib.sft_grad_clip_workspace([dW]), dtype=torch.uint8, device="cuda")
+        hp = adam_dev(lr=1e-2)
+        return (Y, dX, p, W), [_lib.prepare_expert_forward(first, X, W, Y), _lib.prepare_expert_dx(first, dY, W, dX),
+                               _lib.prepare_expert_dw(first, dY, X, dW), _lib.prepare_grad_clip([dW], 0.1, clip, None, ws),
+                               _lib.prepare_adamw([vec], 3, hp, clip)]
+
+    alone, together = [layer(s) for s in (1, 50)], [layer(s) for s in (1, 50)]
+    streams = [torch.cuda.Stream() for _ in alone]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for _, calls in alone:
+            for c in calls:
+                c()
+        torch.cuda.synchronize()
+        for i in range(5):
+            for s, (_, calls) in zip(streams, together):
+                calls[i](s)
+    torch.cuda.synchronize()
+    for (a, _), (b, _) in zip(alone, together):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 @pytest.mark.parametrize("op", ["forward", "dw"])
 def test_gradients_agree_with_differences(gpu_lib, op):
     # <dY, Y> is linear in X and in W: a change of one of them changes it by exactly <gradient, change>
