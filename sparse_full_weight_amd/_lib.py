@@ -945,11 +945,16 @@ def _type(t, what) -> int:
     raise TypeError(f"{what}: expected float32 or bfloat16, got {t.dtype}")
 
 
-def _here(t, dtype=None):
+def _here(t, dtype=None, device=None):
     """Device pointer of a contiguous tensor on the current GPU (None -> NULL)."""
+    if t is None:
+        return None
     import torch
-    if t is not None and t.get_device() != torch.cuda.current_device() and t.is_cuda:
-        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    if device is None:
+        device = torch.cuda.current_device()
+    at = t.get_device()
+    if at != device and at >= 0:
+        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{device}")
     return _dev(t, dtype)
 
 
@@ -1096,7 +1101,7 @@ class AdamwVec:
     scale: "object" = None
     p_live: "object" = None     # bfloat16 copy of the new parameters, or None
 
-    def c(self) -> CAdamwVec:
+    def c(self, device=None) -> CAdamwVec:
         import torch
         n = self.p.numel()
         for t in (self.grad, self.m, self.v, self.p_live):
@@ -1106,9 +1111,10 @@ class AdamwVec:
         if self.scale is not None:
             state = torch.float8_e4m3fn
             _shape(self.scale, ((n + 255) // 256, 2), "scale")
-        return CAdamwVec(n, _here(self.p), _here(self.grad), _here(self.m, state), _here(self.v, state),
-                         _here(self.scale, torch.float8_e8m0fnu), _here(self.p_live, torch.bfloat16),
-                         _type(self.p, "p"), _type(self.grad, "grad"))
+        return CAdamwVec(n, _here(self.p, None, device), _here(self.grad, None, device),
+                         _here(self.m, state, device), _here(self.v, state, device),
+                         _here(self.scale, torch.float8_e8m0fnu, device),
+                         _here(self.p_live, torch.bfloat16, device), _type(self.p, "p"), _type(self.grad, "grad"))
 
     @staticmethod
     def alloc8(p, grad, p_live=None) -> "AdamwVec":
@@ -1123,7 +1129,8 @@ def prepare_adamw(vecs: Sequence[AdamwVec], step, hp: Adam, clip=None) -> Prepar
     """sft_adamw with its arguments built once; with a GPU tensor as `step`
     the same object takes every step."""
     import torch
-    arr = (CAdamwVec * max(len(vecs), 1))(*[v.c() for v in vecs])
+    device = torch.cuda.current_device()
+    arr = (CAdamwVec * max(len(vecs), 1))(*[v.c(device) for v in vecs])
     h = hp.c()
     on_dev = isinstance(step, torch.Tensor)
     _here(hp.bc1), _here(hp.bc2)

@@ -448,8 +448,8 @@ __device__ __forceinline__ void multiply_part(const ExpertParams &p, const Tile 
     // A wave turns 32 rows of 128 bytes (one block of fp32, two of bf16, whose
     // halves of the wave first trade quads for eight neighbours a lane) at a
     // time through its own 4 KB of LDS, and stores whole cache lines: 16-byte
-    // group c of row r sits in slot c ^ (r/2 % 8), free of bank conflicts both
-    // ways.  Weight gradient of 8 x 11008 x 4096 at 8192 tokens, fp32: stored
+    // group c of row r sits in slot c ^ (r % 8) ^ (r/8 % 2), so that neither 16
+    // rows of one group, nor 8 rows of two, nor a row's 8 collide on a bank.  Weight gradient of 8 x 11008 x 4096 at 8192 tokens, fp32: stored
     // straight from the registers, 32 bytes a row, 871 us; so 834; and past
     // L2 803 (64 x 1376 x 4096 at 4099 tokens, bf16: 226, 211, 158).
     constexpr bool kF32 = std::is_same<Out, float>::value;
@@ -465,7 +465,7 @@ __device__ __forceinline__ void multiply_part(const ExpertParams &p, const Tile 
         for (int j = 0; j < FN; j += kJ) {
             const int groups = (FN - j < kJ ? FN - j : kJ) * (32 / kLane);     // of 16 bytes in a row: 8, or 4
             auto slot = [&](int r, int c) __attribute__((always_inline)) {
-                return (lds_u32x4 *)(turn + (128 * r + 16 * (c ^ (r >> 1 & 7))));
+                return (lds_u32x4 *)(turn + (128 * r + 16 * (c ^ (r & 7) ^ (r >> 3 & 1))));
             };
 #pragma unroll
             for (int b = j; b < j + kJ && b < FN; ++b) {
