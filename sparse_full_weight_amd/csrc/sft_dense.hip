@@ -137,6 +137,8 @@ __device__ __forceinline__ double wave_sum(double x) {
     return x;
 }
 
+__device__ __forceinline__ double square_on(double x, double sum) { return __builtin_fma(x, x, sum); }
+
 template <class G>
 __device__ __forceinline__ void norm_chunk(const typename G::type *g, int64_t n, bool vec, double &sum) {
     constexpr int kStep = 8;
@@ -146,7 +148,7 @@ __device__ __forceinline__ void norm_chunk(const typename G::type *g, int64_t n,
             float x[kStep];
             G::load(g + (k * kThreads + threadIdx.x) * kStep, x);
 #pragma unroll
-            for (int i = 0; i < kStep; ++i) sum = __builtin_fma(static_cast<double>(x[i]), static_cast<double>(x[i]), sum);
+            for (int i = 0; i < kStep; ++i) sum = square_on(x[i], sum);
         }
     } else {
         const int end = static_cast<int>(n < kNormChunk ? n : kNormChunk), runs = vec ? end / kStep * kStep : 0;
@@ -154,7 +156,7 @@ __device__ __forceinline__ void norm_chunk(const typename G::type *g, int64_t n,
             float x[kStep];
             G::load(g + i, x);
 #pragma unroll
-            for (int j = 0; j < kStep; ++j) sum = __builtin_fma(static_cast<double>(x[j]), static_cast<double>(x[j]), sum);
+            for (int j = 0; j < kStep; ++j) sum = square_on(x[j], sum);
         }
         for (int i = runs + threadIdx.x; i < end; i += kThreads) {
             const double x = G::one(g + i);
@@ -245,6 +247,17 @@ __device__ __forceinline__ float adam_param(const AdamScalars &h, const AdamStep
     return p * h.decay - (kRcp ? num * __builtin_amdgcn_rcpf(den) : num / den);
 }
 
+// A group of elements with their moments in fp32.
+template <int N>
+__device__ __forceinline__ void adam_group(const AdamScalars &h, const AdamStep &s, float (&p)[N], const float (&g)[N],
+                                           float (&m)[N], float (&v)[N]) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        adam_moments(h, s, g[j], m[j], v[j]);
+        p[j] = adam_param<false>(h, s, p[j], m[j], __builtin_sqrtf(v[j]));
+    }
+}
+
 constexpr int kVecs32 = 74;
 constexpr int64_t kChunk32 = 2048;
 
@@ -270,9 +283,12 @@ __global__ __launch_bounds__(kThreads) void k_adamw32(const Adam32Params a) {
     const typename G::type *g = static_cast<const typename G::type *>(a.g[e]) + at;
     float *m = a.m[e] + at, *v = a.v[e] + at;
     uint16_t *live = a.live[e] ? a.live[e] + at : nullptr;
-    if ((a.n[e] & 1) && n >= kChunk32) {
-        constexpr int N = 4, K = kChunk32 / (kThreads * N);
-        float pp[K][N], gg[K][N], mm[K][N], vv[K][N];
+    constexpr int N = 4, K = kChunk32 / (kThreads * N);
+    float pp[K][N], gg[K][N], mm[K][N], vv[K][N];
+    const bool aligned = a.n[e] & 1;
+    // whole groups of N where the pointers allow it, one by one at the end and
+    // in unaligned tensors
+    if (aligned && n >= kChunk32) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int i = (k * kThreads + threadIdx.x) * N;
@@ -284,11 +300,7 @@ __global__ __launch_bounds__(kThreads) void k_adamw32(const Adam32Params a) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int i = (k * kThreads + threadIdx.x) * N;
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                adam_moments(a.h, s, gg[k][j], mm[k][j], vv[k][j]);
-                pp[k][j] = adam_param<false>(a.h, s, pp[k][j], mm[k][j], __builtin_sqrtf(vv[k][j]));
-            }
+            adam_group(a.h, s, pp[k], gg[k], mm[k], vv[k]);
             P::store(p + i, pp[k]);
             F32::store(m + i, mm[k]);
             F32::store(v + i, vv[k]);
@@ -296,15 +308,26 @@ __global__ __launch_bounds__(kThreads) void k_adamw32(const Adam32Params a) {
         }
         return;
     }
-    const int end = static_cast<int>(n < kChunk32 ? n : kChunk32);
-    for (int i = threadIdx.x; i < end; i += kThreads) {
-        float mi = m[i], vi = v[i];
-        adam_moments(a.h, s, G::one(g + i), mi, vi);
-        const float x = adam_param<false>(a.h, s, P::one(p + i), mi, __builtin_sqrtf(vi));
-        P::put(p + i, x);
-        m[i] = mi;
-        v[i] = vi;
-        if (live) BF16::put(live + i, x);
+    const int end = static_cast<int>(n < kChunk32 ? n : kChunk32), runs = aligned ? end / N * N : 0;
+    for (int i = threadIdx.x * N; i < runs; i += kThreads * N) {
+        P::load(p + i, pp[0]);
+        G::load(g + i, gg[0]);
+        F32::load(m + i, mm[0]);
+        F32::load(v + i, vv[0]);
+        adam_group(a.h, s, pp[0], gg[0], mm[0], vv[0]);
+        P::store(p + i, pp[0]);
+        F32::store(m + i, mm[0]);
+        F32::store(v + i, vv[0]);
+        if (live) BF16::store(live + i, pp[0]);
+    }
+    for (int i = runs + threadIdx.x; i < end; i += kThreads) {
+        float x[1] = {P::one(p + i)}, mi[1] = {m[i]}, vi[1] = {v[i]};
+        const float gi[1] = {G::one(g + i)};
+        adam_group(a.h, s, x, gi, mi, vi);
+        P::put(p + i, x[0]);
+        m[i] = mi[0];
+        v[i] = vi[0];
+        if (live) BF16::put(live + i, x[0]);
     }
 }
 
@@ -386,7 +409,7 @@ __global__ __launch_bounds__(kThreads) void k_adamw8(const Adam8Params a) {
     const typename G::type *g = static_cast<const typename G::type *>(a.g[e]) + at;
     uint8_t *m = a.m[e] + at, *v = a.v[e] + at, *scale = a.scale[e] + at / kBlock * 2;
     uint16_t *live = a.live[e] ? a.live[e] + at : nullptr;
-    const bool whole = (a.n[e] & 1) && n >= kChunk8;
+    const bool aligned = a.n[e] & 1, whole = aligned && n >= kChunk8;
     constexpr int N = 8, K = kChunk8 / (kThreads * N);
     float pp[K][N], gg[K][N];
     uint32_t mc[K][2], vc[K][2], sm[K], sv[K];
@@ -402,11 +425,22 @@ __global__ __launch_bounds__(kThreads) void k_adamw8(const Adam8Params a) {
             sv[k] = scale[i / kBlock * 2 + 1];
         }
     } else {
+        // a lane's group whole where it is inside, else one by one (on average
+        // half of the last chunk of every tensor: 123 tensors of 26000
+        // elements 18.1 us, one by one throughout 26.7)
+#pragma unroll
         for (int k = 0; k < K; ++k) {
             const int i = (k * kThreads + threadIdx.x) * N;
-            mc[k][0] = mc[k][1] = vc[k][0] = vc[k][1] = 0;
             sm[k] = i < n ? scale[i / kBlock * 2] : 127u;
             sv[k] = i < n ? scale[i / kBlock * 2 + 1] : 127u;
+            if (aligned && i + N <= n) {
+                const u32x2 a0 = stream_get<u32x2>(m + i), a1 = stream_get<u32x2>(v + i);
+                P::load(p + i, pp[k]);
+                G::load(g + i, gg[k]);
+                mc[k][0] = a0.x, mc[k][1] = a0.y, vc[k][0] = a1.x, vc[k][1] = a1.y;
+                continue;
+            }
+            mc[k][0] = mc[k][1] = vc[k][0] = vc[k][1] = 0;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const bool in = i + j < n;
@@ -448,7 +482,7 @@ __global__ __launch_bounds__(kThreads) void k_adamw8(const Adam8Params a) {
             vc[k][j / 4] |= code_of<false>(rr[j], shift_r, w) << (8 * (j & 3));
             w += 0xC2B2AE35u;
         }
-        if (whole) {
+        if (whole || (aligned && i + N <= n)) {
             P::store(p + i, pp[k]);
             if (live) BF16::store(live + i, pp[k]);
             stream_put(m + i, u32x2{mc[k][0], mc[k][1]});
@@ -636,7 +670,8 @@ int adamw(const sft_adamw_vec *vecs, int32_t n_vecs, int32_t step, const int32_t
     SFT_CHECK(hp->beta1 >= 0.0f && hp->beta1 < 1.0f && hp->beta2 >= 0.0f && hp->beta2 < 1.0f, SFT_EINVAL,
               "sft_adamw: beta1 or beta2 outside [0, 1)");
     // (a subnormal eps alone in the denominator would have no reciprocal)
-    SFT_CHECK(hp->eps == 0.0f || hp->eps >= FLT_MIN, SFT_EINVAL, "sft_adamw: eps is negative, subnormal or not a number");
+    SFT_CHECK(hp->eps == 0.0f || hp->eps >= FLT_MIN, SFT_EINVAL,
+              "sft_adamw: eps is negative, subnormal or not a number");
     SFT_CHECK(step_dev || step >= 1, SFT_EINVAL, "sft_adamw: step %d < 1", step);
     SFT_CHECK(aligned(step_dev, 4) && aligned(clip, 4), SFT_EALIGN, "sft_adamw: step_dev or clip not 4-byte aligned");
     std::vector<Range> written;

@@ -284,8 +284,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(a), static_cast<__bf16>(b)});
 }
 
-// Weight gradients are written past L2 (they are larger than every cache and
-// would push the operands out); results for the next layer are not.
+// kStream: past L2.
 template <bool kStream, class V>
 __device__ __forceinline__ void put(V *p, V v) {
     if constexpr (kStream) __builtin_nontemporal_store(v, p);
@@ -449,9 +448,13 @@ __device__ __forceinline__ void multiply_part(const ExpertParams &p, const Tile 
     // halves of the wave first trade quads for eight neighbours a lane) at a
     // time through its own 4 KB of LDS, and stores whole cache lines: 16-byte
     // group c of row r sits in slot c ^ (r % 8) ^ (r/8 % 2), so that neither 16
-    // rows of one group, nor 8 rows of two, nor a row's 8 collide on a bank.  Weight gradient of 8 x 11008 x 4096 at 8192 tokens, fp32: stored
-    // straight from the registers, 32 bytes a row, 871 us; so 834; and past
-    // L2 803 (64 x 1376 x 4096 at 4099 tokens, bf16: 226, 211, 158).
+    // rows of one group, nor 8 rows of two, nor a row's 8 collide on a bank.
+    // Weight gradient of 8 x 11008 x 4096 at 8192 tokens, fp32: stored straight
+    // from the registers, 32 bytes a row, 871 us; so 834; and past L2 803
+    // (64 x 1376 x 4096 at 4099 tokens, bf16: 226, 211, 158).
+    // The old values that a sum goes on from are read a block ahead where rows
+    // start on cache lines (64 x 1376 x 4096: 676 -> 530 us), else just before
+    // they are written (rows of 16416 bytes: 992 us ahead, 782 so).
     constexpr bool kF32 = std::is_same<Out, float>::value;
     constexpr int kJ = kF32 ? 1 : 2, kLane = kF32 ? 4 : 8;    // blocks at a time, values in 16 bytes
     static_assert(SA >= 8192 && SB >= 8192, "4 KB for each of 4 waves");
@@ -459,50 +462,97 @@ __device__ __forceinline__ void multiply_part(const ExpertParams &p, const Tile 
     Out *out = static_cast<Out *>(p.out) +
                (kOp == kDw ? static_cast<int64_t>(t.e) * p.R * p.C : static_cast<int64_t>(t.lo) * N);
     const int half = lane >> 5, row = lane & 31;
+    static_assert(!kAdd || kF32, "sums go on in fp32");
+    f32x4 old[2][4];
+    auto read_old = [&](int block) __attribute__((always_inline)) {
+        const int64_t n = n0 + bn + 32 * (block % FN) + 4 * (lane & 7);
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
+        for (int k = 0; k < 4; ++k) {
+            const int64_t m = m0 + am + 32 * (block / FN) + 8 * k + (lane >> 3);
+            if (m < M && n < N) old[block & 1][k] = *reinterpret_cast<const f32x4 *>(out + m * N + n);
+        }
+    };
+    auto results = [&](auto past) __attribute__((always_inline)) {
+        constexpr bool kAhead = kAdd && decltype(past)::value != 0;
+        if constexpr (kAhead) read_old(0);
 #pragma unroll
-        for (int j = 0; j < FN; j += kJ) {
-            const int groups = (FN - j < kJ ? FN - j : kJ) * (32 / kLane);     // of 16 bytes in a row: 8, or 4
-            auto slot = [&](int r, int c) __attribute__((always_inline)) {
-                return (lds_u32x4 *)(turn + (128 * r + 16 * (c ^ (r & 7) ^ (r >> 3 & 1))));
-            };
+        for (int i = 0; i < FM; ++i) {
 #pragma unroll
-            for (int b = j; b < j + kJ && b < FN; ++b) {
-                const floatx16 &x = acc[i][b];
-                if constexpr (kF32) {
+            for (int j = 0; j < FN; j += kJ) {
+                const int groups = (FN - j < kJ ? FN - j : kJ) * (32 / kLane);     // of 16 bytes in a row: 8, or 4
+                auto slot = [&](int r, int c) __attribute__((always_inline)) {
+                    return (lds_u32x4 *)(turn + (128 * r + 16 * (c ^ (r & 7) ^ (r >> 3 & 1))));
+                };
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        *slot(row, 2 * q + half) = __builtin_bit_cast(
-                            u32x4, f32x4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]});
-                } else {
+                for (int b = j; b < j + kJ && b < FN; ++b) {
+                    const floatx16 &x = acc[i][b];
+                    if constexpr (kF32) {
 #pragma unroll
-                    for (int q = 0; q < 4; q += 2) {
-                        uint32_t w[4];
+                        for (int q = 0; q < 4; ++q)
+                            *slot(row, 2 * q + half) = __builtin_bit_cast(
+                                u32x4, f32x4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]});
+                    } else {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) w[c] = pack2(x[4 * q + 2 * c], x[4 * q + 2 * c + 1]);
-                        const auto lo = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-                        const auto hi = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-                        *slot(row, 4 * (b - j) + q + half) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+                        for (int q = 0; q < 4; q += 2) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) w[c] = pack2(x[4 * q + 2 * c], x[4 * q + 2 * c + 1]);
+                            const auto lo = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+                            const auto hi = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+                            *slot(row, 4 * (b - j) + q + half) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+                        }
+                    }
+                }
+                if constexpr (kAhead) {
+                    if (i * FN + j + 1 < FM * FN) read_old(i * FN + j + 1);
+                }
+                const int rows = 64 / groups, c = lane % groups;                   // of one store
+                const int64_t n = n0 + bn + 32 * j + kLane * c;
+#pragma unroll
+                for (int r0 = 0; r0 < 32; r0 += rows) {
+                    const int r = r0 + lane / groups;
+                    const int64_t m = m0 + am + 32 * i + r;
+                    u32x4 v = *slot(r, c);
+                    if (m < M && n < N) {
+                        u32x4 *o = reinterpret_cast<u32x4 *>(out + m * N + n);
+                        if constexpr (kAdd) {
+                            f32x4 w;
+                            if constexpr (kAhead)
+                                w = old[(i * FN + j) & 1][r0 / 8];
+                            else
+                                w = *reinterpret_cast<const f32x4 *>(o);
+                            v = __builtin_bit_cast(u32x4, w + __builtin_bit_cast(f32x4, v));
+                        }
+                        put<decltype(past)::value != 0>(o, v);
                     }
                 }
             }
-            const int rows = 64 / groups, c = lane % groups;                   // of one store
-            const int64_t n = n0 + bn + 32 * j + kLane * c;
-#pragma unroll
-            for (int r0 = 0; r0 < 32; r0 += rows) {
-                const int r = r0 + lane / groups;
-                const int64_t m = m0 + am + 32 * i + r;
-                u32x4 v = *slot(r, c);
-                if (m < M && n < N) {
-                    u32x4 *o = reinterpret_cast<u32x4 *>(out + m * N + n);
-                    if constexpr (kAdd)
-                        v = __builtin_bit_cast(u32x4, __builtin_bit_cast(f32x4, *o) + __builtin_bit_cast(f32x4, v));
-                    put<kOp == kDw>(o, v);
-                }
-            }
+        }
+    };
+    // Weight gradients are written past L2: they are larger than every cache
+    // and would push the operands out.  Only whole lines, though: where rows
+    // do not start on one, L2 has to join the pieces (1.1 GB of zeros in rows
+    // of 8416 bytes: 580 us past L2, 326 through it).
+    if constexpr (kOp == kDw) {
+        if ((N * sizeof(Out)) % 128 == 0 && reinterpret_cast<uintptr_t>(p.out) % 128 == 0) {
+            results(ic<1>{});
+            asm volatile("; past L2");   // or the ends of both versions become one, through L2
+            return;
         }
     }
+    results(ic<0>{});
+}
+
+// The weight gradient of an expert without rows: zeros, in whole lines
+// whatever the rows' length; part i of `parts` (1.1 GB of rows of 8416 bytes
+// 323 us by tiles, 202 so).
+template <class Out>
+__device__ __forceinline__ void zero_part(const ExpertParams &p, int32_t e, int32_t i, int32_t parts) {
+    const int64_t groups = p.R * p.C * static_cast<int64_t>(sizeof(Out)) / 16;
+    const int64_t each = ((groups + parts - 1) / parts + kThreads - 1) / kThreads * kThreads;
+    u32x4 *o = reinterpret_cast<u32x4 *>(static_cast<Out *>(p.out) + static_cast<int64_t>(e) * p.R * p.C);
+    const int64_t end = min((i + 1) * each, groups);
+    for (int64_t g = i * each + threadIdx.x; g < end; g += kThreads) put<true>(o + g, u32x4{0, 0, 0, 0});
 }
 
 // The last rows of an expert take a tile of the height that they need, in
@@ -531,6 +581,10 @@ __global__ __launch_bounds__(kThreads, S::kPerCu) void k_expert(const ExpertPara
         t.lo = r.x;
         t.n = r.y;
         t.half = -1;
+        if (t.n == 0) {
+            if constexpr (!kAdd) zero_part<Out>(p, t.e, v - t.e * each, each);
+            return;
+        }
         place(t, v - t.e * each, m_tiles, n_tiles);
     } else {
         if (!token_tile<S::kM, kHalves>(p, n_tiles, t)) return;
