@@ -782,7 +782,8 @@ enum { SFT_F32 = 0, SFT_BF16 = 1 };
  * sizes: results are deterministic, and a token's do not depend on the other
  * tokens of its group.  No workspace, nothing allocated.
  * Limits: R and C multiples of 8 and at most 2^20, T < 2^30, E <= 65536,
- * fewer than 2^31 output tiles.
+ * fewer than 2^24 output tiles (of 64 x 64 to 256 x 256).  What a call writes
+ * must not overlap what it reads.
  * Errors: SFT_EINVAL (null pointers, negative sizes, bad out_type),
  * SFT_ESHAPE (R or C), SFT_EALIGN, SFT_ENOTSUP (beyond the limits), SFT_EHIP.
  */
@@ -820,7 +821,7 @@ size_t sft_grad_clip_workspace(const sft_grad_vec *vecs, int32_t n_vecs);
 /*
  * The norm of many gradients taken together, and the factor that clips it:
  *   norm = sqrt(sum over every value g of g^2),  clip = min(1, max_norm / norm)
- * and clip = 0 where norm is infinite or not a number.  sft_adamw and
+ * and clip = 0 where a value is infinite or not a number.  sft_adamw and
  * sft_coupled_update read such a factor from the device (sft_coupled_update
  * a pair of them: two calls, each with its half of the pair as `clip`).
  *   clip      device float, 4-byte aligned
@@ -830,7 +831,8 @@ size_t sft_grad_clip_workspace(const sft_grad_vec *vecs, int32_t n_vecs);
  *             (16-byte aligned; no initialisation needed); calls sharing it
  *             must be ordered on one stream
  * Summed in fp64 in a fixed order: deterministic, and no square of a float
- * overflows.  An empty list has norm 0 and clip 1.
+ * overflows; a norm beyond the range of a float is written as infinity, with
+ * the factor that it asks for.  An empty list has norm 0 and clip 1.
  * Errors: SFT_EINVAL (null pointers, negative sizes, bad type, max_norm not
  * positive), SFT_EALIGN, SFT_ECAPACITY (workspace too small), SFT_ENOTSUP
  * (2^42 values in a vector, or 2^31 chunks of 8192 values in a launch),
@@ -892,12 +894,11 @@ typedef struct sft_adamw_vec {
  *             the tables
  *   clip      device float, 4-byte aligned, or NULL for 1.  Where it is not a
  *             positive finite number the step is left out: no tensor changes.
- * Arrays that the step writes must not overlap.
+ * Arrays that the step writes must not overlap each other, nor a gradient.
  * Errors: SFT_EINVAL (null pointers, bad sizes, types, betas, eps (negative or
- * subnormal) or step,
- * overlapping arrays), SFT_EALIGN, SFT_ENOTSUP (2^42 values in a tensor, or
- * 2^31 chunks in a launch), SFT_EHIP; a failed argument check launches
- * nothing.
+ * subnormal) or step, written arrays that overlap), SFT_EALIGN, SFT_ENOTSUP
+ * (2^42 values in a tensor, or 2^24 chunks of 2048 values, of 4096 with 8-bit
+ * states, in all), SFT_EHIP; a failed argument check launches nothing.
  */
 int sft_adamw(const sft_adamw_vec *vecs, int32_t n_vecs, int32_t step, const int32_t *step_dev, const float *clip,
               const sft_adam *hp, void *stream);

@@ -471,7 +471,7 @@ __global__ __launch_bounds__(kThreads) void k_adamw8(const Adam8Params a) {
             top_r = max(top_r, __builtin_bit_cast(uint32_t, rr[j]) & 0x7fffffffu);
         }
         const uint32_t bm = scale_byte(block_max(top_m)), br = scale_byte(block_max(top_r));
-        // codes of a block that is not finite are zero: its scale says so
+        // in a block that is not finite the codes mean nothing: its scale says so
         const int32_t shift_m = bm == 255u ? -1000 : 7 - static_cast<int32_t>(bm);
         const int32_t shift_r = br == 255u ? -1000 : 7 - static_cast<int32_t>(br);
         uint32_t w = (static_cast<uint32_t>(at) + static_cast<uint32_t>(i)) * 0xC2B2AE35u + s.t * 0x9E3779B9u;
@@ -607,7 +607,6 @@ int send(L &l, int p_type, int g_type, hipStream_t st);
 template <class L>
 int send(L &l, int p_type, int g_type, hipStream_t st) {
     if (l.used == 0) return SFT_OK;
-    SFT_CHECK(l.chunks < (int64_t(1) << 31), SFT_ENOTSUP, "sft_adamw: 2^31 chunks or more in one launch");
     l.close();
     const dim3 grid(static_cast<uint32_t>(l.chunks)), block(kThreads);
     if constexpr (std::is_same<L, Launch32>::value) {
@@ -674,6 +673,7 @@ int adamw(const sft_adamw_vec *vecs, int32_t n_vecs, int32_t step, const int32_t
               "sft_adamw: eps is negative, subnormal or not a number");
     SFT_CHECK(step_dev || step >= 1, SFT_EINVAL, "sft_adamw: step %d < 1", step);
     SFT_CHECK(aligned(step_dev, 4) && aligned(clip, 4), SFT_EALIGN, "sft_adamw: step_dev or clip not 4-byte aligned");
+    int64_t chunks = 0;
     std::vector<Range> written;
     written.reserve(static_cast<size_t>(n_vecs) * 3);
     const auto writes = [&](const void *p, int64_t bytes) {
@@ -691,7 +691,10 @@ int adamw(const sft_adamw_vec *vecs, int32_t n_vecs, int32_t step, const int32_t
         SFT_CHECK(aligned(v.p, type_size(v.p_type)) && aligned(v.grad, type_size(v.g_type)) &&
                       aligned(v.p_live, 2) && (v.scale || (aligned(v.m, 4) && aligned(v.v, 4))),
                   SFT_EALIGN, "sft_adamw: vector %d: a pointer is not aligned to its type", i);
+        chunks += v.scale ? (v.n + kChunk8 - 1) / kChunk8 : (v.n + kChunk32 - 1) / kChunk32;
     }
+    // a launch has fewer than 2^32 threads
+    SFT_CHECK(chunks < (int64_t(1) << 32) / kThreads, SFT_ENOTSUP, "sft_adamw: 2^24 chunks of values or more");
     // array by array: each ascends on its own where the tensors are views of flat buffers
     for (int32_t i = 0; i < n_vecs; ++i)
         if (vecs[i].n) writes(vecs[i].p, vecs[i].n * int64_t(type_size(vecs[i].p_type)));

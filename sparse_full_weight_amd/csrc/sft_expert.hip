@@ -634,7 +634,8 @@ int launch(const char *who, ExpertParams p, int32_t out_type, bool add, hipStrea
     // fewer where the launch has less than a round
     p.chunk = static_cast<int32_t>(std::min<int64_t>(32 * S::kPerCu, (units + 7) / 8));
     const int64_t run = 8 * int64_t(p.chunk), groups = (units + run - 1) / run * run;
-    SFT_CHECK(groups < (int64_t(1) << 31), SFT_ENOTSUP, "%s: 2^31 output tiles or more", who);
+    // a launch has fewer than 2^32 threads
+    SFT_CHECK(groups < (int64_t(1) << 32) / kThreads, SFT_ENOTSUP, "%s: 2^24 output tiles or more", who);
     const dim3 grid(static_cast<uint32_t>(groups)), block(kThreads);
     if (out_type == SFT_BF16)
         hipLaunchKernelGGL((k_expert<kOp, S, uint16_t, false>), grid, block, 0, st, p);

@@ -30,6 +30,8 @@ def _hp(**kw):
 @pytest.mark.parametrize("what,code", [
     (dict(vecs=[_vec(n=-1)]), _lib.SFT_EINVAL),
     (dict(vecs=[_vec(n=1 << 42)]), _lib.SFT_ENOTSUP),
+    (dict(vecs=[_vec(n=(2048 << 24) - 2047)]), _lib.SFT_ENOTSUP),                # 2^24 chunks
+    (dict(vecs=[_vec(n=4096 << 23, scale=BASE), _vec(n=2048 << 23)]), _lib.SFT_ENOTSUP),
     (dict(vecs=[_vec(p_type=2)]), _lib.SFT_EINVAL),
     (dict(vecs=[_vec(g_type=-1)]), _lib.SFT_EINVAL),
     (dict(vecs=[_lib.CAdamwVec(16, BASE, None, BASE + 2048, BASE + 3072, None, None, 0, 0)]), _lib.SFT_EINVAL),

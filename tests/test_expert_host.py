@@ -35,6 +35,11 @@ def test_refuses(op, kw, code):
     assert _lib.lib().sft_last_error()
 
 
+@pytest.mark.parametrize("kw", [dict(E=65536, R=8, C=65536), dict(E=65536, R=1 << 20, C=8, accumulate=1)])
+def test_weight_gradients_in_too_many_tiles(kw):
+    assert _call("dw", **kw) == _lib.SFT_ENOTSUP
+
+
 def test_dw_accumulates_only_fp32():
     assert _call("dw", type=1, accumulate=1) == _lib.SFT_EINVAL
 
