@@ -401,8 +401,9 @@ __device__ __forceinline__ void multiply_part(const ExpertParams &p, const Tile 
         f(ic<1>{});
         if constexpr (kStages > 2) f(ic<2>{});
         if constexpr (kStages > 3) f(ic<3>{});
+        if constexpr (kStages > 4) f(ic<4>{});
     };
-    static_assert(kStages >= 2 && kStages <= 4 && KK % 2 == 0, "stages");
+    static_assert(kStages >= 2 && kStages <= 5 && KK % 2 == 0, "stages");
     // The loop takes kStages stages a turn; the KT % kStages stages that do not
     // fill a turn come first, by code of their own for each such number: the
     // first stage then sits in LDS where the loop's first turn will find its
@@ -426,6 +427,9 @@ __device__ __forceinline__ void multiply_part(const ExpertParams &p, const Tile 
     if (KT > 0) {
         constexpr bool kOdd = kStages > 2 && BM * BN <= 128 * 256;
         const int32_t odd = kOdd ? KT % kStages : 0;
+        if constexpr (kOdd && kStages > 4) {
+            if (odd == 4) start(ic<kStages - 4>{});
+        }
         if constexpr (kOdd && kStages > 3) {
             if (odd == 3) start(ic<kStages - 3>{});
         }
@@ -667,7 +671,10 @@ int launch(const char *who, ExpertParams p, int32_t out_type, bool add, hipStrea
 //   64 x 128 and 64 x 64: few tiles (16 x 1024 x 1024 forward at 4096: 64 x
 //     128 20.2, 128 x 192 26.1, 64 x 64 26.8; at 1024: 13.9, 17.8, 12.0)
 //   64 x 64 with four stages, forward: weights streamed for a few tokens (64 x
-//     1376 x 4096 at 8 tokens: 20, every other shape 34 to 62)
+//     1376 x 4096 at 8 tokens: 20, every other shape 34 to 62); five stages
+//     where sums are long and no CU has more than one tile, so that only the
+//     ring keeps loads in flight (the same 17.0, four stages 19.1; 12 x 1000 x
+//     520 at 1003 tokens, of two tiles a CU and short sums, 9.3 and 8.9)
 template <int kOp>
 int product(const char *who, const ExpertParams &p, int32_t out_type, bool add, void *stream) {
     const hipStream_t st = static_cast<hipStream_t>(stream);
@@ -691,6 +698,10 @@ int product(const char *who, const ExpertParams &p, int32_t out_type, bool add, 
             return launch<kOp, Shape<128, 192, 64, 2>>(who, p, out_type, add, st);
         if (tiles_of<kOp>(p, 64, 128) >= 256 && rows >= 128)
             return launch<kOp, Shape<64, 128, 64, 2>>(who, p, out_type, add, st);
+    }
+    if constexpr (kOp == kForward) {
+        if (p.C >= 2048 && tiles_of<kOp>(p, 64, 64) <= sft::num_cus())
+            return launch<kOp, Shape<64, 64, 64, 5>>(who, p, out_type, add, st);
     }
     return launch<kOp, Shape<64, 64, 64, 4>>(who, p, out_type, add, st);
 }

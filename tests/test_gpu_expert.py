@@ -124,6 +124,13 @@ def test_every_shape_of_tiles(gpu_lib, op, counts, R, C, integer):
         _run(op, counts, R, C, BF16)
 
 
+@pytest.mark.parametrize("C", [2040, 2048, 2104, 2176, 2240, 2248, 2304, 4096])
+def test_few_tokens_with_long_sums(gpu_lib, C):
+    # sums that end in each place of the five stages of the forward's ring; integers are exact below 2^24
+    _run("forward", [2, 0, 1, 66], 328, C, F32, start=1, behind=2, integer=True)
+    _run("forward", [1], 136, C, BF16)
+
+
 @pytest.mark.parametrize("op", OPS)
 @pytest.mark.parametrize("E", [1, 63, 64, 65, 200])
 def test_numbers_of_experts(gpu_lib, op, E):
