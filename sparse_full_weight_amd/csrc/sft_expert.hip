@@ -664,20 +664,29 @@ int launch(const char *who, ExpertParams p, int32_t out_type, bool add, hipStrea
 //     shorter sums or groups (64 x 1376 x 4096 at 16384, forward 275, 256 x
 //     256 299; input gradient 265, 256 x 256 272, at 4096 143 and 162)
 //   128 x 128: forward of groups about that long (8 x 11008 x 4096 at 1024:
-//     177, 128 x 192 207, 256 x 256 202)
+//     177, 128 x 192 207, 256 x 256 202; 64 x 1376 x 4096 at 8192: 184, 221),
+//     and shorter groups where the rounds of workgroups come out so much better
+//     (64 x 2816 x 2048 at 256 to 4096, input gradient: 125 to 143, 128 x 192
+//     143 to 160; but 64 x 1376 x 4096 at 4096, forward: 190, 166)
 //   128 x 256, stages of 32: the weight gradient, whose operands are both
 //     read in long rows (8 x 11008 x 4096 at 64 / 4096 / 16384: 259 / 599 /
 //     1412; 128 x 192 287 / 632 / 1553, 256 x 256 449 / 639 / 1409)
-//   64 x 128 and 64 x 64: few tiles (16 x 1024 x 1024 forward at 4096: 64 x
-//     128 20.2, 128 x 192 26.1, 64 x 64 26.8; at 1024: 13.9, 17.8, 12.0)
-//   64 x 64 with four stages, forward: weights streamed for a few tokens (64 x
-//     1376 x 4096 at 8 tokens: 20, every other shape 34 to 62); five stages
+//   64 x 128: few tiles of longer groups (16 x 1024 x 1024 forward at 4096:
+//     20.2, 128 x 192 26.1, 64 x 64 26.8); with three stages where there is
+//     more than one 64 x 64 tile a CU, but one round of these (16 x 1376 x 1000
+//     at 256 / 1024, input gradient 15.5 / 17.8, 64 x 64 18.1 / 20.8; forward at
+//     1024 25.9 and 28.9; long sums need the loads of more tiles in flight: 8 x
+//     4096 x 11008 forward at 64: 182, 64 x 64 136)
+//   64 x 64 with four stages: the fewest tiles, and forward of short groups
+//     (64 x 1376 x 4096 at 8 / 1024: 20 / 138, 128 x 192 34 / 159; 32 x 4096 x
+//     4096 at 256: 196 and 220; 64 x 4096 x 1376: 124 and 145); five stages
 //     where sums are long and no CU has more than one tile, so that only the
 //     ring keeps loads in flight (the same 17.0, four stages 19.1; 12 x 1000 x
 //     520 at 1003 tokens, of two tiles a CU and short sums, 9.3 and 8.9)
 template <int kOp>
 int product(const char *who, const ExpertParams &p, int32_t out_type, bool add, void *stream) {
     const hipStream_t st = static_cast<hipStream_t>(stream);
+    [[maybe_unused]] const int64_t cus = sft::num_cus();
     if constexpr (kOp == kDw) {
         if (tiles_of<kOp>(p, 128, 256) >= 256)
             return launch<kOp, Shape<128, 256, 32, 3>>(who, p, out_type, add, st);
@@ -685,22 +694,32 @@ int product(const char *who, const ExpertParams &p, int32_t out_type, bool add, 
             return launch<kOp, Shape<128, 128, 64, 2>>(who, p, out_type, add, st);
     } else {
         const int64_t rows = p.T / p.E;      // of an expert on average
+        const int64_t K = kOp == kForward ? p.C : p.R;
         if constexpr (kOp == kForward) {
             if (rows >= 512 && tiles_of<kOp>(p, 256, 256) >= 1024)
                 return launch<kOp, Shape<256, 256, 64, 2>>(who, p, out_type, add, st);
-            if (rows >= 48 && rows <= 192 && tiles_of<kOp>(p, 128, 128) >= 512)
+            if (rows >= 96 && rows <= 192 && tiles_of<kOp>(p, 128, 128) >= 512)
                 return launch<kOp, Shape<128, 128, 64, 2>>(who, p, out_type, add, st);
         } else {
             if (p.R >= 4096 && tiles_of<kOp>(p, 256, 256) >= 128)
                 return launch<kOp, Shape<256, 256, 32, 4>>(who, p, out_type, add, st);
         }
-        if (tiles_of<kOp>(p, 128, 192) >= 320 && (kOp == kDx || rows > 4))
+        if (tiles_of<kOp>(p, 128, 192) >= 320 && (kOp == kDx || rows >= 48)) {
+            // rounds of one tile an expert and column, times the tile's width
+            const int64_t N = kOp == kForward ? p.R : p.C;
+            const int64_t narrow = 2 * ((p.E * ((N + 127) / 128) + 2 * cus - 1) / (2 * cus));
+            const int64_t wide = 3 * ((p.E * ((N + 191) / 192) + 2 * cus - 1) / (2 * cus));
+            if (rows >= 4 && rows < 96 && 10 * narrow <= 7 * wide)
+                return launch<kOp, Shape<128, 128, 64, 2>>(who, p, out_type, add, st);
             return launch<kOp, Shape<128, 192, 64, 2>>(who, p, out_type, add, st);
+        }
         if (tiles_of<kOp>(p, 64, 128) >= 256 && rows >= 128)
             return launch<kOp, Shape<64, 128, 64, 2>>(who, p, out_type, add, st);
+        if (K <= 4096 && tiles_of<kOp>(p, 64, 64) > cus && tiles_of<kOp>(p, 64, 128) <= 2 * cus)
+            return launch<kOp, Shape<64, 128, 64, 3>>(who, p, out_type, add, st);
     }
     if constexpr (kOp == kForward) {
-        if (p.C >= 2048 && tiles_of<kOp>(p, 64, 64) <= sft::num_cus())
+        if (p.C >= 2048 && tiles_of<kOp>(p, 64, 64) <= cus)
             return launch<kOp, Shape<64, 64, 64, 5>>(who, p, out_type, add, st);
     }
     return launch<kOp, Shape<64, 64, 64, 4>>(who, p, out_type, add, st);

@@ -124,6 +124,19 @@ def test_every_shape_of_tiles(gpu_lib, op, counts, R, C, integer):
         _run(op, counts, R, C, BF16)
 
 
+@pytest.mark.parametrize("integer", [False, True])
+@pytest.mark.parametrize("op,counts,R,C", [
+    ("forward", [50, 48, 0, 129] * 12, 2056, 72), ("dx", [4, 0, 70, 9] * 12, 136, 2056),     # 128 x 128, short groups
+    ("forward", [3, 1, 0] * 11, 520, 72), ("forward", [3, 65, 0] * 11, 520, 200),            # 64 x 128, three stages
+    ("forward", [30, 1, 0] * 11, 584, 328), ("dx", [3, 1, 0] * 11, 56, 520), ("dx", [3, 65, 0] * 11, 200, 520),
+    ("dx", [30, 1, 0] * 11, 328, 584),
+])
+def test_shapes_of_tiles_of_short_groups(gpu_lib, op, counts, R, C, integer):
+    _run(op, counts, R, C, F32, start=1, behind=2, integer=integer)
+    if not integer:
+        _run(op, counts, R, C, BF16)
+
+
 @pytest.mark.parametrize("C", [2040, 2048, 2104, 2176, 2240, 2248, 2304, 4096])
 def test_few_tokens_with_long_sums(gpu_lib, C):
     # sums that end in each place of the five stages of the forward's ring; integers are exact below 2^24
