@@ -664,10 +664,12 @@ int launch(const char *who, ExpertParams p, int32_t out_type, bool add, hipStrea
 //     shorter sums or groups (64 x 1376 x 4096 at 16384, forward 275, 256 x
 //     256 299; input gradient 265, 256 x 256 272, at 4096 143 and 162)
 //   128 x 128: forward of groups about that long (8 x 11008 x 4096 at 1024:
-//     177, 128 x 192 207, 256 x 256 202; 64 x 1376 x 4096 at 8192: 184, 221),
-//     and shorter groups where the rounds of workgroups come out so much better
-//     (64 x 2816 x 2048 at 256 to 4096, input gradient: 125 to 143, 128 x 192
-//     143 to 160; but 64 x 1376 x 4096 at 4096, forward: 190, 166)
+//     177, 128 x 192 207, 256 x 256 202; 64 x 1376 x 4096 at 8192: 184, 221;
+//     not where they take more rounds: 24 x 1536 x 2048 at 4096: 70, 49),
+//     and where the rounds of workgroups come out much better (64 x 2816 x 2048
+//     at 256 to 4096, input gradient: 125 to 143, 128 x 192 143 to 160; 16 x
+//     1376 x 1000 at 4096, forward: 32, 42; but 64 x 1376 x 4096 at 4096: 190,
+//     166)
 //   128 x 256, stages of 32: the weight gradient, whose operands are both
 //     read in long rows (8 x 11008 x 4096 at 64 / 4096 / 16384: 259 / 599 /
 //     1412; 128 x 192 287 / 632 / 1553, 256 x 256 449 / 639 / 1409)
@@ -687,6 +689,8 @@ template <int kOp>
 int product(const char *who, const ExpertParams &p, int32_t out_type, bool add, void *stream) {
     const hipStream_t st = static_cast<hipStream_t>(stream);
     [[maybe_unused]] const int64_t cus = sft::num_cus();
+    // rounds of workgroups, two a CU, that so many tiles take
+    [[maybe_unused]] const auto rounds = [cus](int64_t tiles) { return (tiles + 2 * cus - 1) / (2 * cus); };
     if constexpr (kOp == kDw) {
         if (tiles_of<kOp>(p, 128, 256) >= 256)
             return launch<kOp, Shape<128, 256, 32, 3>>(who, p, out_type, add, st);
@@ -698,18 +702,22 @@ int product(const char *who, const ExpertParams &p, int32_t out_type, bool add, 
         if constexpr (kOp == kForward) {
             if (rows >= 512 && tiles_of<kOp>(p, 256, 256) >= 1024)
                 return launch<kOp, Shape<256, 256, 64, 2>>(who, p, out_type, add, st);
-            if (rows >= 96 && rows <= 192 && tiles_of<kOp>(p, 128, 128) >= 512)
+            if (rows >= 96 && rows <= 192 && tiles_of<kOp>(p, 128, 128) >= 512 &&
+                2 * rounds(tiles_of<kOp>(p, 128, 128)) <= 3 * rounds(tiles_of<kOp>(p, 128, 192)))
                 return launch<kOp, Shape<128, 128, 64, 2>>(who, p, out_type, add, st);
         } else {
             if (p.R >= 4096 && tiles_of<kOp>(p, 256, 256) >= 128)
                 return launch<kOp, Shape<256, 256, 32, 4>>(who, p, out_type, add, st);
         }
         if (tiles_of<kOp>(p, 128, 192) >= 320 && (kOp == kDx || rows >= 48)) {
-            // rounds of one tile an expert and column, times the tile's width
+            // rounds times a tile's width; an expert has one tile a column, or
+            // its rows and half a step of 64 more (between, whether one or two
+            // is up to the groups: 64 x 1408 x 2048 at 8192, input gradient, 90
+            // by this shape, 128 x 128 102)
             const int64_t N = kOp == kForward ? p.R : p.C;
-            const int64_t narrow = 2 * ((p.E * ((N + 127) / 128) + 2 * cus - 1) / (2 * cus));
-            const int64_t wide = 3 * ((p.E * ((N + 191) / 192) + 2 * cus - 1) / (2 * cus));
-            if (rows >= 4 && rows < 96 && 10 * narrow <= 7 * wide)
+            const int64_t high = p.E * (rows < 96 ? 128 : rows + 32) / 128;
+            const int64_t narrow = 2 * rounds(high * ((N + 127) / 128)), wide = 3 * rounds(high * ((N + 191) / 192));
+            if (rows >= 4 && (rows < 96 || rows > 192) && 10 * narrow <= 7 * wide)
                 return launch<kOp, Shape<128, 128, 64, 2>>(who, p, out_type, add, st);
             return launch<kOp, Shape<128, 192, 64, 2>>(who, p, out_type, add, st);
         }
