@@ -13,7 +13,7 @@ HP = (0.1, 0.9, 0.999, 1e-8, 0.0, BASE + 8192, BASE + 8192, 4)
 
 
 def _vec(n=16, at=BASE, scale=None, live=None, p_type=0, g_type=0):
-    return _lib.CAdamwVec(n, at, at + 1024, at + 2048, at + 3072, scale, live, p_type, g_type)
+    return _lib.CAdamwVec(n, at, at + 1024, at + 2048, at + 3328, scale, live, p_type, g_type)
 
 
 def _adamw(vecs, step=1, hp=HP, clip=None, step_dev=None):
@@ -34,7 +34,7 @@ def _hp(**kw):
     (dict(vecs=[_vec(n=4096 << 23, scale=BASE), _vec(n=2048 << 23)]), _lib.SFT_ENOTSUP),
     (dict(vecs=[_vec(p_type=2)]), _lib.SFT_EINVAL),
     (dict(vecs=[_vec(g_type=-1)]), _lib.SFT_EINVAL),
-    (dict(vecs=[_lib.CAdamwVec(16, BASE, None, BASE + 2048, BASE + 3072, None, None, 0, 0)]), _lib.SFT_EINVAL),
+    (dict(vecs=[_lib.CAdamwVec(16, BASE, None, BASE + 2048, BASE + 3328, None, None, 0, 0)]), _lib.SFT_EINVAL),
     (dict(vecs=[_vec(at=BASE + 2)]), _lib.SFT_EALIGN),
     (dict(vecs=[_vec(live=BASE + 4097)]), _lib.SFT_EALIGN),
     (dict(vecs=[_vec(), _vec()]), _lib.SFT_EINVAL),                              # the same tensor twice
