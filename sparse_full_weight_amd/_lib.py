@@ -556,8 +556,16 @@ class Adam:
     weight_decay: float = 0.0
 
     def c(self) -> CAdam:
+        """The C struct, after checking that both tables are fp32 and equally
+        long (the kernels read both up to entry t_max)."""
+        import torch
+        n = self.bc1.numel()
+        if self.bc1.dtype != torch.float32 or self.bc2.dtype != torch.float32:
+            raise TypeError(f"bias tables: expected float32, got {self.bc1.dtype} and {self.bc2.dtype}")
+        if n < 2 or self.bc2.numel() != n:
+            raise ValueError(f"bias tables: {n} and {self.bc2.numel()} entries, expected t_max + 1 >= 2 of each")
         return CAdam(self.lr, self.beta1, self.beta2, self.eps, self.weight_decay, _dev(self.bc1),
-                     _dev(self.bc2), self.bc1.numel() - 1)
+                     _dev(self.bc2), n - 1)
 
 
 @dataclass

@@ -98,3 +98,18 @@ def test_grad_clip_workspace():
     assert need([_lib.CGradVec(1 << 40, BASE, 1)]) == 8 * 2048
     assert need([_lib.CGradVec(1, BASE, 1)] * 201) == 8 * 201
     assert need([_lib.CGradVec(-1, BASE, 1)]) == C.c_size_t(-1).value
+
+
+@pytest.mark.parametrize("bc1,bc2,error", [
+    ((5, "float32"), (4, "float32"), ValueError), ((4, "float32"), (5, "float32"), ValueError),
+    ((1, "float32"), (1, "float32"), ValueError), ((0, "float32"), (0, "float32"), ValueError),
+    ((5, "float64"), (5, "float64"), TypeError), ((5, "float32"), (5, "float64"), TypeError),
+    ((5, "float16"), (5, "float32"), TypeError),
+])
+def test_adam_refuses_bias_tables_that_do_not_fit(bc1, bc2, error):
+    # a kernel reads both tables up to entry numel - 1 of the first, as fp32: whatever the call, these are refused
+    # before it is looked where the tables are
+    torch = pytest.importorskip("torch")
+    tables = [torch.zeros(n, dtype=getattr(torch, t)) for n, t in (bc1, bc2)]
+    with pytest.raises(error, match="bias table"):
+        _lib.Adam(0.1, 0.9, 0.999, 1e-8, *tables).c()
