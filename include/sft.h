@@ -573,7 +573,10 @@ int sft_masked_dw_update_noalloc(const sft_dw_group *groups, int32_t n_groups, c
  * its list contributes a zero gradient; then each matrix whose row is listed
  * takes the plain update above with its effective gradient.  The blend
  * weights a_own/a_cross come from the caller's phase schedule; clip points to
- * a device float[2] {clipA, clipB}, or is NULL for {1, 1}.
+ * a device float[2] {clipA, clipB}, or is NULL for {1, 1}.  A gradient whose
+ * factor is 0 counts as zero, whatever it holds: with the factors that
+ * sft_grad_clip writes, infinities and NaN reach neither matrix.  (Both still
+ * take their step: the moments decay, and move the weights.)
  */
 /* The union of the two row lists is never formed: each matrix's rows are
  * updated by their own workgroups, which find the partner's row (if any) by a
@@ -823,7 +826,9 @@ size_t sft_grad_clip_workspace(const sft_grad_vec *vecs, int32_t n_vecs);
  *   norm = sqrt(sum over every value g of g^2),  clip = min(1, max_norm / norm)
  * and clip = 0 where a value is infinite or not a number.  sft_adamw and
  * sft_coupled_update read such a factor from the device (sft_coupled_update
- * a pair of them: two calls, each with its half of the pair as `clip`).
+ * a pair of them: two calls, each with its half of the pair as `clip`).  At 0
+ * sft_adamw leaves the step out; sft_coupled_update takes the step with that
+ * gradient as zero.
  *   clip      device float, 4-byte aligned
  *   norm      device float, 4-byte aligned, or NULL
  *   max_norm  positive; infinity measures only (clip = 1 for a finite norm)

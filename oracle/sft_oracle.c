@@ -595,7 +595,9 @@ ORACLE_API int oracle_sparse_update(oracle_mat *M, const oracle_adam *hp)
  *   gB~ = a_own * (clip_b * gB) + a_cross * (clip_a * gA),
  * each product and the sum rounded in fp32, over the union of the two masks;
  * a matrix whose row is inactive contributes a zero gradient and its own row
- * is not updated.  Each effective gradient then drives the step above.
+ * is not updated.  A gradient whose factor is 0 (one that is not finite)
+ * counts as zero, whatever it holds.  Each effective gradient then drives the
+ * step above.
  */
 ORACLE_API int oracle_coupled_update(oracle_mat *A, oracle_mat *B, float a_own, float a_cross,
                                      float clip_a, float clip_b, const oracle_adam *hp)
@@ -625,8 +627,8 @@ ORACLE_API int oracle_coupled_update(oracle_mat *A, oracle_mat *B, float a_own, 
             gb[c] = has_b ? B->G[ib * C + c] : 0.0f;
         }
         for (int64_t c = 0; c < C; ++c) {
-            float ca = clip_a * ga[c];
-            float cb = clip_b * gb[c];
+            float ca = clip_a * (clip_a != 0.0f ? ga[c] : 0.0f);
+            float cb = clip_b * (clip_b != 0.0f ? gb[c] : 0.0f);
             float own_a = a_own * ca, cross_a = a_cross * cb;
             float own_b = a_own * cb, cross_b = a_cross * ca;
             ea[c] = own_a + cross_a;

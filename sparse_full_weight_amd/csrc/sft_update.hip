@@ -527,15 +527,18 @@ __global__ __launch_bounds__(kThreads) void k_coupled_update(const PairParams p)
         constexpr int kPer = decltype(per)::value;
         const int64_t k = (wg - M.row_begin) * kPer + static_cast<int>(threadIdx.x) / (kThreads / kPer);
         const bool valid = k < M.n_active;
-        const int64_t r = valid ? M.rows[k] : 0;
-        const int64_t pk = valid ? find_row_wave(S.prow, S.pn, r) : -1;
         const float clip_a = S.clip ? S.clip[0] : 1.0f;
         const float clip_b = S.clip ? S.clip[1] : 1.0f;
+        const int64_t r = valid ? M.rows[k] : 0;
+        const int64_t pk = valid ? find_row_wave(S.prow, S.pn, r) : -1;
         PairGrad gr;
-        gr.own_row = row_buf(M.G + (valid ? k : 0) * M.C, valid ? 4 * M.C : 0);
-        gr.part_row = row_buf(pk >= 0 ? S.pG + pk * M.C : M.G, pk >= 0 ? 4 * M.C : 0);
         gr.c_self = S.self_is_b ? clip_b : clip_a;
         gr.c_part = S.self_is_b ? clip_a : clip_b;
+        // A gradient whose factor is 0 may hold infinities and NaN: its row
+        // becomes an empty buffer, which reads zero, not a product with 0.
+        const bool own = valid && gr.c_self != 0.0f, part = pk >= 0 && gr.c_part != 0.0f;
+        gr.own_row = row_buf(M.G + (own ? k : 0) * M.C, own ? 4 * M.C : 0);
+        gr.part_row = row_buf(part ? S.pG + pk * M.C : M.G, part ? 4 * M.C : 0);
         gr.a_own = S.a_own;
         gr.a_cross = S.a_cross;
         update_row<kThreads, kChunks, kPer>(M, k, valid, p.hp, gr);

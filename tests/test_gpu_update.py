@@ -188,6 +188,38 @@ def test_coupled_update_two_rows_per_workgroup(gpu_lib):
         assert_state_equal(mb.to_state(), wb, f"pair B C={A.q.shape[1]}")
 
 
+@pytest.mark.parametrize("C", [512, 4096, 8200])
+@pytest.mark.parametrize("side", ["a", "b", "ab"])
+def test_coupled_update_of_gradients_that_are_not_finite(gpu_lib, side, C):
+    # the factors as sft_grad_clip writes them, 0 for a gradient with an infinity or a NaN: it counts as zero, and
+    # neither matrix takes anything of it (at 4096 columns with more rows than CUs: two to a workgroup)
+    k, R = (163, 400) if C == 4096 else (20, 64)
+    g = synth.rng(1100 + C)
+    A, B = make_state(R, C, 1110, k + 4, True), make_state(R, C, 1120, k + 4, True)
+    ra, rb = (np.sort(g.choice(R, k, replace=False)).astype(np.int32) for _ in range(2))
+    sa, sb = (g.choice(k + 4, k, replace=False).astype(np.int32) for _ in range(2))
+    GA, GB = synth.gradient_rows(k, C, 0.2, 1130), synth.gradient_rows(k, C, 0.2, 1140)
+    if "a" in side:
+        GA[k // 2, 5], GA[3, C - 1] = np.nan, -np.inf
+    if "b" in side:
+        GB[2, 8], GB[k - 1, 0] = np.inf, np.nan
+    ma, mb = GpuMat(A, GA, ra, sa, None), GpuMat(B, GB, rb, sb, None)
+    clip = torch.full((2,), 9.0, device="cuda")
+    for i, m in enumerate((ma, mb)):
+        ws = torch.empty(_lib.sft_grad_clip_workspace([m.G]), dtype=torch.uint8, device="cuda")
+        _lib.sft_grad_clip([m.G], 1.0, clip[i:i + 1], None, ws)
+    ca, cb = clip.tolist()
+    assert (ca == 0.0) == ("a" in side) and (cb == 0.0) == ("b" in side)
+    _lib.sft_coupled_update([_lib.Pair(ma.upd(), mb.upd(), 0.8, 0.3, clip)], adam_dev(**HP))
+    torch.cuda.synchronize()
+    wa, wb = A.copy(), B.copy()
+    oracle.coupled_update(wa, GA, ra, sa, None, wb, GB, rb, sb, None, a_own=0.8, a_cross=0.3, clip_a=ca, clip_b=cb,
+                          weight_decay=0.0, **HP)
+    for m, want in ((ma, wa), (mb, wb)):
+        assert np.isfinite(want.delta).all() and np.isfinite(want.s).all()
+        assert_state_equal(m.to_state(), want, f"C={C}")
+
+
 def test_masked_writeback_bit_exact(gpu_lib):
     R, C = 333, 1032
     q, s, delta = synth.quant_state(R, C, 700)

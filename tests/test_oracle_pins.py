@@ -664,6 +664,26 @@ def test_coupled_swap_symmetry_and_partner_isolation():
         assert B1.s[r] == B.s[r]
 
 
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("side", ["a", "b", "ab"])
+def test_coupled_factor_of_zero_takes_a_gradient_as_zero(bad, side):
+    # a factor of 0 is what the norm of a gradient that is not finite gives: neither matrix may see any of it
+    A, B, ra, rb, GA, GB, sa, sb = _pair_inputs(500)
+    A2, B2 = A.copy(), B.copy()
+    ZA, ZB = GA.copy(), GB.copy()
+    kw = dict(a_own=0.8, a_cross=0.35, clip_a=0.9, clip_b=0.7, **HP)
+    if "a" in side:
+        GA[1, 3] = bad
+        ZA[:], kw["clip_a"] = 0, 0.0
+    if "b" in side:
+        GB[0, 5] = bad
+        ZB[:], kw["clip_b"] = 0, 0.0
+    oracle.coupled_update(A, GA, ra, sa, None, B, GB, rb, sb, None, **kw)
+    oracle.coupled_update(A2, ZA, ra, sa, None, B2, ZB, rb, sb, None, **kw)
+    assert _same(A, A2) and _same(B, B2)
+    assert np.isfinite(A.delta).all() and np.isfinite(B.delta).all()
+
+
 def test_coupled_blend_direction_vs_float64():
     # At t = 1 from zero moments each element moves by ~lr against the sign of
     # its effective gradient, so the direction exposes the blend
