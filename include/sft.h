@@ -899,11 +899,13 @@ typedef struct sft_adamw_vec {
  *             the tables
  *   clip      device float, 4-byte aligned, or NULL for 1.  Where it is not a
  *             positive finite number the step is left out: no tensor changes.
- * Arrays that the step writes must not overlap each other, nor a gradient.
+ * Arrays that the step writes must not overlap each other, nor a gradient, a
+ * bias table, clip or step_dev.
  * Errors: SFT_EINVAL (null pointers, bad sizes, types, betas, eps (negative or
- * subnormal) or step, written arrays that overlap), SFT_EALIGN, SFT_ENOTSUP
- * (2^42 values in a tensor, or 2^24 chunks of 2048 values, of 4096 with 8-bit
- * states, in all), SFT_EHIP; a failed argument check launches nothing.
+ * subnormal) or step, written arrays that overlap each other or an input),
+ * SFT_EALIGN, SFT_ENOTSUP (2^42 values in a tensor, or 2^24 chunks of 2048
+ * values, of 4096 with 8-bit states, in all), SFT_EHIP; a failed argument
+ * check launches nothing.
  */
 int sft_adamw(const sft_adamw_vec *vecs, int32_t n_vecs, int32_t step, const int32_t *step_dev, const float *clip,
               const sft_adam *hp, void *stream);

@@ -567,6 +567,16 @@ bool overlap(std::vector<Range> &r) {
     return false;
 }
 
+// Whether the `bytes` bytes at p touch one of the ranges, which ascend and are
+// apart; at: the range where the last search ended, tried first.
+bool inside(const std::vector<Range> &r, const void *p, int64_t bytes, size_t &at) {
+    const uint8_t *lo = static_cast<const uint8_t *>(p);
+    if (!((at == 0 || r[at - 1].hi <= lo) && (at == r.size() || r[at].hi > lo)))
+        at = static_cast<size_t>(std::partition_point(r.begin(), r.end(), [lo](const Range &x) { return x.hi <= lo; }) -
+                                 r.begin());
+    return at < r.size() && r[at].lo < lo + bytes;
+}
+
 template <class Params, int kMax, int64_t kChunk>
 struct Launch {
     Params a{};
@@ -708,6 +718,15 @@ int adamw(const sft_adamw_vec *vecs, int32_t n_vecs, int32_t step, const int32_t
             writes(vecs[i].p_live, vecs[i].n * 2);
         }
     SFT_CHECK(!overlap(written), SFT_EINVAL, "sft_adamw: two arrays that the step writes overlap");
+    // other workgroups may still read what one of them writes
+    size_t at = 0;
+    for (int32_t i = 0; i < n_vecs; ++i)
+        SFT_CHECK(vecs[i].n == 0 || !inside(written, vecs[i].grad, vecs[i].n * int64_t(type_size(vecs[i].g_type)), at),
+                  SFT_EINVAL, "sft_adamw: vector %d: the gradient overlaps an array that the step writes", i);
+    const int64_t table = 4 * (int64_t(hp->t_max) + 1);
+    SFT_CHECK(!inside(written, hp->bc1, table, at) && !inside(written, hp->bc2, table, at) &&
+                  !(clip && inside(written, clip, 4, at)) && !(step_dev && inside(written, step_dev, 4, at)),
+              SFT_EINVAL, "sft_adamw: a bias table, clip or step_dev overlaps an array that the step writes");
 
     AdamScalars h{};
     h.lr = hp->lr;

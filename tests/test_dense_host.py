@@ -113,3 +113,25 @@ def test_adam_refuses_bias_tables_that_do_not_fit(bc1, bc2, error):
     tables = [torch.zeros(n, dtype=getattr(torch, t)) for n, t in (bc1, bc2)]
     with pytest.raises(error, match="bias table"):
         _lib.Adam(0.1, 0.9, 0.999, 1e-8, *tables).c()
+
+
+@pytest.mark.parametrize("what", [
+    dict(vecs=[_lib.CAdamwVec(16, BASE, BASE, BASE + 2048, BASE + 3328, None, None, 0, 0)]),          # p itself
+    dict(vecs=[_lib.CAdamwVec(16, BASE, BASE + 60, BASE + 2048, BASE + 3328, None, None, 0, 0)]),     # p's last value
+    dict(vecs=[_lib.CAdamwVec(16, BASE, BASE + 2048 - 60, BASE + 2048, BASE + 3328, None, None, 0, 0)]),
+    dict(vecs=[_lib.CAdamwVec(16, BASE, BASE + 3328 + 32, BASE + 2048, BASE + 3328, None, None, 0, 1)]),
+    dict(vecs=[_lib.CAdamwVec(16, BASE, BASE + 1024, BASE + 2048, BASE + 3328, None, BASE + 1024, 0, 1)]),
+    dict(vecs=[_lib.CAdamwVec(16, BASE, BASE + 1024, BASE + 2048, BASE + 3328, BASE + 1084, None, 0, 0)]),
+    # a gradient longer than the gap to another tensor's p, both lists out of order
+    dict(vecs=[_vec(at=BASE + 4608), _lib.CAdamwVec(64, BASE, BASE + 4400, BASE + 2048, BASE + 3328, None, None, 0, 0)]),
+    # two gradients with a short one behind a long one's start: the long one reaches p
+    dict(vecs=[_lib.CAdamwVec(300, BASE + 4096, BASE, BASE + 6144, BASE + 9600, None, None, 0, 0),
+               _lib.CAdamwVec(4, BASE + 1100, BASE + 16, BASE + 1536, BASE + 1792, None, None, 0, 0)]),
+    dict(vecs=[_vec()], clip=BASE + 2048 + 60),
+    dict(vecs=[_vec()], step_dev=BASE + 4),
+    dict(vecs=[_vec(n=1)], hp=_hp(bc1=BASE + 2048 - 16)),      # entry t_max of a table is the first of m
+    dict(vecs=[_vec(n=1)], hp=_hp(bc2=BASE + 3328)),
+])
+def test_adamw_refuses_inputs_inside_what_it_writes(what):
+    assert _adamw(**what) == _lib.SFT_EINVAL
+    assert b"overlap" in _lib.lib().sft_last_error()
