@@ -830,18 +830,18 @@ size_t sft_grad_clip_workspace(const sft_grad_vec *vecs, int32_t n_vecs);
  * sft_adamw leaves the step out; sft_coupled_update takes the step with that
  * gradient as zero.
  *   clip      device float, 4-byte aligned
- *   norm      device float, 4-byte aligned, or NULL
+ *   norm      device float, 4-byte aligned, apart from clip, or NULL
  *   max_norm  positive; infinity measures only (clip = 1 for a finite norm)
  *   ws        device scratch of at least sft_grad_clip_workspace() bytes
- *             (16-byte aligned; no initialisation needed); calls sharing it
- *             must be ordered on one stream
+ *             (16-byte aligned, apart from the gradients; no initialisation
+ *             needed); calls sharing it must be ordered on one stream
  * Summed in fp64 in a fixed order: deterministic, and no square of a float
  * overflows; a norm beyond the range of a float is written as infinity, with
  * the factor that it asks for.  An empty list has norm 0 and clip 1.
  * Errors: SFT_EINVAL (null pointers, negative sizes, bad type, max_norm not
- * positive), SFT_EALIGN, SFT_ECAPACITY (workspace too small), SFT_ENOTSUP
- * (2^42 values in a vector, or 2^31 chunks of 8192 values in a launch),
- * SFT_EHIP.
+ * positive, arrays that overlap), SFT_EALIGN, SFT_ECAPACITY (workspace too
+ * small), SFT_ENOTSUP (2^42 values in a vector, or 2^31 chunks of 8192 values
+ * in a launch), SFT_EHIP.
  */
 int sft_grad_clip(const sft_grad_vec *vecs, int32_t n_vecs, float max_norm, float *clip, float *norm, void *ws,
                   size_t ws_bytes, void *stream);

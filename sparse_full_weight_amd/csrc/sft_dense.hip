@@ -642,6 +642,13 @@ int grad_clip(const sft_grad_vec *vecs, int32_t n_vecs, float max_norm, float *c
     SFT_CHECK(ws_bytes >= need, SFT_ECAPACITY, "sft_grad_clip: workspace %zu < %zu bytes", ws_bytes, need);
     SFT_CHECK(need == 0 || ws, SFT_EINVAL, "sft_grad_clip: workspace is null");
     SFT_CHECK(sft::aligned16(ws), SFT_EALIGN, "sft_grad_clip: workspace not 16-byte aligned");
+    SFT_CHECK(clip != norm, SFT_EINVAL, "sft_grad_clip: clip and norm overlap");
+    const uint8_t *const lo = static_cast<const uint8_t *>(ws);
+    for (int32_t i = 0; i < n_vecs; ++i) {
+        const uint8_t *const g = static_cast<const uint8_t *>(vecs[i].grad);
+        SFT_CHECK(vecs[i].n == 0 || g + vecs[i].n * int64_t(type_size(vecs[i].type)) <= lo || lo + need <= g, SFT_EINVAL,
+                  "sft_grad_clip: vector %d and the workspace overlap", i);
+    }
     const hipStream_t st = static_cast<hipStream_t>(stream);
     double *part = static_cast<double *>(ws);
     int32_t parts = 0;

@@ -135,3 +135,21 @@ def test_adam_refuses_bias_tables_that_do_not_fit(bc1, bc2, error):
 def test_adamw_refuses_inputs_inside_what_it_writes(what):
     assert _adamw(**what) == _lib.SFT_EINVAL
     assert b"overlap" in _lib.lib().sft_last_error()
+
+
+@pytest.mark.parametrize("what", [
+    dict(vecs=[_lib.CGradVec(8, BASE, 0)], norm=BASE + 8192),                 # the factor's own place
+    dict(vecs=[_lib.CGradVec(8, BASE + 4096, 0)]),                             # the gradient where the sums go
+    dict(vecs=[_lib.CGradVec(8, BASE, 0), _lib.CGradVec(8, BASE + 4096 + 8, 1)]),
+    dict(vecs=[_lib.CGradVec(1 + 1024, BASE, 0)]),
+    dict(vecs=[]) | dict(norm=BASE + 8192),
+])
+def test_grad_clip_refuses_arrays_that_overlap(what):
+    assert _clip(**what) == _lib.SFT_EINVAL
+    assert b"overlap" in _lib.lib().sft_last_error()
+
+
+def test_grad_clip_workspace_may_follow_a_gradient():
+    # no byte shared: not refused for it (a workspace too small is looked at first)
+    assert _clip([_lib.CGradVec(1024, BASE, 0)], ws_bytes=0) == _lib.SFT_ECAPACITY
+    assert _clip([_lib.CGradVec(8, BASE, 0)], ws=BASE + 32, norm=BASE + 8194) == _lib.SFT_EALIGN
