@@ -787,8 +787,9 @@ enum { SFT_F32 = 0, SFT_BF16 = 1 };
  * Limits: R and C multiples of 8 and at most 2^20, T < 2^30, E <= 65536,
  * fewer than 2^24 output tiles (of 64 x 64 to 256 x 256).  What a call writes
  * must not overlap what it reads.
- * Errors: SFT_EINVAL (null pointers, negative sizes, bad out_type),
- * SFT_ESHAPE (R or C), SFT_EALIGN, SFT_ENOTSUP (beyond the limits), SFT_EHIP.
+ * Errors: SFT_EINVAL (null pointers, negative sizes, bad out_type, results
+ * that overlap an input), SFT_ESHAPE (R or C), SFT_EALIGN, SFT_ENOTSUP (beyond
+ * the limits), SFT_EHIP.
  */
 
 /* Y[t, r] = sum_c X[t, c] * W_e[r, c], Y [T x R] of out_type. */

@@ -630,6 +630,20 @@ int64_t tiles_of(const ExpertParams &p, int64_t kM, int64_t kN) {
     return m * ((N + kN - 1) / kN);
 }
 
+// Whether the results share bytes with an array that other workgroups may
+// still read.
+template <int kOp>
+bool writes_an_input(const ExpertParams &p, int32_t out_type) {
+    const auto meet = [](const void *x, int64_t nx, const void *y, int64_t ny) {
+        const uint8_t *a = static_cast<const uint8_t *>(x), *b = static_cast<const uint8_t *>(y);
+        return nx && ny && a < b + ny && b < a + nx;
+    };
+    const int64_t W = int64_t(p.E) * p.R * p.C;
+    const int64_t out = (kOp == kForward ? p.T * p.R : kOp == kDx ? p.T * p.C : W) * (out_type == SFT_F32 ? 4 : 2);
+    return meet(p.out, out, p.a, 2 * p.T * (kOp == kForward ? p.C : p.R)) ||
+           meet(p.out, out, p.b, 2 * (kOp == kDw ? p.T * p.C : W)) || meet(p.out, out, p.first, 4 * (int64_t(p.E) + 1));
+}
+
 template <int kOp, class S>
 int launch(const char *who, ExpertParams p, int32_t out_type, bool add, hipStream_t st) {
     p.cus = sft::num_cus();
@@ -640,6 +654,7 @@ int launch(const char *who, ExpertParams p, int32_t out_type, bool add, hipStrea
     const int64_t run = 8 * int64_t(p.chunk), groups = (units + run - 1) / run * run;
     // a launch has fewer than 2^32 threads
     SFT_CHECK(groups < (int64_t(1) << 32) / kThreads, SFT_ENOTSUP, "%s: 2^24 output tiles or more", who);
+    SFT_CHECK(!writes_an_input<kOp>(p, out_type), SFT_EINVAL, "%s: the results overlap an input", who);
     const dim3 grid(static_cast<uint32_t>(groups)), block(kThreads);
     if (out_type == SFT_BF16)
         hipLaunchKernelGGL((k_expert<kOp, S, uint16_t, false>), grid, block, 0, st, p);

@@ -48,3 +48,20 @@ def test_dw_accumulates_only_fp32():
 def test_nothing_to_write_is_nothing(op, empty):
     for name in empty:
         assert _call(op, **{name: 0}, first=None, a=None, b=None, out=None) == _lib.SFT_OK
+
+
+# bytes of the arrays at E = 2, T = 4, R = 8, C = 16 with fp32 results
+BYTES = {"forward": dict(first=12, a=128, b=512, out=128), "dx": dict(first=12, a=64, b=512, out=256),
+         "dw": dict(first=12, a=64, b=128, out=1024)}
+
+
+@pytest.mark.parametrize("op", ["forward", "dx", "dw"])
+@pytest.mark.parametrize("which", ["first", "a", "b"])
+@pytest.mark.parametrize("end", ["the results' first bytes", "the results' last bytes"])
+def test_refuses_results_over_an_input(op, which, end):
+    size = BYTES[op]
+    k = dict(T=4, first=BASE + 256, a=BASE + 512, b=BASE + 1024, out=BASE + 2048)
+    k[which] = k["out"] + (16 - (size[which] + 15) // 16 * 16 if "first" in end else size["out"] - 16)
+    assert k[which] < k["out"] + size["out"] and k["out"] < k[which] + size[which]
+    assert _call(op, **k) == _lib.SFT_EINVAL
+    assert b"overlap" in _lib.lib().sft_last_error()

@@ -415,3 +415,29 @@ def test_gradients_agree_with_differences(gpu_lib, op):
         change, got = loss(X, other) - loss(X, W), (grad.double() * (other.double() - W.double())).sum().item()
     # both sides are sums of T*R*C products in fp32 pieces of at most 72 terms
     assert abs(change - got) <= 4 * (72 + 4) * U * T * R * C ** 0.5 * 4
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_arrays_behind_one_another(gpu_lib, op):
+    # the results between the inputs of one buffer, not a byte apart
+    counts, R, C = [3, 0, 9, 2, 2], 24, 40
+    E, T = len(counts), sum(counts)
+    X, dY, W = _normal((T, C), 1.0, 1), _normal((T, R), 0.1, 2), _normal((E, R, C), 0.1, 3)
+    first = torch.cat([_first(counts), torch.zeros(2, dtype=torch.int32, device="cuda")])     # 32 bytes
+    a, b = {"forward": (X, W), "dx": (dY, W), "dw": (dY, X)}[op]
+    shape = {"forward": (T, R), "dx": (T, C), "dw": (E, R, C)}[op]
+    out = torch.full(shape, MARK, device="cuda")
+    parts = [x.reshape(-1).view(torch.uint8) for x in (first, a, out, b)]
+    whole = torch.cat(parts)
+    at = np.cumsum([0] + [p.numel() for p in parts])
+    f, a1, o, b1 = (whole[at[i]:at[i + 1]].view(t).view(s) for i, (t, s) in enumerate(
+        ((torch.int32, (E + 3,)), (BF16, a.shape), (F32, shape), (BF16, b.shape))))
+    {"forward": _lib.sft_expert_forward, "dx": _lib.sft_expert_dx, "dw": _lib.sft_expert_dw}[op](f[:E + 1], a1, b1, o)
+    assert torch.equal(a1, a) and torch.equal(b1, b)
+    bounds = first.tolist()
+    for e in range(E):
+        lo, hi = bounds[e], bounds[e + 1]
+        if op == "dw":
+            _check(o[e], dY[lo:hi].t(), X[lo:hi], "dW")
+        else:
+            _check(o[lo:hi], a[lo:hi], W[e].t() if op == "forward" else W[e], op)
