@@ -87,7 +87,7 @@
 extern "C" {
 #endif
 
-#define SFT_ABI_VERSION 15
+#define SFT_ABI_VERSION 16
 
 enum {
     SFT_OK = 0,

@@ -51,6 +51,16 @@ int sft_probe_mfma(int64_t iters, float *out, void *stream);
  */
 int sft_probe_dw_plan(const sft_dw_group *groups, int32_t n_groups, int32_t cus, int32_t *out, int32_t cap);
 
+/*
+ * Which tiles a product grouped by expert would take for these sizes (host
+ * only).  op: 0 sft_expert_forward, 1 sft_expert_dx, 2 sft_expert_dw; cus as
+ * above.  Writes four values: rows and columns of a tile, the summed
+ * axis of a stage, and the stages in LDS.
+ * Errors: SFT_EINVAL (bad arguments, or a call that would launch nothing),
+ * SFT_ESHAPE, SFT_ENOTSUP, as the call itself.
+ */
+int sft_probe_expert_tiles(int32_t op, int64_t E, int64_t T, int64_t R, int64_t C, int32_t cus, int32_t *out);
+
 #ifdef __cplusplus
 }
 #endif

@@ -37,7 +37,7 @@ EXPORTS = (
     "sft_helix_coupling", "sft_probe_grid", "sft_probe_read", "sft_probe_copy", "sft_probe_mfma", "sft_probe_dw_plan",
     "sft_noalloc_scratch_bytes", "sft_masked_dw_update_noalloc", "sft_plan_layer_words", "sft_plan_layer",
     "sft_plan_upload", "sft_grad_clip_workspace", "sft_grad_clip", "sft_adamw",
-    "sft_expert_forward", "sft_expert_dx", "sft_expert_dw",
+    "sft_expert_forward", "sft_expert_dx", "sft_expert_dw", "sft_probe_expert_tiles",
 )
 
 
@@ -203,6 +203,7 @@ def lib() -> C.CDLL:
         L.sft_probe_copy.argtypes = [p, p, C.c_size_t, p]
         L.sft_probe_mfma.argtypes = [i64, p, p]
         L.sft_probe_dw_plan.argtypes = [C.POINTER(CDwGroup), i32, i32, p, i32]
+        L.sft_probe_expert_tiles.argtypes = [i32, i64, i64, i64, i64, i32, p]
         L.sft_helix_init.argtypes = [C.POINTER(CHelix)]
         L.sft_helix_step.argtypes = [C.POINTER(CHelix), C.c_double, i32, C.POINTER(C.c_int32),
                                      C.POINTER(C.c_double)]
@@ -1232,3 +1233,14 @@ def sft_probe_dw_plan(groups, cus: int = 0) -> list:
                     "groups": [tuple(v[i + 3 * g:i + 3 * g + 3]) for g in range(ng)]})
         i += 3 * ng
     return res
+
+
+EXPERT_OPS = ("forward", "dx", "dw")
+
+
+def sft_probe_expert_tiles(op: str, E: int, T: int, R: int, Cc: int, cus: int = 0) -> tuple:
+    """Which tiles sft_expert_<op> would take for these sizes (no device work):
+    (rows, columns, summed axis of a stage, stages)."""
+    out = np.zeros(4, np.int32)
+    _check(lib().sft_probe_expert_tiles(EXPERT_OPS.index(op), E, T, R, Cc, cus, _np_ptr(out)))
+    return tuple(out.tolist())

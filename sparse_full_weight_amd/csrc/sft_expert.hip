@@ -20,6 +20,7 @@
 #include <type_traits>
 
 #include "sft_internal.h"
+#include "sft_probe.h"
 
 namespace {
 
@@ -300,6 +301,14 @@ struct Shape {
     static constexpr int kM = M_, kN = N_, kBK = BK_, kStages = STAGES_;
     static constexpr int kLds = (kM + kN) * kBK * 2 * kStages;
     static constexpr int kPerCu = 160 * 1024 / kLds < 4 ? 160 * 1024 / kLds : 4;
+};
+// The same as values.
+struct ShapeOf {
+    int m, n, k, stages;
+    template <class S>
+    bool is() const {
+        return m == S::kM && n == S::kN && k == S::kBK && stages == S::kStages;
+    }
 };
 
 // BM x BN from (m0, n0) on of expert t.e's product, by 2 x 2 waves, each
@@ -701,28 +710,22 @@ int launch(const char *who, ExpertParams p, int32_t out_type, bool add, hipStrea
 //     ring keeps loads in flight (the same 17.0, four stages 19.1; 12 x 1000 x
 //     520 at 1003 tokens, of two tiles a CU and short sums, 9.3 and 8.9)
 template <int kOp>
-int product(const char *who, const ExpertParams &p, int32_t out_type, bool add, void *stream) {
-    const hipStream_t st = static_cast<hipStream_t>(stream);
-    [[maybe_unused]] const int64_t cus = sft::num_cus();
+ShapeOf shape_for(const ExpertParams &p, int64_t cus) {
     // rounds of workgroups, two a CU, that so many tiles take
     [[maybe_unused]] const auto rounds = [cus](int64_t tiles) { return (tiles + 2 * cus - 1) / (2 * cus); };
     if constexpr (kOp == kDw) {
-        if (tiles_of<kOp>(p, 128, 256) >= 256)
-            return launch<kOp, Shape<128, 256, 32, 3>>(who, p, out_type, add, st);
-        if (tiles_of<kOp>(p, 128, 128) >= 256)
-            return launch<kOp, Shape<128, 128, 64, 2>>(who, p, out_type, add, st);
+        if (tiles_of<kOp>(p, 128, 256) >= 256) return {128, 256, 32, 3};
+        if (tiles_of<kOp>(p, 128, 128) >= 256) return {128, 128, 64, 2};
     } else {
         const int64_t rows = p.T / p.E;      // of an expert on average
         const int64_t K = kOp == kForward ? p.C : p.R;
         if constexpr (kOp == kForward) {
-            if (rows >= 512 && tiles_of<kOp>(p, 256, 256) >= 1024)
-                return launch<kOp, Shape<256, 256, 64, 2>>(who, p, out_type, add, st);
+            if (rows >= 512 && tiles_of<kOp>(p, 256, 256) >= 1024) return {256, 256, 64, 2};
             if (rows >= 96 && rows <= 192 && tiles_of<kOp>(p, 128, 128) >= 512 &&
                 2 * rounds(tiles_of<kOp>(p, 128, 128)) <= 3 * rounds(tiles_of<kOp>(p, 128, 192)))
-                return launch<kOp, Shape<128, 128, 64, 2>>(who, p, out_type, add, st);
+                return {128, 128, 64, 2};
         } else {
-            if (p.R >= 4096 && tiles_of<kOp>(p, 256, 256) >= 128)
-                return launch<kOp, Shape<256, 256, 32, 4>>(who, p, out_type, add, st);
+            if (p.R >= 4096 && tiles_of<kOp>(p, 256, 256) >= 128) return {256, 256, 32, 4};
         }
         if (tiles_of<kOp>(p, 128, 192) >= 320 && (kOp == kDx || rows >= 48)) {
             // rounds times a tile's width; an expert has one tile a column, or
@@ -732,20 +735,42 @@ int product(const char *who, const ExpertParams &p, int32_t out_type, bool add, 
             const int64_t N = kOp == kForward ? p.R : p.C;
             const int64_t high = p.E * (rows < 96 ? 128 : rows + 32) / 128;
             const int64_t narrow = 2 * rounds(high * ((N + 127) / 128)), wide = 3 * rounds(high * ((N + 191) / 192));
-            if (rows >= 4 && (rows < 96 || rows > 192) && 10 * narrow <= 7 * wide)
-                return launch<kOp, Shape<128, 128, 64, 2>>(who, p, out_type, add, st);
-            return launch<kOp, Shape<128, 192, 64, 2>>(who, p, out_type, add, st);
+            if (rows >= 4 && (rows < 96 || rows > 192) && 10 * narrow <= 7 * wide) return {128, 128, 64, 2};
+            return {128, 192, 64, 2};
         }
-        if (tiles_of<kOp>(p, 64, 128) >= 256 && rows >= 128)
-            return launch<kOp, Shape<64, 128, 64, 2>>(who, p, out_type, add, st);
-        if (K <= 4096 && tiles_of<kOp>(p, 64, 64) > cus && tiles_of<kOp>(p, 64, 128) <= 2 * cus)
-            return launch<kOp, Shape<64, 128, 64, 3>>(who, p, out_type, add, st);
+        if (tiles_of<kOp>(p, 64, 128) >= 256 && rows >= 128) return {64, 128, 64, 2};
+        if (K <= 4096 && tiles_of<kOp>(p, 64, 64) > cus && tiles_of<kOp>(p, 64, 128) <= 2 * cus) return {64, 128, 64, 3};
     }
     if constexpr (kOp == kForward) {
-        if (p.C >= 2048 && tiles_of<kOp>(p, 64, 64) <= cus)
-            return launch<kOp, Shape<64, 64, 64, 5>>(who, p, out_type, add, st);
+        if (p.C >= 2048 && tiles_of<kOp>(p, 64, 64) <= cus) return {64, 64, 64, 5};
     }
-    return launch<kOp, Shape<64, 64, 64, 4>>(who, p, out_type, add, st);
+    return {64, 64, 64, 4};
+}
+
+// The one of these kernels that the rule chose.
+template <int kOp, class... S>
+int launch_one(const ShapeOf &shape, const char *who, const ExpertParams &p, int32_t out_type, bool add,
+               hipStream_t st) {
+    int rc = SFT_ENOTSUP;
+    (void)((shape.is<S>() && (rc = launch<kOp, S>(who, p, out_type, add, st), true)) || ...);
+    return rc;
+}
+
+template <int kOp>
+int product(const char *who, const ExpertParams &p, int32_t out_type, bool add, void *stream) {
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const ShapeOf shape = shape_for<kOp>(p, sft::num_cus());
+    if constexpr (kOp == kDw)
+        return launch_one<kOp, Shape<128, 256, 32, 3>, Shape<128, 128, 64, 2>, Shape<64, 64, 64, 4>>(shape, who, p, out_type,
+                                                                                                    add, st);
+    else if constexpr (kOp == kDx)
+        return launch_one<kOp, Shape<256, 256, 32, 4>, Shape<128, 192, 64, 2>, Shape<128, 128, 64, 2>,
+                          Shape<64, 128, 64, 2>, Shape<64, 128, 64, 3>, Shape<64, 64, 64, 4>>(shape, who, p, out_type,
+                                                                                             add, st);
+    else
+        return launch_one<kOp, Shape<256, 256, 64, 2>, Shape<128, 192, 64, 2>, Shape<128, 128, 64, 2>,
+                          Shape<64, 128, 64, 2>, Shape<64, 128, 64, 3>, Shape<64, 64, 64, 5>, Shape<64, 64, 64, 4>>(
+            shape, who, p, out_type, add, st);
 }
 
 }  // namespace
@@ -782,6 +807,21 @@ int sft_expert_dw(int64_t E, int64_t T, int64_t R, int64_t C, const int32_t *fir
     if (E == 0 || R == 0 || C == 0) return SFT_OK;
     return product<kDw>("sft_expert_dw", ExpertParams{dY, X, dW, first, T, R, C, int32_t(E), 0, 0}, out_type,
                         accumulate != 0, stream);
+}
+
+int sft_probe_expert_tiles(int32_t op, int64_t E, int64_t T, int64_t R, int64_t C, int32_t cus, int32_t *out) {
+    sft::clear_error();
+    SFT_CHECK(op >= kForward && op <= kDw && cus >= 0 && out, SFT_EINVAL, "sft_probe_expert_tiles: bad arguments");
+    if (int rc = check("sft_probe_expert_tiles", E, T, R, C, nullptr, nullptr, false, nullptr, false, nullptr, false,
+                       SFT_F32))
+        return rc;
+    SFT_CHECK(E && R && C && (T || op == kDw), SFT_EINVAL, "sft_probe_expert_tiles: nothing to launch");
+    const ExpertParams p{nullptr, nullptr, nullptr, nullptr, T, R, C, int32_t(E), 0, 0};
+    const int64_t n = cus ? cus : sft::num_cus();
+    const ShapeOf s = op == kForward ? shape_for<kForward>(p, n) : op == kDx ? shape_for<kDx>(p, n)
+                                                                            : shape_for<kDw>(p, n);
+    out[0] = s.m, out[1] = s.n, out[2] = s.k, out[3] = s.stages;
+    return SFT_OK;
 }
 
 }  // extern "C"

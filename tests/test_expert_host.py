@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 
 from sparse_full_weight_amd import _lib
+from tests import expert_shapes
 
 BUF = np.zeros(1 << 12, np.uint8)
 BASE = (BUF.ctypes.data + 255) // 256 * 256
@@ -65,3 +66,42 @@ def test_refuses_results_over_an_input(op, which, end):
     assert k[which] < k["out"] + size["out"] and k["out"] < k[which] + size[which]
     assert _call(op, **k) == _lib.SFT_EINVAL
     assert b"overlap" in _lib.lib().sft_last_error()
+
+
+@pytest.mark.parametrize("op,counts,R,C,shape", expert_shapes.CASES)
+def test_sizes_of_the_gpu_tests_take_the_shapes_they_name(op, counts, R, C, shape):
+    for more in (0, expert_shapes.AROUND):
+        assert _lib.sft_probe_expert_tiles(op, len(counts), sum(counts) + more, R, C, 256) == shape
+
+
+def test_every_shape_has_a_size():
+    for op, shapes in expert_shapes.SHAPES.items():
+        assert {c[4] for c in expert_shapes.CASES if c[0] == op} == shapes
+    # and the last launch round of the largest tiles comes whole and in halves
+    for cases in (expert_shapes.FORWARD, expert_shapes.DX):
+        assert {expert_shapes.halved(*c) for c in cases if c[4][0] == 256} == {True, False}
+
+
+def test_no_size_takes_a_shape_without_a_kernel():
+    # the choice over many sizes stays within the shapes that are tested
+    rs = np.random.RandomState(0)
+    seen = {op: set() for op in expert_shapes.SHAPES}
+    for _ in range(6000):
+        E, T = int(2 ** rs.uniform(0, 10)), int(2 ** rs.uniform(0, 18))
+        R, C = (8 * int(2 ** rs.uniform(0, 12)) for _ in range(2))
+        for op in seen:
+            try:
+                seen[op].add(_lib.sft_probe_expert_tiles(op, E, T, R, C, int(rs.choice([64, 256, 304]))))
+            except _lib.SftError as e:
+                assert e.code == _lib.SFT_ENOTSUP
+    assert seen == expert_shapes.SHAPES
+
+
+@pytest.mark.parametrize("args,code", [
+    ((3, 1, 1, 8, 8, 0), _lib.SFT_EINVAL), ((-1, 1, 1, 8, 8, 0), _lib.SFT_EINVAL), ((0, 1, 1, 8, 8, -1), _lib.SFT_EINVAL),
+    ((0, 0, 1, 8, 8, 0), _lib.SFT_EINVAL), ((1, 1, 0, 8, 8, 0), _lib.SFT_EINVAL), ((0, 1, 1, 12, 8, 0), _lib.SFT_ESHAPE),
+    ((0, 1, 1 << 30, 8, 8, 0), _lib.SFT_ENOTSUP)])
+def test_probe_of_the_tiles_refuses(args, code):
+    out = np.zeros(4, np.int32)
+    assert _lib.lib().sft_probe_expert_tiles(*args, out.ctypes.data) == code
+    assert _lib.lib().sft_probe_expert_tiles(0, 1, 1, 8, 8, 0, None) == _lib.SFT_EINVAL

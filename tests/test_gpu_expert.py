@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from sparse_full_weight_amd import _lib
+from tests import expert_shapes
 from tests.gpu_helpers import adam_dev
 
 pytestmark = pytest.mark.gpu
@@ -441,3 +442,12 @@ def test_arrays_behind_one_another(gpu_lib, op):
             _check(o[e], dY[lo:hi].t(), X[lo:hi], "dW")
         else:
             _check(o[lo:hi], a[lo:hi], W[e].t() if op == "forward" else W[e], op)
+
+
+@pytest.mark.parametrize("op,counts,R,C,shape", expert_shapes.CASES)
+def test_the_shape_that_the_sizes_name(gpu_lib, op, counts, R, C, shape):
+    for more in (0, expert_shapes.AROUND):
+        assert _lib.sft_probe_expert_tiles(op, len(counts), sum(counts) + more, R, C) == shape
+    _run(op, counts, R, C, F32, start=1, behind=expert_shapes.AROUND - 1)
+    _run(op, counts, R, C, F32, integer=True, seed=10)
+    _run(op, counts, R, C, BF16, start=2, behind=expert_shapes.AROUND - 2, seed=20)
