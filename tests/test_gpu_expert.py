@@ -451,3 +451,41 @@ def test_the_shape_that_the_sizes_name(gpu_lib, op, counts, R, C, shape):
     _run(op, counts, R, C, F32, start=1, behind=expert_shapes.AROUND - 1)
     _run(op, counts, R, C, F32, integer=True, seed=10)
     _run(op, counts, R, C, BF16, start=2, behind=expert_shapes.AROUND - 2, seed=20)
+
+
+@pytest.mark.parametrize("counts,R,C,shape", [c[1:] for c in expert_shapes.DW])
+@pytest.mark.parametrize("shift", [0, 4])
+def test_dw_accumulates_on_every_shape(gpu_lib, counts, R, C, shape, shift):
+    # whole numbers throughout, so that every sum is exact whatever its order: old values that were read from another
+    # place, late or twice would show.  Rows of whole cache lines (old values read ahead, results past L2) and others;
+    # with the array 16 bytes behind a line no row starts on one.  Rows of experts without tokens stay as they were.
+    E, T = len(counts), sum(counts)
+    assert _lib.sft_probe_expert_tiles("dw", E, T, R, C) == shape
+    first = _first(counts)
+    X, dY = ((_normal((T, n), 1.0, i) * 2).round().clamp(-3, 3) for i, n in ((1, C), (2, R)))
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    whole = torch.randint(-100000, 100000, (E * R * C + 64,), generator=gen, device="cuda").float()
+    before = whole.clone()
+    D, old = (x[shift:shift + E * R * C].view(E, R, C) for x in (whole, before))
+    assert D.data_ptr() % 128 == 4 * shift
+    for turn in (1, 2):                                          # and once more onto the sums
+        _lib.sft_expert_dw(first, dY, X, D, accumulate=True)
+        for e, (lo, hi) in enumerate(zip(first.tolist(), first.tolist()[1:])):
+            assert torch.equal(D[e].double(), old[e].double() + turn * (dY[lo:hi].double().t() @ X[lo:hi].double()))
+    assert torch.equal(whole[:shift], before[:shift])
+    assert torch.equal(whole[shift + E * R * C:], before[shift + E * R * C:])
+
+
+@pytest.mark.parametrize("counts,R,C,shape", [c[1:] for c in expert_shapes.DW])
+def test_dw_accumulates_ordinary_values(gpu_lib, counts, R, C, shape):
+    # fp32 sums of exact products, then one addition to the old value, rounded: (rows + 5) U of the magnitudes
+    T = sum(counts)
+    first, X, dY = _first(counts), _normal((T, C), 1.0, 1), _normal((T, R), 0.1, 2)
+    D = torch.randn((len(counts), R, C), device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
+    old = D.clone()
+    _lib.sft_expert_dw(first, dY, X, D, accumulate=True)
+    for e, (lo, hi) in enumerate(zip(first.tolist(), first.tolist()[1:])):
+        a, b = dY[lo:hi].t().double(), X[lo:hi].double()
+        bound = (hi - lo + 5) * U * (a.abs() @ b.abs() + old[e].abs().double())
+        assert bool(((D[e].double() - (old[e].double() + a @ b)).abs() <= bound).all())
+        assert hi > lo or torch.equal(D[e], old[e])
