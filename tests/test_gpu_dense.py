@@ -399,3 +399,51 @@ def test_adamw_python_refuses(gpu_lib, wrong):
         clip = torch.ones(2, device="cuda")
     with pytest.raises((TypeError, ValueError)):
         _lib.sft_adamw([_lib.AdamwVec(p, g, m, v, scale)], 1, adam_dev(), clip=clip)
+
+
+def check_8_bit_step(vec, before, g, step, hp, clip, what):
+    """One step of 8-bit states against the formula: before = (p, m, sqrt(v)) in fp64 on the host, g the gradient (fp32
+    values, fp64), clip as the kernel read it (an fp32 number)."""
+    p, m, root = (x.reshape(-1) for x in before)
+    g = g.reshape(-1)
+    want, bound = _formula(p, g, m, root * root, step, hp, clip)
+    _close(vec.p.view(-1), want[0], bound[0], "p " + what, vec.p.dtype)
+    if vec.p_live is not None:
+        _close(vec.p_live.view(-1), want[0], bound[0], "live " + what, BF16)
+    # the same fp32 arithmetic on the host gives the same scales and codes
+    f = np.float32
+    g32, m32, r32 = (x.float().numpy() for x in (g, m, root))
+    g32 = g32 * f(clip)
+    m1 = f(hp["beta1"]) * m32 + (f(1) - f(hp["beta1"])) * g32
+    r1 = np.sqrt(f(hp["beta2"]) * (r32 * r32) + (f(1) - f(hp["beta2"])) * (g32 * g32))
+    for x, code, turn, least, col in ((m1, vec.m, 0x55555555, False, 0), (r1, vec.v, 0, True, 1)):
+        y, k, unit, near = _codes(torch.from_numpy(np.abs(x)), step, turn, least)
+        assert torch.equal(vec.scale[:, col].float().cpu().double(), torch.exp2(k)), what
+        got = code.view(-1).float().cpu().double()
+        off = (got.abs() - y).abs()
+        assert bool(((off == 0) | (near & (off <= 2 * unit))).all()), what
+        assert int(near.sum()) <= 1 + g32.size // 100
+        assert bool(((got == 0) | (torch.signbit(got) == torch.from_numpy(np.signbit(x)))).all()), what
+
+
+def before_8_bit_step(vec):
+    return (vec.p.double().cpu(), *_decode(vec.m.view(-1), vec.v.view(-1), vec.scale))
+
+
+@pytest.mark.parametrize("p_type,g_type", [(F32, F32), (BF16, BF16)])
+@pytest.mark.parametrize("on_device", [False, True])
+@pytest.mark.parametrize("clip", [1.0, 0.375, 0.1, 2.0 ** -30])
+def test_adamw_8_bit_states_with_a_clip_factor(gpu_lib, p_type, g_type, on_device, clip):
+    sizes = [1, 257, 4096, 9003]
+    vecs = []
+    for i, n in enumerate(sizes):
+        p, g = _normal(n, 0.5, 10 + i, p_type).cuda(), _normal(n, 0.1, 50 + i, g_type).cuda()
+        vecs.append(_lib.AdamwVec.alloc8(p, g, torch.zeros(n, dtype=BF16, device="cuda") if i % 2 else None))
+    hp, factor = adam_dev(**HP), torch.full((1,), clip, device="cuda")
+    step = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for t in (1, 2, 6):
+        before = [before_8_bit_step(v) for v in vecs]
+        step.fill_(t)
+        _lib.sft_adamw(vecs, step if on_device else t, hp, clip=factor)
+        for n, vec, b in zip(sizes, vecs, before):
+            check_8_bit_step(vec, b, vec.grad.double().cpu(), t, HP, factor.item(), f"of {n} at step {t}")

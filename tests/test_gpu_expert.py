@@ -8,6 +8,7 @@ import torch
 from sparse_full_weight_amd import _lib
 from tests import expert_shapes
 from tests.gpu_helpers import adam_dev
+from tests.test_gpu_dense import before_8_bit_step, check_8_bit_step
 
 pytestmark = pytest.mark.gpu
 
@@ -489,3 +490,36 @@ def test_dw_accumulates_ordinary_values(gpu_lib, counts, R, C, shape):
         bound = (hi - lo + 5) * U * (a.abs() @ b.abs() + old[e].abs().double())
         assert bool(((D[e].double() - (old[e].double() + a @ b)).abs() <= bound).all())
         assert hi > lo or torch.equal(D[e], old[e])
+
+
+def test_captured_8_bit_steps_of_an_expert_layer(gpu_lib):
+    # the clipped 8-bit update behind an expert layer's gradients, captured once: every replay's weights, scales and
+    # codes against the formula at that step's number, factor and gradient
+    hp = dict(lr=1e-2, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.1)
+    E, T, R, C = 5, 300, 136, 200
+    X, dY, W = _normal((T, C), 1.0, 1), _normal((T, R), 0.1, 2), _normal((E, R, C), 0.1, 3)
+    first, p = _first([0] * E), W.float()
+    Y, dX, dW = (torch.zeros(s, dtype=t, device="cuda") for s, t in (((T, R), BF16), ((T, C), BF16), ((E, R, C), F32)))
+    vec = _lib.AdamwVec.alloc8(p, dW, W)
+    clip, norm = torch.zeros(1, device="cuda"), torch.zeros(1, device="cuda")
+    ws = torch.empty(_lib.sft_grad_clip_workspace([dW]), dtype=torch.uint8, device="cuda")
+    step = torch.zeros(1, dtype=torch.int32, device="cuda")
+    calls = _layer_step(first, X, W, dY, p, vec, adam_dev(**hp), ws, clip, norm, Y, dX, dW, step)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step += 1
+        for c in calls:
+            c()
+    rs = np.random.RandomState(0)
+    for t in range(1, 6):
+        first.copy_(_first(rs.multinomial(T - 7, rs.dirichlet(np.ones(E)))))
+        X.copy_(_normal((T, C), 1.0, 10 * t))
+        dY.copy_(_normal((T, R), 0.1, 10 * t + 1))
+        before = before_8_bit_step(vec)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert step.item() == t and 0.0 < clip.item() < 1.0
+        check_8_bit_step(vec, before, dW.double().cpu(), t, hp, clip.item(), f"at step {t}")
+        assert not torch.equal(p.double().cpu(), before[0])
