@@ -295,19 +295,24 @@ __device__ __forceinline__ void put(V *p, V v) {
 constexpr int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
 // A kernel's tiles: kM x kN, by stages of kBK along k, kStages of them in LDS;
-// kPerCu workgroups share a CU.
+// per_cu workgroups share a CU.
+constexpr int per_cu(int m, int n, int k, int stages) {
+    const int fit = 160 * 1024 / ((m + n) * k * 2 * stages);
+    return fit < 4 ? fit : 4;
+}
 template <int M_, int N_, int BK_, int STAGES_>
 struct Shape {
     static constexpr int kM = M_, kN = N_, kBK = BK_, kStages = STAGES_;
-    static constexpr int kLds = (kM + kN) * kBK * 2 * kStages;
-    static constexpr int kPerCu = 160 * 1024 / kLds < 4 ? 160 * 1024 / kLds : 4;
+    static constexpr int kPerCu = per_cu(kM, kN, kBK, kStages);
 };
 // The same as values.
 struct ShapeOf {
     int m, n, k, stages;
+    int per_cu() const { return ::per_cu(m, n, k, stages); }
+    bool operator==(const ShapeOf &o) const { return m == o.m && n == o.n && k == o.k && stages == o.stages; }
     template <class S>
-    bool is() const {
-        return m == S::kM && n == S::kN && k == S::kBK && stages == S::kStages;
+    static ShapeOf of() {
+        return {S::kM, S::kN, S::kBK, S::kStages};
     }
 };
 
@@ -639,6 +644,19 @@ int64_t tiles_of(const ExpertParams &p, int64_t kM, int64_t kN) {
     return m * ((N + kN - 1) / kN);
 }
 
+// Workgroups of a launch (the XCDs' runs of units in p.chunk): fewer than 2^32
+// threads.
+constexpr int64_t kMaxGroups = (int64_t(1) << 32) / kThreads;
+template <int kOp>
+int64_t groups_of(const ExpertParams &p, const ShapeOf &s, int64_t cus, int32_t &chunk) {
+    const int64_t units = tiles_of<kOp>(p, s.m, s.n) + (kOp != kDw && s.per_cu() == 1 ? cus / 2 : 0);
+    // runs of a whole round of workgroups (per_cu() on each of an XCD's 32 CUs),
+    // fewer where the launch has less than a round
+    chunk = static_cast<int32_t>(std::min<int64_t>(32 * s.per_cu(), (units + 7) / 8));
+    const int64_t run = 8 * int64_t(chunk);
+    return (units + run - 1) / run * run;
+}
+
 // Whether the results share bytes with an array that other workgroups may
 // still read.
 template <int kOp>
@@ -656,13 +674,8 @@ bool writes_an_input(const ExpertParams &p, int32_t out_type) {
 template <int kOp, class S>
 int launch(const char *who, ExpertParams p, int32_t out_type, bool add, hipStream_t st) {
     p.cus = sft::num_cus();
-    const int64_t units = tiles_of<kOp>(p, S::kM, S::kN) + (kOp != kDw && S::kPerCu == 1 ? p.cus / 2 : 0);
-    // runs of a whole round of workgroups (kPerCu on each of an XCD's 32 CUs),
-    // fewer where the launch has less than a round
-    p.chunk = static_cast<int32_t>(std::min<int64_t>(32 * S::kPerCu, (units + 7) / 8));
-    const int64_t run = 8 * int64_t(p.chunk), groups = (units + run - 1) / run * run;
-    // a launch has fewer than 2^32 threads
-    SFT_CHECK(groups < (int64_t(1) << 32) / kThreads, SFT_ENOTSUP, "%s: 2^24 output tiles or more", who);
+    const int64_t groups = groups_of<kOp>(p, ShapeOf::of<S>(), p.cus, p.chunk);
+    SFT_CHECK(groups < kMaxGroups, SFT_ENOTSUP, "%s: 2^24 output tiles or more", who);
     SFT_CHECK(!writes_an_input<kOp>(p, out_type), SFT_EINVAL, "%s: the results overlap an input", who);
     const dim3 grid(static_cast<uint32_t>(groups)), block(kThreads);
     if (out_type == SFT_BF16)
@@ -710,7 +723,7 @@ int launch(const char *who, ExpertParams p, int32_t out_type, bool add, hipStrea
 //     ring keeps loads in flight (the same 17.0, four stages 19.1; 12 x 1000 x
 //     520 at 1003 tokens, of two tiles a CU and short sums, 9.3 and 8.9)
 template <int kOp>
-ShapeOf shape_for(const ExpertParams &p, int64_t cus) {
+ShapeOf shape_by_sizes(const ExpertParams &p, int64_t cus) {
     // rounds of workgroups, two a CU, that so many tiles take
     [[maybe_unused]] const auto rounds = [cus](int64_t tiles) { return (tiles + 2 * cus - 1) / (2 * cus); };
     if constexpr (kOp == kDw) {
@@ -747,12 +760,22 @@ ShapeOf shape_for(const ExpertParams &p, int64_t cus) {
     return {64, 64, 64, 4};
 }
 
+// The same, but where a launch does not hold so many tiles (one row on each of
+// 16384 experts of 65536 x 8: 17 million of 64 x 64), larger ones.
+template <int kOp>
+ShapeOf shape_for(const ExpertParams &p, int64_t cus) {
+    const ShapeOf s = shape_by_sizes<kOp>(p, cus);
+    int32_t chunk;
+    if (kOp != kDw && groups_of<kOp>(p, s, cus, chunk) >= kMaxGroups) return {128, 192, 64, 2};
+    return s;
+}
+
 // The one of these kernels that the rule chose.
 template <int kOp, class... S>
 int launch_one(const ShapeOf &shape, const char *who, const ExpertParams &p, int32_t out_type, bool add,
                hipStream_t st) {
     int rc = SFT_ENOTSUP;
-    (void)((shape.is<S>() && (rc = launch<kOp, S>(who, p, out_type, add, st), true)) || ...);
+    (void)((shape == ShapeOf::of<S>() && (rc = launch<kOp, S>(who, p, out_type, add, st), true)) || ...);
     return rc;
 }
 
@@ -818,8 +841,16 @@ int sft_probe_expert_tiles(int32_t op, int64_t E, int64_t T, int64_t R, int64_t 
     SFT_CHECK(E && R && C && (T || op == kDw), SFT_EINVAL, "sft_probe_expert_tiles: nothing to launch");
     const ExpertParams p{nullptr, nullptr, nullptr, nullptr, T, R, C, int32_t(E), 0, 0};
     const int64_t n = cus ? cus : sft::num_cus();
-    const ShapeOf s = op == kForward ? shape_for<kForward>(p, n) : op == kDx ? shape_for<kDx>(p, n)
-                                                                            : shape_for<kDw>(p, n);
+    ShapeOf s;
+    int64_t groups;
+    const auto look = [&](auto o) {
+        constexpr int kOp = decltype(o)::value;
+        int32_t chunk;
+        s = shape_for<kOp>(p, n);
+        groups = groups_of<kOp>(p, s, n, chunk);
+    };
+    op == kForward ? look(ic<kForward>{}) : op == kDx ? look(ic<kDx>{}) : look(ic<kDw>{});
+    SFT_CHECK(groups < kMaxGroups, SFT_ENOTSUP, "sft_probe_expert_tiles: 2^24 output tiles or more");
     out[0] = s.m, out[1] = s.n, out[2] = s.k, out[3] = s.stages;
     return SFT_OK;
 }

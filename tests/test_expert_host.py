@@ -105,3 +105,23 @@ def test_probe_of_the_tiles_refuses(args, code):
     out = np.zeros(4, np.int32)
     assert _lib.lib().sft_probe_expert_tiles(*args, out.ctypes.data) == code
     assert _lib.lib().sft_probe_expert_tiles(0, 1, 1, 8, 8, 0, None) == _lib.SFT_EINVAL
+
+
+@pytest.mark.parametrize("op,E,T,R,C,shape", [
+    # 2^24 tiles or more of the shape that the number of rows asks for, fewer of a larger one
+    ("forward", 16384, 16384, 65536, 8, (128, 192, 64, 2)), ("forward", 65536, 1 << 20, 16384, 8, (128, 192, 64, 2)),
+    ("forward", 8192, 1 << 20, 1 << 17, 8, (128, 192, 64, 2)),              # 128 x 128 for 128 rows on average
+    # fewer than 2^24 anyway
+    ("forward", 16384, 16384, 64000, 8, (64, 64, 64, 4)), ("dx", 16384, 16384, 8, 65536, (128, 192, 64, 2)),
+])
+def test_many_tiles_take_a_shape_that_fits_a_launch(op, E, T, R, C, shape):
+    assert _lib.sft_probe_expert_tiles(op, E, T, R, C, 256) == shape
+
+
+@pytest.mark.parametrize("op,E,T,R,C", [
+    ("forward", 65536, 1 << 20, 1 << 18, 8), ("dx", 65536, 1 << 20, 8, 1 << 18), ("dw", 65536, 1, 8, 65536)])
+def test_more_tiles_than_a_launch_has_workgroups(op, E, T, R, C):
+    with pytest.raises(_lib.SftError) as e:
+        _lib.sft_probe_expert_tiles(op, E, T, R, C, 256)
+    assert e.value.code == _lib.SFT_ENOTSUP
+    assert _call(op, E=E, T=T, R=R, C=C) == _lib.SFT_ENOTSUP

@@ -523,3 +523,16 @@ def test_captured_8_bit_steps_of_an_expert_layer(gpu_lib):
         assert step.item() == t and 0.0 < clip.item() < 1.0
         check_8_bit_step(vec, before, dW.double().cpu(), t, hp, clip.item(), f"at step {t}")
         assert not torch.equal(p.double().cpu(), before[0])
+
+
+def test_more_short_groups_than_a_launch_has_small_tiles(gpu_lib):
+    # one row on each of 16384 experts of 65536 x 8: 17 million tiles of 64 x 64, more than a launch has workgroups
+    E, R, C = 16384, 65536, 8
+    first = torch.arange(E + 1, dtype=torch.int32, device="cuda")
+    X, W = _normal((E, C), 1.0, 1), torch.empty((E, R, C), dtype=BF16, device="cuda")
+    W.normal_(0.0, 0.1, generator=torch.Generator(device="cuda").manual_seed(2))
+    Y = torch.full((E, R), float("nan"), dtype=BF16, device="cuda")
+    _lib.sft_expert_forward(first, X, W, Y)
+    assert not torch.isnan(Y).any()
+    for e in (0, 1, 63, 64, 8191, 16320, 16383):
+        _check(Y[e:e + 1], X[e:e + 1], W[e].t(), f"expert {e}")
