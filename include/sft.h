@@ -787,7 +787,8 @@ enum { SFT_F32 = 0, SFT_BF16 = 1 };
  * Limits: R and C multiples of 8 and at most 2^20, T < 2^30, E <= 65536,
  * fewer than 2^24 output tiles (of 128 x 192, T/128 + min(E, T) of them along
  * the tokens; 128 x 256 of every expert for dW).  What a call writes must not
- * overlap what it reads.
+ * overlap what it reads.  Every workgroup of the forward and of dX walks
+ * `first`: beyond about a thousand experts that takes longer than the products.
  * Errors: SFT_EINVAL (null pointers, negative sizes, bad out_type, results
  * that overlap an input), SFT_ESHAPE (R or C), SFT_EALIGN, SFT_ENOTSUP (beyond
  * the limits), SFT_EHIP.
