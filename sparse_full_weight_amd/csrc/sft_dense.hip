@@ -691,6 +691,7 @@ int adamw(const sft_adamw_vec *vecs, int32_t n_vecs, int32_t step, const int32_t
     SFT_CHECK(step_dev || step >= 1, SFT_EINVAL, "sft_adamw: step %d < 1", step);
     SFT_CHECK(aligned(step_dev, 4) && aligned(clip, 4), SFT_EALIGN, "sft_adamw: step_dev or clip not 4-byte aligned");
     int64_t chunks = 0;
+    const uint8_t *low = reinterpret_cast<const uint8_t *>(UINTPTR_MAX), *top = nullptr;    // of the gradients
     std::vector<Range> written;
     written.reserve(static_cast<size_t>(n_vecs) * 3);
     const auto writes = [&](const void *p, int64_t bytes) {
@@ -709,6 +710,9 @@ int adamw(const sft_adamw_vec *vecs, int32_t n_vecs, int32_t step, const int32_t
                       aligned(v.p_live, 2) && (v.scale || (aligned(v.m, 4) && aligned(v.v, 4))),
                   SFT_EALIGN, "sft_adamw: vector %d: a pointer is not aligned to its type", i);
         chunks += v.scale ? (v.n + kChunk8 - 1) / kChunk8 : (v.n + kChunk32 - 1) / kChunk32;
+        const uint8_t *const g = static_cast<const uint8_t *>(v.grad);
+        low = std::min(low, g);
+        top = std::max(top, g + v.n * int64_t(type_size(v.g_type)));
     }
     // a launch has fewer than 2^32 threads
     SFT_CHECK(chunks < (int64_t(1) << 32) / kThreads, SFT_ENOTSUP, "sft_adamw: 2^24 chunks of values or more");
@@ -725,11 +729,13 @@ int adamw(const sft_adamw_vec *vecs, int32_t n_vecs, int32_t step, const int32_t
             writes(vecs[i].p_live, vecs[i].n * 2);
         }
     SFT_CHECK(!overlap(written), SFT_EINVAL, "sft_adamw: two arrays that the step writes overlap");
-    // other workgroups may still read what one of them writes
+    // other workgroups may still read what one of them writes; gradients often
+    // share a buffer, so first from the lowest address to the highest
     size_t at = 0;
-    for (int32_t i = 0; i < n_vecs; ++i)
-        SFT_CHECK(vecs[i].n == 0 || !inside(written, vecs[i].grad, vecs[i].n * int64_t(type_size(vecs[i].g_type)), at),
-                  SFT_EINVAL, "sft_adamw: vector %d: the gradient overlaps an array that the step writes", i);
+    if (top > low && inside(written, low, top - low, at))
+        for (int32_t i = 0; i < n_vecs; ++i)
+            SFT_CHECK(vecs[i].n == 0 || !inside(written, vecs[i].grad, vecs[i].n * int64_t(type_size(vecs[i].g_type)), at),
+                      SFT_EINVAL, "sft_adamw: vector %d: the gradient overlaps an array that the step writes", i);
     const int64_t table = 4 * (int64_t(hp->t_max) + 1);
     SFT_CHECK(!inside(written, hp->bc1, table, at) && !inside(written, hp->bc2, table, at) &&
                   !(clip && inside(written, clip, 4, at)) && !(step_dev && inside(written, step_dev, 4, at)),
