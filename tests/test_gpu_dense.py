@@ -447,3 +447,49 @@ def test_adamw_8_bit_states_with_a_clip_factor(gpu_lib, p_type, g_type, on_devic
         _lib.sft_adamw(vecs, step if on_device else t, hp, clip=factor)
         for n, vec, b in zip(sizes, vecs, before):
             check_8_bit_step(vec, b, vec.grad.double().cpu(), t, HP, factor.item(), f"of {n} at step {t}")
+
+
+@pytest.mark.parametrize("held", [False, True])
+def test_arrays_behind_one_another_are_not_refused(gpu_lib, held):
+    # parameters, gradients and states of two tensors in turn in one buffer, not a byte apart, with the factor and
+    # the step number between them, and the norm's workspace behind a gradient: as in buffers of their own
+    n = [512, 1280]
+    size = dict(p=4, g=4, m=1 if held else 4, v=1 if held else 4)
+    order = [("p", 0), ("g", 0), ("m", 0), ("clip", 0), ("v", 0), ("g", 1), ("ws", 0), ("v", 1), ("step", 0), ("m", 1), ("p", 1)]
+    grads = [_normal(k, 0.1, 40 + i).cuda() for i, k in enumerate(n)]
+    ws = _lib.sft_grad_clip_workspace(grads)
+    at, where = 0, {}
+    for name, i in order:
+        at = -(-at // 16) * 16 if name == "ws" else at
+        where[name, i] = at
+        at += {"clip": 16, "step": 16, "ws": ws}.get(name) or size[name] * n[i]
+    whole = torch.zeros(at, dtype=torch.uint8, device="cuda")
+    state = torch.float8_e4m3fn if held else F32
+
+    def part(name, i, count, dtype):
+        lo = where[name, i]
+        return whole[lo:lo + count * dtype.itemsize].view(dtype)
+
+    def make(inside):
+        vecs = []
+        for i, k in enumerate(n):
+            own = [torch.zeros(k, dtype=t, device="cuda") for t in (F32, F32, state, state)]
+            p, g, m, v = [part(c, i, k, t) for c, t in zip("pgmv", (F32, F32, state, state))] if inside else own
+            p.copy_(_normal(k, 1.0, 30 + i).cuda())
+            g.copy_(grads[i])
+            vecs.append(_lib.AdamwVec(p, g, m, v, _lib.AdamwVec.alloc8(p, g).scale if held else None))
+        return vecs
+
+    a, b, hp = make(True), make(False), adam_dev(**HP)
+    clip, step = part("clip", 0, 1, F32), part("step", 0, 1, torch.int32)
+    step.fill_(3)
+    _lib.sft_grad_clip([v.grad for v in a], 1.0, clip, None, part("ws", 0, ws, torch.uint8))
+    other = torch.zeros(1, device="cuda")
+    _lib.sft_grad_clip([v.grad for v in b], 1.0, other, None, torch.empty(ws, dtype=torch.uint8, device="cuda"))
+    assert 0.0 < clip.item() < 1.0 and torch.equal(clip, other)
+    _lib.sft_adamw(a, step, hp, clip=clip)
+    _lib.sft_adamw(b, 3, hp, clip=other)
+    for x, y, g in zip(a, b, grads):
+        assert torch.equal(x.grad, g) and torch.equal(x.p, y.p)
+        assert torch.equal(x.m.view(torch.uint8), y.m.view(torch.uint8))
+        assert torch.equal(x.v.view(torch.uint8), y.v.view(torch.uint8))
