@@ -46,6 +46,16 @@
  *                                                                     sft_expert_dw,
  *                                                                     sft_grad_clip,
  *                                                                     sft_adamw
+ *   Between the products of a layer: its input's norm with the gradients of
+ *   the gains, rotary positions of queries and keys, and behind the last
+ *   product the log probabilities of the given tokens, from which the loss
+ *   comes, with their gradient.
+ *                                                                  -> sft_norm_forward,
+ *                                                                     sft_norm_backward,
+ *                                                                     sft_rotary_table,
+ *                                                                     sft_rotary,
+ *                                                                     sft_logprob,
+ *                                                                     sft_logprob_grad
  *   The element-sparse variant of the blog post "SparseLeaf: synaptic sparse
  *   fine-tuning" (K selected connections of a frozen weight train their own
  *   increments): their gradients and their Adam step.
@@ -87,7 +97,7 @@
 extern "C" {
 #endif
 
-#define SFT_ABI_VERSION 16
+#define SFT_ABI_VERSION 17
 
 enum {
     SFT_OK = 0,
@@ -912,6 +922,257 @@ typedef struct sft_adamw_vec {
  */
 int sft_adamw(const sft_adamw_vec *vecs, int32_t n_vecs, int32_t step, const int32_t *step_dev, const float *clip,
               const sft_adam *hp, void *stream);
+
+/* ======================================================================= */
+/* device: norms                                                            */
+/* ======================================================================= */
+
+/* What a norm takes off a row before it is scaled: its mean, or nothing. */
+enum { SFT_NORM_LAYER = 0, SFT_NORM_RMS = 1 };
+
+/*
+ * The norm of every row of H = X + res (of X where res is NULL; the sum is
+ * rounded to x_type before it is used):
+ *   mean = sum_c H[c] / C for SFT_NORM_LAYER, 0 for SFT_NORM_RMS
+ *   rstd = 1 / sqrt(sum_c (H[c] - mean)^2 / C + eps)
+ *   Y[c] = (H[c] - mean) * rstd * gain[c] + bias[c]
+ *   X, res, H   x_type [T x C]; res NULL = nothing is added; H receives the
+ *               sum, and is NULL exactly where res is
+ *   gain, bias  w_type [C], either may be NULL (1 and 0)
+ *   Y           y_type [T x C]: x_type, or SFT_BF16 of fp32 rows
+ *   mean, rstd  fp32 [T] out, for the backward pass; either may be NULL
+ *   ldx, ldr, ldh, ldy   elements from one row to the next, at least C
+ * Sums are in fp32 (the squares are taken of the centred values); results are
+ * deterministic, and a row's do not depend on the other rows.  Pointers are
+ * aligned to their types; nothing else is asked of sizes or addresses.
+ * What is written must not overlap anything else, but H may be X or res
+ * itself (the same address and row distance).
+ * With eps = 0 a row of equal values (of zeros, for SFT_NORM_RMS) becomes
+ * NaN, as the formula has it; a row that holds NaN or infinities as well.
+ * Limits: 1 <= C <= 16384, T < 2^31, rows less than 2^40 elements apart,
+ * arrays that span less than 2^46 bytes.
+ * Errors: SFT_EINVAL (null pointers, negative sizes, bad kind or type, eps
+ * negative or not finite, arrays that overlap), SFT_ESHAPE (C = 0, a row
+ * distance below C), SFT_EALIGN, SFT_ENOTSUP (beyond the limits), SFT_EHIP.
+ */
+typedef struct sft_norm_args {
+    int64_t T, C;
+    const void *X;
+    const void *res;
+    void *H;
+    const void *gain;
+    const void *bias;
+    void *Y;
+    float *mean;
+    float *rstd;
+    int64_t ldx, ldr, ldh, ldy;
+    float eps;
+    int32_t kind, x_type, w_type, y_type;
+} sft_norm_args;
+
+int sft_norm_forward(const sft_norm_args *args, void *stream);
+
+/* Workspace bytes sft_norm_backward needs where dgain or dbias is asked for
+ * (with_bias: dbias among them), or (size_t)-1 on invalid input (message in
+ * sft_last_error). */
+size_t sft_norm_backward_workspace(int64_t T, int64_t C, int32_t with_bias);
+
+/*
+ * The backward pass: with xhat = (H - mean) * rstd and g = dY * gain,
+ *   dX    = rstd * (g - xhat * sum_c(g * xhat) / C - sum_c(g) / C) + dH
+ *           (the last sum for SFT_NORM_LAYER only)
+ *   dgain = sum over the rows of dY * xhat,  dbias = sum over the rows of dY
+ *   H           x_type [T x C]: the rows that were normed (X where res was NULL)
+ *   gain        w_type [C], NULL as in the forward pass
+ *   mean, rstd  fp32 [T] from the forward pass; mean NULL for SFT_NORM_RMS
+ *   dY          y_type [T x C]
+ *   dH          x_type [T x C]: the gradient that reaches H on other paths
+ *               (the residual's), or NULL
+ *   dX          x_type [T x C]: the gradient of X, and of res
+ *   dgain, dbias   g_type [C], or NULL where not wanted.  accumulate != 0
+ *               (fp32 only, else SFT_EINVAL): the sums are added to them.
+ *               With T = 0 they are zero (unchanged with accumulate).
+ *   ws / ws_bytes  device scratch of at least sft_norm_backward_workspace()
+ *               bytes (16-byte aligned; no initialisation needed), NULL where
+ *               neither dgain nor dbias is wanted; calls sharing it must be
+ *               ordered on one stream
+ *   ldh, ldy, ldr, ldx   row distances of H, dY, dH and dX
+ * Sums over a row and over the rows are in fp32, in an order that depends
+ * only on T, C and the device: results are deterministic.  What is written
+ * must not overlap anything else, but dX may be dY or dH itself (the same
+ * address, row distance and type).
+ * Limits and errors: as sft_norm_forward, SFT_ECAPACITY (workspace too small).
+ */
+typedef struct sft_norm_grad_args {
+    int64_t T, C;
+    const void *H;
+    const void *gain;
+    const float *mean;
+    const float *rstd;
+    const void *dY;
+    const void *dH;
+    void *dX;
+    void *dgain;
+    void *dbias;
+    int64_t ldh, ldy, ldr, ldx;
+    int32_t kind, x_type, w_type, y_type, g_type, accumulate;
+} sft_norm_grad_args;
+
+int sft_norm_backward(const sft_norm_grad_args *args, void *ws, size_t ws_bytes, void *stream);
+
+/* ======================================================================= */
+/* rotary positions                                                         */
+/* ======================================================================= */
+
+/* How a table's turns are slowed for contexts longer than the one trained on. */
+enum { SFT_ROTARY_PLAIN = 0, SFT_ROTARY_LINEAR = 1, SFT_ROTARY_BASE = 2, SFT_ROTARY_BANDS = 3 };
+
+/* Which elements of a head make a pair: j and j + rot/2, or 2j and 2j + 1. */
+enum { SFT_ROTARY_HALF = 0, SFT_ROTARY_PAIRS = 1 };
+
+/*
+ * Host: the angle (radians) that pair j of rot/2 turns by from one position
+ * to the next, f_j = base^(-2j/rot), or slowed by `factor`:
+ *   SFT_ROTARY_PLAIN    f_j
+ *   SFT_ROTARY_LINEAR   f_j / factor
+ *   SFT_ROTARY_BASE     (base * factor^(rot/(rot-2)))^(-2j/rot): the slowest
+ *                       pair slows by factor, the fastest stays (rot = 2: f_j)
+ *   SFT_ROTARY_BANDS    f_j * (w + (1 - w)/factor) with w = (n_j - low)/(high -
+ *                       low) limited to [0, 1], n_j = context * f_j / (2 pi)
+ *                       the turns that the pair makes over `context`, the
+ *                       length trained on: pairs of more than `high` turns
+ *                       stay, those of fewer than `low` slow by factor
+ *   freq [rot/2] out, fp64
+ * context, low and high are read for SFT_ROTARY_BANDS only.
+ * Errors: SFT_EINVAL (null, bad kind, base <= 0, factor < 1, context <= 0,
+ * high <= low, anything not finite), SFT_ESHAPE (rot odd or below 2).
+ */
+int sft_rotary_table(int64_t rot, double base, int32_t kind, double factor, double context, double low, double high,
+                     double *freq);
+
+/*
+ * One array of heads that sft_rotary turns: element d of head h of token t of
+ * sequence b is at X[b*x_batch + t*x_row + h*x_head + d] (distances in
+ * elements, not negative), and likewise in Y, whose elements must all be
+ * apart.  Y may be X itself (the same address and distances).
+ */
+typedef struct sft_rotary_mat {
+    const void *X;
+    void *Y;
+    int64_t heads;
+    int64_t x_batch, x_row, x_head;
+    int64_t y_batch, y_row, y_head;
+} sft_rotary_mat;
+
+/*
+ * Device: turns the first `rot` elements of every head of the arrays (queries
+ * and keys, say) by their token's position, in one launch: with the angle
+ * a = pos * freq[j], a pair (u, v) becomes
+ *   amplitude * (u*cos(a) - v*sin(a), u*sin(a) + v*cos(a)),
+ * with inverse != 0 the angle is -a, which is the backward pass: Y takes the
+ * gradient of X from that of Y, given as X.  Elements from rot on are copied
+ * (left as they are where Y is X).
+ *   B, T        sequences, and tokens of each
+ *   D           elements of a head, rot of them turned (even, 2 <= rot <= D)
+ *   pos         device int32, position of token t of sequence b at
+ *               pos[b*pos_batch + t]; pos_batch 0 = the same for every
+ *               sequence; any value, negative ones turn backwards
+ *   freq        device double [rot/2], as sft_rotary_table fills it; 8-byte
+ *               aligned.  Angles are taken in fp64, so that far positions
+ *               keep their place; products and sums are in fp32.
+ *   type        SFT_F32 or SFT_BF16 of every array
+ * Limits: D <= 4096, B*T < 2^30, fewer than 2^16 heads in an array, at most 8
+ * arrays, distances below 2^40 elements, arrays that span less than 2^46 bytes.
+ * What is written must not overlap anything else that the call reads or
+ * writes (arrays whose heads lie side by side in the rows of one buffer may
+ * interleave, if their sequences and rows are equally far apart).
+ * Errors: SFT_EINVAL (null pointers, negative sizes or distances, bad layout
+ * or type, amplitude not finite, arrays that overlap), SFT_ESHAPE (rot),
+ * SFT_EALIGN, SFT_ENOTSUP (beyond the limits), SFT_EHIP.
+ */
+int sft_rotary(const sft_rotary_mat *mats, int32_t n_mats, int64_t B, int64_t T, int64_t D, int64_t rot,
+               const double *freq, const int32_t *pos, int64_t pos_batch, float amplitude, int32_t layout,
+               int32_t inverse, int32_t type, void *stream);
+
+/* ======================================================================= */
+/* device: log probabilities of given tokens                                */
+/* ======================================================================= */
+
+/*
+ * For every row z of N rows of V logits, with M = max_j z_j:
+ *   L       = ln sum_j exp(scale * (z_j - M))
+ *   logp_j  = scale * (z_j - M) - L
+ *   entropy = -sum_j exp(logp_j) * logp_j
+ *   Z        z_type [N x V], ldz elements from one row to the next, at least V
+ *   target   device int32 [N]: the given token of each row.  A value outside
+ *            [0, V) means none: the row's logp is 0.  NULL exactly where logp is.
+ *   scale    positive and finite (1 / temperature)
+ *   logp     fp32 [N] out: logp of the given token
+ *   stats    fp32 [N x 2] out: M and L, which the gradient reads; may be NULL
+ *   entropy  fp32 [N] out, or NULL
+ *   top_k    how many alternatives to tell (0 to 64, 0 = none): the K largest
+ *            logits of the row in descending order, of equal ones the lower
+ *            index first
+ *   top_logp, top_index   fp32 and int32 [N x top_k] out: their logp and
+ *            index; top_logp may be NULL
+ * A logit of -infinity marks a token that is not allowed: its probability is
+ * 0, and it is no alternative; where fewer than K are left, the others have
+ * index -1 and logp -infinity.  A row of nothing else has M = L = logp =
+ * -infinity and entropy 0.  A row with +infinity or NaN has NaN for L, logp
+ * and entropy, and its alternatives, NaN never among them, have logp NaN.
+ * Sums are in fp32; results are deterministic, and a row's do not depend on
+ * the other rows.  Pointers are aligned to their types.  No workspace.
+ * Limits: 1 <= V < 2^30, N < 2^31, distances and spans as in sft_norm_forward.
+ * What is written must not overlap anything else.
+ * Errors: SFT_EINVAL (null pointers, negative sizes, bad type, scale or top_k,
+ * arrays that overlap), SFT_ESHAPE (V = 0, ldz below V), SFT_EALIGN,
+ * SFT_ENOTSUP (beyond the limits), SFT_EHIP.
+ */
+typedef struct sft_logprob_args {
+    int64_t N, V, ldz;
+    const void *Z;
+    const int32_t *target;
+    float *logp;
+    float *stats;
+    float *entropy;
+    float *top_logp;
+    int32_t *top_index;
+    int32_t z_type, top_k;
+    float scale;
+} sft_logprob_args;
+
+int sft_logprob(const sft_logprob_args *args, void *stream);
+
+/*
+ * The gradient with respect to the logits of a loss whose derivatives by each
+ * row's logp and entropy are dlogp and dentropy:
+ *   dZ_j = scale * (dlogp * [j = target] - p_j * (dlogp + dentropy * (logp_j + entropy))),
+ * p_j = exp(logp_j), with dlogp counting as 0 in rows without a given token.
+ *   Z, ldz, target, scale   as in sft_logprob; target NULL exactly where dlogp is
+ *   stats      fp32 [N x 2] from sft_logprob
+ *   entropy    fp32 [N] from sft_logprob, NULL exactly where dentropy is
+ *   dlogp, dentropy   fp32 [N], either may be NULL (0)
+ *   dZ         dz_type [N x V], lddz elements from one row to the next: z_type,
+ *              or SFT_BF16 of fp32 logits
+ * Where both derivatives of a row are 0, or every logit of it is -infinity,
+ * dZ is 0 and Z is not read.  A row with +infinity or NaN becomes NaN.
+ * dZ may be Z itself (the same address, row distance and type).
+ * Limits and errors: as sft_logprob.
+ */
+typedef struct sft_logprob_grad_args {
+    int64_t N, V, ldz, lddz;
+    const void *Z;
+    const int32_t *target;
+    const float *stats;
+    const float *entropy;
+    const float *dlogp;
+    const float *dentropy;
+    void *dZ;
+    int32_t z_type, dz_type;
+    float scale;
+} sft_logprob_grad_args;
+
+int sft_logprob_grad(const sft_logprob_grad_args *args, void *stream);
 
 #ifdef __cplusplus
 }

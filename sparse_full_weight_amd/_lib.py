@@ -38,6 +38,8 @@ EXPORTS = (
     "sft_noalloc_scratch_bytes", "sft_masked_dw_update_noalloc", "sft_plan_layer_words", "sft_plan_layer",
     "sft_plan_upload", "sft_grad_clip_workspace", "sft_grad_clip", "sft_adamw",
     "sft_expert_forward", "sft_expert_dx", "sft_expert_dw", "sft_probe_expert_tiles",
+    "sft_norm_forward", "sft_norm_backward_workspace", "sft_norm_backward", "sft_rotary_table", "sft_rotary",
+    "sft_logprob", "sft_logprob_grad",
 )
 
 
@@ -144,6 +146,42 @@ class CAdamwVec(C.Structure):
                 ("scale", C.c_void_p), ("p_live", C.c_void_p), ("p_type", C.c_int32), ("g_type", C.c_int32)]
 
 
+SFT_NORM_LAYER, SFT_NORM_RMS = 0, 1
+SFT_ROTARY_PLAIN, SFT_ROTARY_LINEAR, SFT_ROTARY_BASE, SFT_ROTARY_BANDS = 0, 1, 2, 3
+SFT_ROTARY_HALF, SFT_ROTARY_PAIRS = 0, 1
+
+
+class CNormArgs(C.Structure):
+    _fields_ = [("T", C.c_int64), ("C", C.c_int64)] + [
+        (n, C.c_void_p) for n in ("X", "res", "H", "gain", "bias", "Y", "mean", "rstd")] + [
+        (n, C.c_int64) for n in ("ldx", "ldr", "ldh", "ldy")] + [("eps", C.c_float)] + [
+        (n, C.c_int32) for n in ("kind", "x_type", "w_type", "y_type")]
+
+
+class CNormGradArgs(C.Structure):
+    _fields_ = [("T", C.c_int64), ("C", C.c_int64)] + [
+        (n, C.c_void_p) for n in ("H", "gain", "mean", "rstd", "dY", "dH", "dX", "dgain", "dbias")] + [
+        (n, C.c_int64) for n in ("ldh", "ldy", "ldr", "ldx")] + [
+        (n, C.c_int32) for n in ("kind", "x_type", "w_type", "y_type", "g_type", "accumulate")]
+
+
+class CRotaryMat(C.Structure):
+    _fields_ = [("X", C.c_void_p), ("Y", C.c_void_p)] + [
+        (n, C.c_int64) for n in ("heads", "x_batch", "x_row", "x_head", "y_batch", "y_row", "y_head")]
+
+
+class CLogprobArgs(C.Structure):
+    _fields_ = [(n, C.c_int64) for n in ("N", "V", "ldz")] + [
+        (n, C.c_void_p) for n in ("Z", "target", "logp", "stats", "entropy", "top_logp", "top_index")] + [
+        ("z_type", C.c_int32), ("top_k", C.c_int32), ("scale", C.c_float)]
+
+
+class CLogprobGradArgs(C.Structure):
+    _fields_ = [(n, C.c_int64) for n in ("N", "V", "ldz", "lddz")] + [
+        (n, C.c_void_p) for n in ("Z", "target", "stats", "entropy", "dlogp", "dentropy", "dZ")] + [
+        ("z_type", C.c_int32), ("dz_type", C.c_int32), ("scale", C.c_float)]
+
+
 _lib: Optional[C.CDLL] = None
 
 
@@ -198,6 +236,15 @@ def lib() -> C.CDLL:
         L.sft_grad_clip_workspace.restype = C.c_size_t
         L.sft_grad_clip.argtypes = [C.POINTER(CGradVec), i32, f32, p, p, p, C.c_size_t, p]
         L.sft_adamw.argtypes = [C.POINTER(CAdamwVec), i32, i32, p, p, C.POINTER(CAdam), p]
+        L.sft_norm_forward.argtypes = [C.POINTER(CNormArgs), p]
+        L.sft_norm_backward_workspace.argtypes = [i64, i64, i32]
+        L.sft_norm_backward_workspace.restype = C.c_size_t
+        L.sft_norm_backward.argtypes = [C.POINTER(CNormGradArgs), p, C.c_size_t, p]
+        f64 = C.c_double
+        L.sft_rotary_table.argtypes = [i64, f64, i32, f64, f64, f64, f64, p]
+        L.sft_rotary.argtypes = [C.POINTER(CRotaryMat), i32, i64, i64, i64, i64, p, p, i64, f32, i32, i32, i32, p]
+        L.sft_logprob.argtypes = [C.POINTER(CLogprobArgs), p]
+        L.sft_logprob_grad.argtypes = [C.POINTER(CLogprobGradArgs), p]
         L.sft_probe_grid.argtypes = []
         L.sft_probe_read.argtypes = [p, C.c_size_t, p, p]
         L.sft_probe_copy.argtypes = [p, p, C.c_size_t, p]
@@ -211,7 +258,7 @@ def lib() -> C.CDLL:
                                          C.POINTER(C.c_double)]
         for n in EXPORTS[2:]:
             if n not in ("sft_masked_dw_workspace", "sft_leaf_grad_workspace", "sft_grad_clip_workspace",
-                         "sft_noalloc_scratch_bytes"):
+                         "sft_norm_backward_workspace", "sft_noalloc_scratch_bytes"):
                 getattr(L, n).restype = C.c_int
         _lib = L
     return _lib
@@ -1155,6 +1202,258 @@ def sft_adamw(vecs: Sequence[AdamwVec], step, hp: Adam, clip=None, stream=None) 
     element that multiplies the gradients, as sft_grad_clip writes it (the
     step is left out where it is not a positive finite number)."""
     prepare_adamw(vecs, step, hp, clip)(stream)
+
+
+# ------------------------------------------------------------------ norms
+def _rows(t, what, dtype=None, like=None):
+    """(pointer, row distance) of a 2-D tensor on the current GPU whose rows are
+    contiguous, of the shape `like` where one is given (None -> (NULL, 0))."""
+    if t is None:
+        return None, 0
+    if t.dim() != 2:
+        raise ValueError(f"{what}: {t.dim()} dimensions, expected rows of values")
+    if like is not None:
+        _shape(t, like, what)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
+    n, width = t.shape
+    if width > 1 and n and t.stride(1) != 1:
+        raise ValueError(f"{what}: the values of a row must be contiguous")
+    return _at(t), (t.stride(0) if n > 1 else width)
+
+
+def _at(t):
+    """Device pointer of a tensor on the current GPU, whatever its strides."""
+    import torch
+    if not t.is_cuda:
+        raise TypeError("device argument must be a GPU tensor")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return t.data_ptr()
+
+
+def _vector(t, n, what, dtype=None):
+    """Device pointer of a contiguous vector of n values (None -> NULL)."""
+    if t is not None:
+        _shape(t, (n,), what)
+    return _here(t, dtype)
+
+
+NORM_KINDS = {"layer": SFT_NORM_LAYER, "rms": SFT_NORM_RMS}
+
+
+def _of(table, key, what):
+    if key not in table:
+        raise ValueError(f"{what}: {key!r} is none of {', '.join(table)}")
+    return table[key]
+
+
+def _gains(gain, bias, cols):
+    """Pointers and type of a norm's gain and bias."""
+    first = gain if gain is not None else bias
+    dtype = None if first is None else first.dtype
+    return (_vector(gain, cols, "gain", dtype), _vector(bias, cols, "bias", dtype),
+            SFT_F32 if first is None else _type(first, "gain"))
+
+
+def prepare_norm_forward(X, gain, Y, *, kind: str = "rms", eps: float = 1e-5, bias=None, res=None, H=None, mean=None,
+                         rstd=None) -> PreparedHere:
+    """sft_norm_forward with its arguments built once."""
+    import torch
+    x, ldx = _rows(X, "X")
+    T, cols = X.shape
+    r, ldr = _rows(res, "res", X.dtype, X.shape)
+    h, ldh = _rows(H, "H", X.dtype, X.shape)
+    y, ldy = _rows(Y, "Y", None, X.shape)
+    g, b, w_type = _gains(gain, bias, cols)
+    args = CNormArgs(T, cols, x, r, h, g, b, y, _vector(mean, T, "mean", torch.float32),
+                     _vector(rstd, T, "rstd", torch.float32), ldx, ldr, ldh, ldy, float(eps),
+                     _of(NORM_KINDS, kind, "kind"), _type(X, "X"), w_type, _type(Y, "Y"))
+    return PreparedHere(lib().sft_norm_forward, (C.byref(args),), (args, X, gain, Y, bias, res, H, mean, rstd))
+
+
+def sft_norm_forward(X, gain, Y, *, kind: str = "rms", eps: float = 1e-5, bias=None, res=None, H=None, mean=None,
+                     rstd=None, stream=None) -> None:
+    """Norm of every row of H = X + res (of X where res is None), async on the
+    stream: Y = (H - mean) * rstd * gain + bias, with the mean 0 for the kind
+    "rms" and the row's for "layer".  X, res, H [T x C] of one type (rows may
+    lie apart; H may be X or res), Y of that type or bfloat16; gain and bias
+    [C] or None; mean and rstd float32 [T] for the backward pass, or None."""
+    prepare_norm_forward(X, gain, Y, kind=kind, eps=eps, bias=bias, res=res, H=H, mean=mean, rstd=rstd)(stream)
+
+
+def sft_norm_backward_workspace(T: int, cols: int, *, bias: bool = False) -> int:
+    """Workspace bytes of sft_norm_backward with dgain (and dbias, with `bias`)."""
+    n = lib().sft_norm_backward_workspace(T, cols, int(bool(bias)))
+    if n == C.c_size_t(-1).value:
+        raise SftError(SFT_EINVAL, lib().sft_last_error().decode())
+    return n
+
+
+def prepare_norm_backward(H, gain, rstd, dY, dX, dgain, *, kind: str = "rms", mean=None, dbias=None, dH=None,
+                          accumulate: bool = False, ws=None) -> PreparedHere:
+    """sft_norm_backward with its arguments built once."""
+    import torch
+    h, ldh = _rows(H, "H")
+    T, cols = H.shape
+    y, ldy = _rows(dY, "dY", None, H.shape)
+    r, ldr = _rows(dH, "dH", H.dtype, H.shape)
+    x, ldx = _rows(dX, "dX", H.dtype, H.shape)
+    g, _, w_type = _gains(gain, None, cols)
+    sums = dgain if dgain is not None else dbias
+    dtype = None if sums is None else sums.dtype
+    args = CNormGradArgs(T, cols, h, g, _vector(mean, T, "mean", torch.float32),
+                         _vector(rstd, T, "rstd", torch.float32), y, r, x, _vector(dgain, cols, "dgain", dtype),
+                         _vector(dbias, cols, "dbias", dtype), ldh, ldy, ldr, ldx, _of(NORM_KINDS, kind, "kind"),
+                         _type(H, "H"), w_type, _type(dY, "dY"),
+                         SFT_F32 if sums is None else _type(sums, "dgain"), int(bool(accumulate)))
+    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    return PreparedHere(lib().sft_norm_backward, (C.byref(args), _here(ws), nbytes),
+                        (args, H, gain, rstd, dY, dX, dgain, mean, dbias, dH, ws))
+
+
+def sft_norm_backward(H, gain, rstd, dY, dX, dgain, *, kind: str = "rms", mean=None, dbias=None, dH=None,
+                      accumulate: bool = False, ws=None, stream=None) -> None:
+    """Backward pass of sft_norm_forward (async on the stream): dX [T x C] from
+    dY and the rows H that were normed, plus dH (the gradient that reaches H
+    on other paths) where given; dgain and dbias [C], float32 or bfloat16, or
+    None where not wanted, added to what is there with accumulate (float32).
+    ws holds sft_norm_backward_workspace(T, C, bias=dbias is not None) bytes
+    where one of them is wanted.  dX may be dY or dH."""
+    prepare_norm_backward(H, gain, rstd, dY, dX, dgain, kind=kind, mean=mean, dbias=dbias, dH=dH,
+                          accumulate=accumulate, ws=ws)(stream)
+
+
+# ------------------------------------------------------------------ rotary positions
+ROTARY_SCALING = {"plain": SFT_ROTARY_PLAIN, "linear": SFT_ROTARY_LINEAR, "base": SFT_ROTARY_BASE,
+                  "bands": SFT_ROTARY_BANDS}
+ROTARY_LAYOUTS = {"half": SFT_ROTARY_HALF, "pairs": SFT_ROTARY_PAIRS}
+
+
+def sft_rotary_table(rot: int, base: float = 10000.0, *, scaling: str = "plain", factor: float = 1.0,
+                     context: float = 0.0, low: float = 1.0, high: float = 4.0) -> np.ndarray:
+    """Angles (float64 [rot/2], radians a position) of the pairs of a head, as
+    they are or slowed by `factor` for contexts longer than the one trained on:
+    all of them ("linear"), by a larger base ("base"), or those of few turns
+    over `context`, the length trained on ("bands")."""
+    freq = np.zeros(max(rot // 2, 1), np.float64)
+    _check(lib().sft_rotary_table(rot, base, _of(ROTARY_SCALING, scaling, "scaling"), factor, context, low, high,
+                                  _np_ptr(freq)))
+    return freq
+
+
+def _heads(t, what, shape=None):
+    """(pointer, sequences, tokens, heads, size, distances) of heads [T x heads
+    x D] or [B x T x heads x D] with contiguous heads."""
+    if t.dim() not in (3, 4):
+        raise ValueError(f"{what}: {t.dim()} dimensions, expected tokens x heads x size, with or without sequences")
+    if shape is not None:
+        _shape(t, shape, what)
+    if t.shape[-1] > 1 and t.numel() and t.stride(-1) != 1:
+        raise ValueError(f"{what}: the values of a head must be contiguous")
+    size, dist = tuple(t.shape), tuple(t.stride())
+    if t.dim() == 3:
+        size, dist = (1, *size), (0, *dist)
+    # the distance of a single sequence, token or head is never used
+    return _at(t), size, tuple(d if n > 1 else 0 for n, d in zip(size, dist[:3]))
+
+
+def prepare_rotary(arrays, pos, freq, rot: int, *, layout: str = "half", inverse: bool = False,
+                   amplitude: float = 1.0) -> PreparedHere:
+    """sft_rotary with its arguments built once."""
+    import torch
+    if not arrays:
+        raise ValueError("no arrays")
+    mats, first = [], None
+    for i, (X, Y) in enumerate(arrays):
+        x, size, xd = _heads(X, f"X of array {i}")
+        y, _, yd = _heads(Y, f"Y of array {i}", X.shape)
+        first = first or (size, X.dtype)
+        if size[:2] != first[0][:2] or size[3] != first[0][3] or X.dtype != first[1] or Y.dtype != first[1]:
+            raise ValueError(f"array {i}: its sequences, tokens, head size and type must be those of the first")
+        mats.append(CRotaryMat(x, y, size[2], *xd, *yd))
+    B, T, _, D = first[0]
+    if pos.dim() == 1:
+        _shape(pos, (T,), "pos")
+        at, pos_batch = _here(pos, torch.int32), 0
+    else:
+        _shape(pos, (B, T), "pos")
+        at, pos_batch = _rows(pos, "pos", torch.int32)
+    arr = (CRotaryMat * len(mats))(*mats)
+    args = (arr, len(mats), B, T, D, rot, _vector(freq, rot // 2, "freq", torch.float64), at, pos_batch,
+            float(amplitude), _of(ROTARY_LAYOUTS, layout, "layout"), int(bool(inverse)), _type(arrays[0][0], "X"))
+    return PreparedHere(lib().sft_rotary, args, (arr, list(arrays), pos, freq))
+
+
+def sft_rotary(arrays, pos, freq, rot: int, *, layout: str = "half", inverse: bool = False, amplitude: float = 1.0,
+               stream=None) -> None:
+    """Turns the first `rot` elements of every head by its token's position
+    (async on the stream).  arrays: (X, Y) pairs of tensors [T x heads x D] or
+    [B x T x heads x D], float32 or bfloat16, of any strides with contiguous
+    heads (Y may be X): queries and keys go in one call.  pos int32 [T], or [B x
+    T]; freq float64 [rot/2] as sft_rotary_table makes it; layout "half" pairs
+    j with j + rot/2, "pairs" 2j with 2j + 1.  inverse: the backward pass, from
+    the gradient of Y to that of X."""
+    prepare_rotary(arrays, pos, freq, rot, layout=layout, inverse=inverse, amplitude=amplitude)(stream)
+
+
+# ------------------------------------------------------------------ log probabilities of given tokens
+def prepare_logprob(Z, target, logp, *, scale: float = 1.0, stats=None, entropy=None, top_logp=None,
+                    top_index=None) -> PreparedHere:
+    """sft_logprob with its arguments built once."""
+    import torch
+    z, ld = _rows(Z, "Z")
+    N, V = Z.shape
+    f32, i32 = torch.float32, torch.int32
+    K = 0
+    if top_index is not None:
+        _shape(top_index, (N, None), "top_index")
+        K = top_index.shape[1]
+    if top_logp is not None:
+        _shape(top_logp, (N, K), "top_logp")
+    if stats is not None:
+        _shape(stats, (N, 2), "stats")
+    args = CLogprobArgs(N, V, ld, z, _vector(target, N, "target", i32), _vector(logp, N, "logp", f32),
+                        _here(stats, f32), _vector(entropy, N, "entropy", f32), _here(top_logp, f32),
+                        _here(top_index, i32), _type(Z, "Z"), K, float(scale))
+    return PreparedHere(lib().sft_logprob, (C.byref(args),), (args, Z, target, logp, stats, entropy, top_logp, top_index))
+
+
+def sft_logprob(Z, target, logp, *, scale: float = 1.0, stats=None, entropy=None, top_logp=None, top_index=None,
+                stream=None) -> None:
+    """Log probabilities of the given tokens from rows of logits (async on the
+    stream).  Z [N x V] float32 or bfloat16 (rows may lie apart, -infinity
+    marks what is not allowed), target int32 [N] (outside [0, V): none, logp
+    0), logp float32 [N]; target and logp may both be None.  Where given:
+    stats float32 [N x 2] for the gradient, entropy float32 [N], top_index int32
+    and top_logp float32 [N x K] with the K likeliest tokens (up to 64)."""
+    prepare_logprob(Z, target, logp, scale=scale, stats=stats, entropy=entropy, top_logp=top_logp,
+                    top_index=top_index)(stream)
+
+
+def prepare_logprob_grad(Z, target, stats, dlogp, dZ, *, scale: float = 1.0, entropy=None,
+                         dentropy=None) -> PreparedHere:
+    """sft_logprob_grad with its arguments built once."""
+    import torch
+    z, ld = _rows(Z, "Z")
+    N, V = Z.shape
+    d, ldd = _rows(dZ, "dZ", None, Z.shape)
+    f32 = torch.float32
+    _shape(stats, (N, 2), "stats")
+    args = CLogprobGradArgs(N, V, ld, ldd, z, _vector(target, N, "target", torch.int32), _here(stats, f32),
+                            _vector(entropy, N, "entropy", f32), _vector(dlogp, N, "dlogp", f32),
+                            _vector(dentropy, N, "dentropy", f32), d, _type(Z, "Z"), _type(dZ, "dZ"), float(scale))
+    return PreparedHere(lib().sft_logprob_grad, (C.byref(args),), (args, Z, target, stats, dlogp, dZ, entropy, dentropy))
+
+
+def sft_logprob_grad(Z, target, stats, dlogp, dZ, *, scale: float = 1.0, entropy=None, dentropy=None,
+                     stream=None) -> None:
+    """Gradient of a loss by the logits (async on the stream), from its
+    derivatives by each row's logp (dlogp float32 [N]; target and dlogp may both
+    be None) and entropy (dentropy float32 [N] with the entropy of sft_logprob,
+    or both None).  Z, target, scale and stats as in sft_logprob; dZ [N x V] of
+    Z's type or bfloat16, may be Z."""
+    prepare_logprob_grad(Z, target, stats, dlogp, dZ, scale=scale, entropy=entropy, dentropy=dentropy)(stream)
 
 
 # ------------------------------------------------------------------ coupled-update schedule

@@ -1,0 +1,490 @@
+// sft_logprob.hip -- log probabilities of given tokens from rows of logits,
+// with the rows' entropy and likeliest alternatives, and the gradient.
+//
+// The forward pass reads a row once, keeping in every thread the largest logit
+// so far, m, and relative to it the sums of e^(scale (z - m)) and of that
+// times scale (z - m); the threads' parts are joined at the row's end.  Both
+// passes are bound by HBM; a forward pass with entropy in bf16 does about ten
+// operations a logit, which is three quarters of what the time of the read
+// allows.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "sft_blocks.h"
+#include "sft_internal.h"
+#include "sft_vec.h"
+
+namespace {
+
+using namespace sft;
+
+constexpr float kInf = __builtin_huge_valf();
+constexpr float kLn2 = 0.693147180559945309f;
+// Powers of two below this one are 0 in fp32; a bound for exponents that may
+// be minus infinity and get multiplied by 0.
+constexpr float kNothing = -1000.0f;
+// Where the largest logit times c (scale in units of log2) is beyond this, the
+// product with c is no longer safe from overflow and differences come first.
+constexpr float kFar = 1e38f;
+constexpr int kMaxTop = 64;
+constexpr int kCandidates = 1024;
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    // (a NaN among the logits may take m's place for a while; its row's sums
+    // tell, and the row is then read in another way)
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float limit(float x, float lo, float hi) { return __builtin_amdgcn_fmed3f(x, lo, hi); }
+
+// Order of floats (without NaN; the two zeros are one value) as unsigned integers; 0 is below all of them.
+__device__ __forceinline__ uint32_t order_of(float x) {
+    const uint32_t b = float_bits(x + 0.0f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+// Larger for a larger logit, of equal ones for the lower index.
+__device__ __forceinline__ uint64_t key_of(float z, uint32_t at) { return uint64_t(order_of(z)) << 32 | (0xffffffffu - at); }
+
+struct Logprob {
+    const void *z;
+    const int32_t *target;
+    float *logp, *stats, *entropy, *top_logp;
+    int32_t *top_index;
+    int64_t ld;
+    int32_t N, V, top;
+    float scale, c;                // c = scale * log2(e)
+};
+
+// A row's running state in one thread, relative to m2 = m * c.
+struct Running {
+    float m, m2, sum, along;
+};
+
+// Takes up U groups of logits.
+template <bool kEntropy, int U>
+__device__ __forceinline__ void take_up(Running &r, const float (&z)[U][8], float c) {
+    float m = r.m;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) m = max3(m, z[u][i], z[u][i + 1]);
+    const float m2 = __builtin_fmaxf(m * c, -kFar);       // (of minus infinity as well)
+    const float less = limit(r.m2 - m2, kNothing, 0.0f), part = exp2_of(less);
+    r.along = kEntropy ? part * __builtin_fmaf(r.sum, less, r.along) : 0.0f;
+    r.sum *= part;
+    r.m = m;
+    r.m2 = m2;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float d = __builtin_fmaf(z[u][i], c, -m2), e = exp2_of(d);
+            r.sum += e;
+            if (kEntropy) r.along = __builtin_fmaf(e, __builtin_fmaxf(d, kNothing), r.along);
+        }
+}
+
+template <class Op, int kThreads>
+__device__ __forceinline__ float block_of(float x, float *red) {
+    x = lanes_of<Op, 64>(x);
+    if constexpr (kThreads > 64) {
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
+        __syncthreads();
+        x = red[0];
+#pragma unroll
+        for (int i = 1; i < kThreads / 64; ++i) x = Op::of(x, red[i]);
+    }
+    return x;
+}
+
+__device__ __forceinline__ uint64_t wave_max(uint64_t x) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+        const uint64_t y = __shfl_xor(x, d);
+        x = y > x ? y : x;
+    }
+    return x;
+}
+
+template <class Z>
+__device__ __forceinline__ float logit(const typename Z::type *z, int at) {
+    return Z::up(z[at]);
+}
+
+struct TopPlace {
+    float threshold;
+    int owners, found;
+};
+
+// The K likeliest of a row, of which every thread knows the largest logit that
+// it has seen.  The K-th largest of those is a bound that at least K logits
+// reach, so only threads whose own largest reaches it have alternatives; their
+// logits are read again (a few of them, by the whole workgroup, out of the
+// caches), those that reach the bound are collected and ranked by counting.
+// Where too many do, or a NaN may have hidden a thread's largest, the
+// alternatives are looked for one by one.
+template <class Z, int kThreads>
+__device__ void top_of(const Logprob &a, int64_t row, float mine, bool plain, float M, float L, float *most,
+                       int32_t *owner, uint64_t *found, TopPlace *place) {
+    const typename Z::type *z = static_cast<const typename Z::type *>(a.z) + row * a.ld;
+    float *top_logp = a.top_logp ? a.top_logp + row * a.top : nullptr;
+    int32_t *top_index = a.top_index + row * a.top;
+    const auto tell = [&](int rank, uint64_t key) {
+        const int at = static_cast<int>(0xffffffffu - static_cast<uint32_t>(key));
+        top_index[rank] = at;
+        if (top_logp) top_logp[rank] = a.scale * (logit<Z>(z, at) - M) - L;
+    };
+    const auto nothing = [&](int rank) {
+        top_index[rank] = -1;
+        if (top_logp) top_logp[rank] = -kInf;
+    };
+    if (plain) {
+        most[threadIdx.x] = mine;
+        if (threadIdx.x == 0) place->owners = place->found = 0;
+        __syncthreads();
+        if (threadIdx.x < 64) {
+            // of every 64th thread the largest, then the K-th largest of those 64 by halving
+            float x = most[threadIdx.x];
+#pragma unroll
+            for (int i = 1; i < kThreads / 64; ++i) x = __builtin_fmaxf(x, most[threadIdx.x + 64 * i]);
+            const uint32_t o = order_of(x);
+            uint32_t bound = 0;
+            for (uint32_t bit = 1u << 31; bit; bit >>= 1)
+                if (__builtin_popcountll(__ballot(o >= (bound | bit))) >= a.top) bound |= bit;
+            if (threadIdx.x == 0)
+                place->threshold = bits_float(bound & 0x80000000u ? bound & 0x7fffffffu : ~bound);
+        }
+        __syncthreads();
+        const float threshold = place->threshold;
+        if (mine >= threshold && mine > -kInf) owner[atomicAdd(&place->owners, 1)] = threadIdx.x;
+        __syncthreads();
+        const int owners = place->owners, groups = (a.V + kThreads * 8 - 1) / (kThreads * 8);
+        for (int p = threadIdx.x; p < owners * groups; p += kThreads) {
+            const int g = p / owners, at = (g * kThreads + owner[p - g * owners]) * 8, n = a.V - at;
+            if (n <= 0) continue;
+            float x[8];
+            open8<Z>(n >= 8 ? get8<Z>(z + at) : get_few<Z>(z + at, n), x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < n && x[i] >= threshold && x[i] > -kInf) {
+                    const int k = atomicAdd(&place->found, 1);
+                    if (k < kCandidates) found[k] = key_of(x[i], at + i);
+                }
+        }
+        __syncthreads();
+        const int n = place->found;
+        if (n <= kCandidates) {
+            for (int k = threadIdx.x; k < n; k += kThreads) {
+                const uint64_t key = found[k];
+                int rank = 0;
+                for (int j = 0; j < n; ++j) rank += found[j] > key;
+                if (rank < a.top) tell(rank, key);
+            }
+            for (int k = n + threadIdx.x; k < a.top; k += kThreads) nothing(k);
+            return;
+        }
+    }
+    uint64_t last = ~uint64_t(0);
+    for (int rank = 0; rank < a.top; ++rank) {
+        uint64_t best = 0;
+        for (int at = threadIdx.x * 8; at < a.V; at += kThreads * 8) {
+            float x[8];
+            const int n = a.V - at;
+            open8<Z>(n >= 8 ? get8<Z>(z + at) : get_few<Z>(z + at, n), x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint64_t key = key_of(x[i], at + i);
+                if (i < n && x[i] > -kInf && key < last && key > best) best = key;
+            }
+        }
+        best = wave_max(best);
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) found[threadIdx.x >> 6] = best;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kThreads / 64; ++i) best = found[i] > best ? found[i] : best;
+        if (threadIdx.x == 0) {
+            if (best)
+                tell(rank, best);
+            else
+                nothing(rank);
+        }
+        last = best;
+    }
+}
+
+template <class Z, int kThreads, bool kEntropy, bool kTop>
+__global__ __launch_bounds__(kThreads) void k_logprob(const Logprob a) {
+    constexpr int kWaves = kThreads / 64, U = 4;
+    __shared__ float red[3][kWaves];
+    __shared__ float most[kTop ? kThreads : 1];
+    __shared__ int32_t owner[kTop ? kThreads : 1];
+    __shared__ uint64_t found[kTop ? kCandidates : 1];
+    __shared__ TopPlace place;
+    for (int64_t row = blockIdx.x; row < a.N; row += gridDim.x) {
+        const typename Z::type *z = static_cast<const typename Z::type *>(a.z) + row * a.ld;
+        const int target = a.target ? a.target[row] : -1;
+        const bool given = target >= 0 && target < a.V;
+        const float at_target = given ? logit<Z>(z, target) : 0.0f;
+        Running r{-kInf, -kFar, 0.0f, 0.0f};
+        int at = threadIdx.x * 8;
+        for (int base = 0; base + U * kThreads * 8 <= a.V; base += U * kThreads * 8, at += U * kThreads * 8) {
+            Raw<Z> raw[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) raw[u] = get8<Z>(z + at + u * kThreads * 8);
+            float x[U][8];
+#pragma unroll
+            for (int u = 0; u < U; ++u) open8<Z>(raw[u], x[u]);
+            take_up<kEntropy, U>(r, x, a.c);
+        }
+        for (; at < a.V; at += kThreads * 8) {
+            float x[1][8];
+            const int n = a.V - at;
+            open8<Z>(n >= 8 ? get8<Z>(z + at) : get_few<Z>(z + at, n), x[0]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[0][i] = i < n ? x[0][i] : -kInf;
+            take_up<kEntropy, 1>(r, x, a.c);
+        }
+        float M = block_of<Max, kThreads>(r.m, red[0]);
+        const float m2 = __builtin_fmaxf(M * a.c, -kFar);
+        const float less = limit(r.m2 - m2, kNothing, 0.0f), part = exp2_of(less);
+        float along = kEntropy ? block_of<Sum, kThreads>(part * __builtin_fmaf(r.sum, less, r.along), red[1]) : 0.0f;
+        float sum = block_of<Sum, kThreads>(r.sum * part, red[2]);
+        // what m2 is off M * c by
+        float off = __builtin_fmaf(M, a.c, -m2);
+        const bool finite = __builtin_fabsf(M) < kInf;
+        if (finite && !(__builtin_fabsf(M * a.c) < kFar)) {
+            sum = along = off = 0.0f;
+            for (int i = threadIdx.x; i < a.V; i += kThreads) {
+                const float d = (logit<Z>(z, i) - M) * a.c, e = exp2_of(d);
+                sum += e;
+                along = __builtin_fmaf(e, __builtin_fmaxf(d, kNothing), along);
+            }
+            __syncthreads();
+            along = block_of<Sum, kThreads>(along, red[1]);
+            sum = block_of<Sum, kThreads>(sum, red[2]);
+        }
+        const bool none = M == -kInf && sum == 0.0f;      // a row without an allowed token
+        float L = logf(sum), entropy = 0.0f;
+        // neither is below 0, whatever the roundings
+        if (kEntropy) entropy = __builtin_fmaxf(L - kLn2 * (along / sum), 0.0f);
+        L = __builtin_fmaxf(L - kLn2 * off, 0.0f);
+        if (!finite || sum != sum) {
+            const float nan = __builtin_nanf("");
+            M = none ? -kInf : nan;
+            L = none ? -kInf : nan;
+            entropy = none ? 0.0f : nan;
+        }
+        if (threadIdx.x == 0) {
+            if (a.logp) a.logp[row] = !given ? 0.0f : none ? -kInf : a.scale * (at_target - M) - L;
+            if (a.stats) {
+                a.stats[2 * row] = M;
+                a.stats[2 * row + 1] = L;
+            }
+            if (kEntropy) a.entropy[row] = entropy;
+        }
+        if constexpr (kTop) top_of<Z, kThreads>(a, row, r.m, sum == sum, M, L, most, owner, found, &place);
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------------ gradient
+struct LogprobGrad {
+    const void *z;
+    const int32_t *target;
+    const float *stats, *entropy, *dlogp, *dentropy;
+    void *dz;
+    int64_t ld, ldd;
+    int64_t pieces;                // of all rows
+    int32_t N, V, per_row;         // pieces of a row
+    float scale, c;
+};
+
+constexpr int kGradThreads = 256, kGradGroups = 4, kPiece = kGradThreads * kGradGroups * 8;
+
+template <class Z, class D, bool kEntropy>
+__global__ __launch_bounds__(kGradThreads) void k_logprob_grad(const LogprobGrad a) {
+    constexpr float kLog2e = 1.44269504088896340736f;
+    for (int64_t p = blockIdx.x; p < a.pieces; p += gridDim.x) {
+        const int64_t row = p / a.per_row;
+        const int begin = static_cast<int>(p - row * a.per_row) * kPiece;
+        const typename Z::type *z = static_cast<const typename Z::type *>(a.z) + row * a.ld;
+        typename D::type *dz = static_cast<typename D::type *>(a.dz) + row * a.ldd;
+        const int target = a.target ? a.target[row] : -1;
+        const bool given = target >= 0 && target < a.V;
+        const float own = given && a.dlogp ? a.dlogp[row] : 0.0f;
+        const float by_entropy = kEntropy ? a.dentropy[row] : 0.0f;
+        const float M = a.stats[2 * row], L = a.stats[2 * row + 1];
+        if ((own == 0.0f && by_entropy == 0.0f) || (M == -kInf && L == -kInf)) {
+#pragma unroll
+            for (int g = 0; g < kGradGroups; ++g) {
+                const int at = begin + (g * kGradThreads + static_cast<int>(threadIdx.x)) * 8;
+                put_group<D>(dz + at, raw_zero<D>(), a.V - at);
+            }
+            continue;
+        }
+        Raw<Z> raw[kGradGroups];
+#pragma unroll
+        for (int g = 0; g < kGradGroups; ++g) {
+            const int at = begin + (g * kGradThreads + static_cast<int>(threadIdx.x)) * 8, n = a.V - at;
+            raw[g] = n >= 8 ? get8<Z>(z + at) : n > 0 ? get_few<Z>(z + at, n) : raw_zero<Z>();
+        }
+        // scale * (dlogp + dentropy * (logp + entropy)) as a line in log2(p)
+        const float l2 = L * kLog2e, slope = a.scale * by_entropy * kLn2;
+        const float level = a.scale * (own + (kEntropy ? by_entropy * a.entropy[row] : 0.0f));
+        const float extra = a.scale * own;
+#pragma unroll
+        for (int g = 0; g < kGradGroups; ++g) {
+            const int at = begin + (g * kGradThreads + static_cast<int>(threadIdx.x)) * 8;
+            float x[8];
+            open8<Z>(raw[g], x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float d = __builtin_fmaf(x[i] - M, a.c, -l2);
+                const float weight = kEntropy ? __builtin_fmaf(__builtin_fmaxf(d, kNothing), slope, level) : level;
+                x[i] = -exp2_of(d) * weight;
+            }
+            if (given && static_cast<uint32_t>(target - at) < 8u) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i == target - at) x[i] += extra;
+            }
+            put_group<D>(dz + at, close8<D>(x), a.V - at);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ host
+int check(int64_t N, int64_t V, int64_t ld, const void *Z, int32_t type, float scale, const int32_t *target,
+          const char *who, Block *z) {
+    SFT_CHECK(N >= 0 && V >= 0, SFT_EINVAL, "%s: negative size", who);
+    SFT_CHECK(V > 0, SFT_ESHAPE, "%s: V = 0", who);
+    SFT_CHECK(V < (int64_t(1) << 30), SFT_ENOTSUP, "%s: V >= 2^30", who);
+    SFT_CHECK(N < (int64_t(1) << 31), SFT_ENOTSUP, "%s: N >= 2^31", who);
+    SFT_CHECK(ld >= V, SFT_ESHAPE, "%s: rows of Z are closer than V", who);
+    SFT_CHECK(ld < (int64_t(1) << 40), SFT_ENOTSUP, "%s: rows of Z are 2^40 elements apart or more", who);
+    SFT_CHECK(type == SFT_F32 || type == SFT_BF16, SFT_EINVAL, "%s: bad type %d", who, type);
+    SFT_CHECK(scale > 0.0f && std::isfinite(scale), SFT_EINVAL, "%s: scale is not positive and finite", who);
+    SFT_CHECK(Z || N == 0, SFT_EINVAL, "%s: Z is null", who);
+    SFT_CHECK(aligned_to(Z, type_bytes(type)), SFT_EALIGN, "%s: Z not aligned to its type", who);
+    SFT_CHECK(aligned_to(target, 4), SFT_EALIGN, "%s: target not 4-byte aligned", who);
+    *z = rows_block(Z, N, ld, V, type_bytes(type));
+    SFT_CHECK(extent(*z) >= 0, SFT_ENOTSUP, "%s: Z spans 2^46 bytes or more", who);
+    return SFT_OK;
+}
+
+constexpr int64_t kMaxGrid = 1 << 21;
+
+float scaled(float scale) { return static_cast<float>(double(scale) * 1.4426950408889634074); }
+
+template <class Z, int kThreads>
+void send(const Logprob &a, hipStream_t st) {
+    const dim3 grid(static_cast<uint32_t>(std::min<int64_t>(a.N, kMaxGrid))), block(kThreads);
+    if (a.entropy && a.top) hipLaunchKernelGGL((k_logprob<Z, kThreads, true, true>), grid, block, 0, st, a);
+    else if (a.entropy) hipLaunchKernelGGL((k_logprob<Z, kThreads, true, false>), grid, block, 0, st, a);
+    else if (a.top) hipLaunchKernelGGL((k_logprob<Z, kThreads, false, true>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((k_logprob<Z, kThreads, false, false>), grid, block, 0, st, a);
+}
+
+template <class Z>
+void send(const Logprob &a, hipStream_t st) {
+    if (a.V <= 2048) send<Z, 64>(a, st);
+    else if (a.N < 2 * num_cus() && a.V >= 16384) send<Z, 1024>(a, st);
+    else send<Z, 256>(a, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+int sft_logprob(const sft_logprob_args *v, void *stream) {
+    const char *const who = "sft_logprob";
+    clear_error();
+    SFT_CHECK(v, SFT_EINVAL, "%s: args is null", who);
+    Block z;
+    if (int rc = check(v->N, v->V, v->ldz, v->Z, v->z_type, v->scale, v->target, who, &z)) return rc;
+    SFT_CHECK(std::isfinite(scaled(v->scale)), SFT_EINVAL, "%s: scale is too large", who);
+    SFT_CHECK(v->top_k >= 0 && v->top_k <= kMaxTop, SFT_EINVAL, "%s: top_k outside [0, %d]", who, kMaxTop);
+    SFT_CHECK(v->N == 0 || !v->target == !v->logp, SFT_EINVAL, "%s: one of target and logp is null", who);
+    SFT_CHECK(v->N == 0 || v->top_index || !v->top_k, SFT_EINVAL, "%s: top_index is null", who);
+    SFT_CHECK(aligned_to(v->logp, 4) && aligned_to(v->stats, 4) && aligned_to(v->entropy, 4) &&
+                  aligned_to(v->top_logp, 4) && aligned_to(v->top_index, 4),
+              SFT_EALIGN, "%s: an output not 4-byte aligned", who);
+    const int64_t tops = v->N * v->top_k * 4;
+    const Block written[] = {flat_block(v->logp, v->N * 4), flat_block(v->stats, v->N * 8),
+                             flat_block(v->entropy, v->N * 4), flat_block(v->top_logp, tops),
+                             flat_block(v->top_index, tops)};
+    const Block target = flat_block(v->target, v->N * 4);
+    for (int i = 0; i < 5; ++i) {
+        for (int j = 0; j < i; ++j)
+            SFT_CHECK(apart(written[i], written[j]), SFT_EINVAL, "%s: two outputs overlap", who);
+        SFT_CHECK(apart(written[i], z) && apart(written[i], target), SFT_EINVAL, "%s: an output overlaps an input", who);
+    }
+    if (v->N == 0) return SFT_OK;
+    Logprob a{};
+    a.z = v->Z, a.target = v->target, a.logp = v->logp, a.stats = v->stats, a.entropy = v->entropy;
+    a.top_logp = v->top_logp, a.top_index = v->top_index;
+    a.ld = v->ldz;
+    a.N = static_cast<int32_t>(v->N), a.V = static_cast<int32_t>(v->V), a.top = v->top_k;
+    a.scale = v->scale, a.c = scaled(v->scale);
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    if (v->z_type == SFT_BF16) send<Bf16>(a, st);
+    else send<Fp32>(a, st);
+    const hipError_t e = hipGetLastError();
+    SFT_CHECK(e == hipSuccess, SFT_EHIP, "%s: launch failed: %s", who, hipGetErrorString(e));
+    return SFT_OK;
+}
+
+int sft_logprob_grad(const sft_logprob_grad_args *v, void *stream) {
+    const char *const who = "sft_logprob_grad";
+    clear_error();
+    SFT_CHECK(v, SFT_EINVAL, "%s: args is null", who);
+    Block z;
+    if (int rc = check(v->N, v->V, v->ldz, v->Z, v->z_type, v->scale, v->target, who, &z)) return rc;
+    SFT_CHECK(std::isfinite(scaled(v->scale)), SFT_EINVAL, "%s: scale is too large", who);
+    SFT_CHECK(v->dz_type == v->z_type || v->dz_type == SFT_BF16, SFT_EINVAL, "%s: bad type of dZ", who);
+    SFT_CHECK(v->lddz >= v->V, SFT_ESHAPE, "%s: rows of dZ are closer than V", who);
+    SFT_CHECK(v->lddz < (int64_t(1) << 40), SFT_ENOTSUP, "%s: rows of dZ are 2^40 elements apart or more", who);
+    SFT_CHECK(v->N == 0 || (v->dZ && v->stats), SFT_EINVAL, "%s: dZ or stats is null", who);
+    SFT_CHECK(v->N == 0 || !v->target == !v->dlogp, SFT_EINVAL, "%s: one of target and dlogp is null", who);
+    SFT_CHECK(v->N == 0 || !v->entropy == !v->dentropy, SFT_EINVAL, "%s: one of entropy and dentropy is null", who);
+    SFT_CHECK(aligned_to(v->dZ, type_bytes(v->dz_type)) && aligned_to(v->stats, 4) && aligned_to(v->entropy, 4) &&
+                  aligned_to(v->dlogp, 4) && aligned_to(v->dentropy, 4),
+              SFT_EALIGN, "%s: an array not aligned to its type", who);
+    const Block dz = rows_block(v->dZ, v->N, v->lddz, v->V, type_bytes(v->dz_type));
+    SFT_CHECK(extent(dz) >= 0, SFT_ENOTSUP, "%s: dZ spans 2^46 bytes or more", who);
+    SFT_CHECK(same(dz, z) || apart(dz, z), SFT_EINVAL, "%s: dZ overlaps Z", who);
+    for (const Block &b : {flat_block(v->target, v->N * 4), flat_block(v->stats, v->N * 8),
+                           flat_block(v->entropy, v->N * 4), flat_block(v->dlogp, v->N * 4),
+                           flat_block(v->dentropy, v->N * 4)})
+        SFT_CHECK(apart(dz, b), SFT_EINVAL, "%s: dZ overlaps an input", who);
+    if (v->N == 0) return SFT_OK;
+    LogprobGrad a{};
+    a.z = v->Z, a.target = v->target, a.stats = v->stats, a.entropy = v->entropy;
+    a.dlogp = v->dlogp, a.dentropy = v->dentropy, a.dz = v->dZ;
+    a.ld = v->ldz, a.ldd = v->lddz;
+    a.N = static_cast<int32_t>(v->N), a.V = static_cast<int32_t>(v->V);
+    a.per_row = static_cast<int32_t>((v->V + kPiece - 1) / kPiece);
+    a.pieces = v->N * a.per_row;
+    a.scale = v->scale, a.c = scaled(v->scale);
+    const dim3 grid(static_cast<uint32_t>(std::min(a.pieces, kMaxGrid * 4))), block(kGradThreads);
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+#define SFT_SEND(Z, D)                                                                                    \
+    do {                                                                                                  \
+        if (v->dentropy) hipLaunchKernelGGL((k_logprob_grad<Z, D, true>), grid, block, 0, st, a);         \
+        else hipLaunchKernelGGL((k_logprob_grad<Z, D, false>), grid, block, 0, st, a);                    \
+    } while (0)
+    if (v->z_type == SFT_BF16) SFT_SEND(Bf16, Bf16);
+    else if (v->dz_type == SFT_BF16) SFT_SEND(Fp32, Bf16);
+    else SFT_SEND(Fp32, Fp32);
+#undef SFT_SEND
+    const hipError_t e = hipGetLastError();
+    SFT_CHECK(e == hipSuccess, SFT_EHIP, "%s: launch failed: %s", who, hipGetErrorString(e));
+    return SFT_OK;
+}
+
+}  // extern "C"

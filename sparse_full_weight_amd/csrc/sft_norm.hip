@@ -1,0 +1,550 @@
+// sft_norm.hip -- layer norm and RMS norm of rows, with the residual's
+// addition, and their backward pass with the gains' and biases' gradients.
+//
+// A row is read once into the registers of a team of lanes, its mean and the
+// squares of the centred values are summed over the team, and the results are
+// written from the same registers: both passes are bound by HBM, and by launch
+// latency where there are few rows.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "sft_blocks.h"
+#include "sft_internal.h"
+#include "sft_vec.h"
+
+namespace {
+
+using namespace sft;
+
+// Lanes of a team, and groups of 8 elements a lane, for rows of up to
+// kLanes * kGroups * 8 elements.  Below 64 lanes several rows share a wave.
+constexpr int kMaxWidth = 16384;
+
+// The sum over a team, in all of its lanes.  red: one float a wave, of its own
+// for each call (no barrier follows the reads).
+template <int kLanes>
+__device__ __forceinline__ float team_sum(float x, float *red) {
+    x = lanes_of<Sum, (kLanes < 64 ? kLanes : 64)>(x);
+    if constexpr (kLanes > 64) {
+        constexpr int kWaves = kLanes / 64;
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
+        __syncthreads();
+        const float *own = red + threadIdx.x / kLanes * kWaves;
+        x = own[0];
+#pragma unroll
+        for (int i = 1; i < kWaves; ++i) x += own[i];
+    }
+    return x;
+}
+
+// Elements of the vectors gain and bias, of either type.
+__device__ __forceinline__ void vector8(const void *v, bool w32, int at, int n, float (&x)[8]) {
+    if (w32) {
+        const float *p = static_cast<const float *>(v) + at;
+        open8<Fp32>(n >= 8 ? get8<Fp32>(p) : get_few<Fp32>(p, n), x);
+    } else {
+        const uint16_t *p = static_cast<const uint16_t *>(v) + at;
+        open8<Bf16>(n >= 8 ? get8<Bf16>(p) : get_few<Bf16>(p, n), x);
+    }
+}
+
+struct NormForward {
+    const void *x, *res;
+    void *h;
+    const void *gain, *bias;
+    void *y;
+    float *mean, *rstd;
+    int64_t ldx, ldr, ldh, ldy;
+    int32_t T, C;
+    float eps;
+    bool layer, w32;
+};
+
+template <class X, class Y, int kLanes, int kGroups>
+__global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes) void k_norm_forward(const NormForward a) {
+    constexpr int kThreads = kLanes < 256 ? 256 : kLanes, kTeams = kThreads / kLanes;
+    __shared__ float red[2][2][kThreads / 64];       // by turns, so that one barrier a sum is enough
+    const int team = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+    const int C = a.C;
+    typedef typename X::type xt;
+    int turn = 0;
+    for (int64_t first = int64_t(blockIdx.x) * kTeams; first < a.T; first += int64_t(gridDim.x) * kTeams, turn ^= 1) {
+        const bool live = first + team < a.T;
+        const int64_t row = live ? first + team : a.T - 1;      // a team without a row stays for the barriers
+        Raw<X> raw[kGroups];
+        get_row<X, kLanes>(static_cast<const xt *>(a.x) + row * a.ldx, lane, C, raw);
+        float x[kGroups][8];
+        if (a.res) {
+            Raw<X> other[kGroups];
+            get_row<X, kLanes>(static_cast<const xt *>(a.res) + row * a.ldr, lane, C, other);
+            xt *h = static_cast<xt *>(a.h) + row * a.ldh;
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+                float y[8];
+                open8<X>(raw[g], x[g]);
+                open8<X>(other[g], y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[g][i] += y[i];
+                const Raw<X> sum = close8<X>(x[g]);
+                open8<X>(sum, x[g]);                    // what is normed is what is kept
+                const int at = (g * kLanes + lane) * 8;
+                if (live) put_group<X>(h + at, sum, C - at);
+            }
+        } else {
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) open8<X>(raw[g], x[g]);
+        }
+        float mean = 0.0f;
+        if (a.layer) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum += x[g][i];       // zeros behind the row's end
+            mean = team_sum<kLanes>(sum, red[turn][0]) / static_cast<float>(C);
+        }
+        float squares = 0.0f;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+            const int n = C - (g * kLanes + lane) * 8;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[g][i] -= mean;
+                if (i < n) squares = __builtin_fmaf(x[g][i], x[g][i], squares);
+            }
+        }
+        squares = team_sum<kLanes>(squares, red[turn][1]);
+        const float rstd = 1.0f / __builtin_sqrtf(squares / static_cast<float>(C) + a.eps);
+        if (!live) continue;
+        if (lane == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+        typename Y::type *y = static_cast<typename Y::type *>(a.y) + row * a.ldy;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+            const int at = (g * kLanes + lane) * 8, n = C - at;
+            if (n <= 0) continue;
+            float w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[g][i] *= rstd;
+            if (a.gain) {
+                vector8(a.gain, a.w32, at, n, w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[g][i] *= w[i];
+            }
+            if (a.bias) {
+                vector8(a.bias, a.w32, at, n, w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[g][i] += w[i];
+            }
+            put_group<Y>(y + at, close8<Y>(x[g]), n);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ backward
+struct NormBackward {
+    const void *h, *gain;
+    const float *mean, *rstd;
+    const void *dy, *dh;
+    void *dx;
+    float *part;                  // [1 or 2][workgroups][C]
+    int64_t ldh, ldy, ldr, ldx;
+    int32_t T, C;
+    bool layer, w32;
+};
+
+// Each team takes rows in turn, kTeams * gridDim.x apart, and keeps its share
+// of the sums over the rows in registers; a workgroup's teams are added at the
+// end, in order, and its sums go to its own place in the workspace.
+// kSums: 0 = no sums over rows, 1 = dgain, 2 = dgain and dbias.
+template <class X, class Y, int kLanes, int kGroups, int kThreads, int kSums>
+__global__ __launch_bounds__(kThreads) void k_norm_backward(const NormBackward a) {
+    constexpr int kTeams = kThreads / kLanes, kWidth = kLanes * kGroups * 8;
+    __shared__ float red[2][2][kThreads / 64];
+    __shared__ float total[kTeams > 1 && kSums ? kSums * kWidth : 1];
+    const int team = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+    const int C = a.C;
+    typedef typename X::type xt;
+    typedef typename Y::type yt;
+    float dgain[kGroups][8], dbias[kGroups][8], gain[kGroups][8];
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+        const int at = (g * kLanes + lane) * 8, n = C - at;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            dgain[g][i] = dbias[g][i] = 0.0f;
+            gain[g][i] = 1.0f;
+        }
+        if (a.gain && n > 0) vector8(a.gain, a.w32, at, n, gain[g]);
+    }
+    const float per = 1.0f / static_cast<float>(C);
+    int turn = 0;
+    for (int64_t first = int64_t(blockIdx.x) * kTeams; first < a.T; first += int64_t(gridDim.x) * kTeams, turn ^= 1) {
+        const bool live = first + team < a.T;
+        const int64_t row = live ? first + team : a.T - 1;
+        Raw<X> rh[kGroups], rr[kGroups];
+        Raw<Y> ry[kGroups];
+        get_row<X, kLanes>(static_cast<const xt *>(a.h) + row * a.ldh, lane, C, rh);
+        get_row<Y, kLanes>(static_cast<const yt *>(a.dy) + row * a.ldy, lane, C, ry);
+        if (a.dh) get_row<X, kLanes>(static_cast<const xt *>(a.dh) + row * a.ldr, lane, C, rr);
+        const float rstd = a.rstd[row], mean = a.layer ? a.mean[row] : 0.0f;
+        float x[kGroups][8], d[kGroups][8];
+        float along = 0.0f, flat = 0.0f;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+            open8<X>(rh[g], x[g]);
+            open8<Y>(ry[g], d[g]);          // zeros behind the row's end
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[g][i] = (x[g][i] - mean) * rstd;
+                if (kSums && live) {
+                    dgain[g][i] = __builtin_fmaf(d[g][i], x[g][i], dgain[g][i]);
+                    if (kSums > 1) dbias[g][i] += d[g][i];
+                }
+                d[g][i] *= gain[g][i];
+                along = __builtin_fmaf(d[g][i], x[g][i], along);
+                flat += d[g][i];
+            }
+        }
+        if constexpr (kLanes > 64) {        // both sums behind one barrier
+            constexpr int kWaves = kLanes / 64;
+            along = lanes_of<Sum, 64>(along);
+            flat = lanes_of<Sum, 64>(flat);
+            if ((threadIdx.x & 63) == 0) {
+                red[turn][0][threadIdx.x >> 6] = along;
+                red[turn][1][threadIdx.x >> 6] = flat;
+            }
+            __syncthreads();                // the other turn's places are read until the next one
+            along = flat = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kWaves; ++i) {
+                along += red[turn][0][team * kWaves + i];
+                flat += red[turn][1][team * kWaves + i];
+            }
+        } else {
+            along = lanes_of<Sum, kLanes>(along);
+            flat = lanes_of<Sum, kLanes>(flat);
+        }
+        along *= per;
+        flat = a.layer ? flat * per : 0.0f;
+        xt *dx = static_cast<xt *>(a.dx) + row * a.ldx;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+            const int at = (g * kLanes + lane) * 8;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d[g][i] = (d[g][i] - flat - x[g][i] * along) * rstd;
+            if (a.dh) {
+                float r[8];
+                open8<X>(rr[g], r);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d[g][i] += r[i];
+            }
+            if (live) put_group<X>(dx + at, close8<X>(d[g]), C - at);
+        }
+    }
+    if constexpr (kSums > 0) {
+        if constexpr (kTeams > 1) {
+            for (int t = 0; t < kTeams - 1; ++t) {
+                __syncthreads();
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int at = (g * kLanes + lane) * 8 + i;
+                        if (team == t) {
+                            total[at] = t ? total[at] + dgain[g][i] : dgain[g][i];
+                            if (kSums > 1) total[kWidth + at] = t ? total[kWidth + at] + dbias[g][i] : dbias[g][i];
+                        }
+                    }
+            }
+            __syncthreads();
+            if (team != kTeams - 1) return;
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int at = (g * kLanes + lane) * 8 + i;
+                    dgain[g][i] += total[at];
+                    if (kSums > 1) dbias[g][i] += total[kWidth + at];
+                }
+        }
+        float *part = a.part + int64_t(blockIdx.x) * C;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+            const int at = (g * kLanes + lane) * 8;
+            put_group<Fp32>(part + at, close8<Fp32>(dgain[g]), C - at);
+            if (kSums > 1) put_group<Fp32>(part + int64_t(gridDim.x) * C + at, close8<Fp32>(dbias[g]), C - at);
+        }
+    }
+}
+
+// The workgroups' sums in a fixed order: 32 columns a workgroup, 8 shares of
+// the rows each.
+constexpr int kReduceColumns = 32, kReduceShares = 8;
+
+struct NormReduce {
+    const float *part;
+    void *out[2];
+    int32_t groups, C;
+    bool g32, accumulate;
+};
+
+__global__ __launch_bounds__(kReduceColumns *kReduceShares) void k_norm_reduce(const NormReduce a) {
+    __shared__ float s[kReduceShares][kReduceColumns];
+    const int column = threadIdx.x % kReduceColumns, share = threadIdx.x / kReduceColumns;
+    const int c = blockIdx.x * kReduceColumns + column;
+    float sum = 0.0f;
+    if (c < a.C && a.out[blockIdx.y]) {
+        const float *p = a.part + int64_t(blockIdx.y) * a.groups * a.C + c;
+#pragma unroll 8
+        for (int g = share; g < a.groups; g += kReduceShares) sum += p[int64_t(g) * a.C];
+    }
+    s[share][column] = sum;
+    __syncthreads();
+    if (share || c >= a.C || !a.out[blockIdx.y]) return;
+    sum = s[0][column];
+#pragma unroll
+    for (int i = 1; i < kReduceShares; ++i) sum += s[i][column];
+    if (a.g32) {
+        float *out = static_cast<float *>(a.out[blockIdx.y]) + c;
+        *out = a.accumulate ? *out + sum : sum;
+    } else {
+        static_cast<uint16_t *>(a.out[blockIdx.y])[c] = Bf16::down(sum);
+    }
+}
+
+// ------------------------------------------------------------------ host
+bool known(int32_t type) { return type == SFT_F32 || type == SFT_BF16; }
+
+int check_sizes(int64_t T, int64_t C, const char *who) {
+    SFT_CHECK(T >= 0 && C >= 0, SFT_EINVAL, "%s: negative size", who);
+    SFT_CHECK(C > 0, SFT_ESHAPE, "%s: C = 0", who);
+    SFT_CHECK(C <= kMaxWidth, SFT_ENOTSUP, "%s: C > %d", who, kMaxWidth);
+    SFT_CHECK(T < (int64_t(1) << 31), SFT_ENOTSUP, "%s: T >= 2^31", who);
+    return SFT_OK;
+}
+
+int check_types(int32_t kind, int32_t x, int32_t w, int32_t y, const char *who) {
+    SFT_CHECK(kind == SFT_NORM_LAYER || kind == SFT_NORM_RMS, SFT_EINVAL, "%s: bad kind %d", who, kind);
+    SFT_CHECK(known(x) && known(w) && known(y) && (y == x || y == SFT_BF16), SFT_EINVAL, "%s: bad type", who);
+    return SFT_OK;
+}
+
+// One array of rows: its pointer, distance and alignment; *b is filled.
+int check_rows(const void *p, int64_t T, int64_t C, int64_t ld, int32_t type, const char *who, const char *name,
+               Block *b) {
+    SFT_CHECK(ld >= C, SFT_ESHAPE, "%s: rows of %s are closer than C", who, name);
+    SFT_CHECK(ld < (int64_t(1) << 40), SFT_ENOTSUP, "%s: rows of %s are 2^40 elements apart or more", who, name);
+    SFT_CHECK(p || T == 0, SFT_EINVAL, "%s: %s is null", who, name);
+    SFT_CHECK(aligned_to(p, type_bytes(type)), SFT_EALIGN, "%s: %s not aligned to its type", who, name);
+    *b = rows_block(p, T, ld, C, type_bytes(type));
+    SFT_CHECK(extent(*b) >= 0, SFT_ENOTSUP, "%s: %s spans 2^46 bytes or more", who, name);
+    return SFT_OK;
+}
+
+int check_apart(const Block *written, int n_written, const Block *read, int n_read, const char *who) {
+    for (int i = 0; i < n_written; ++i) {
+        for (int j = 0; j < i; ++j)
+            SFT_CHECK(apart(written[i], written[j]), SFT_EINVAL, "%s: two written arrays overlap", who);
+        for (int j = 0; j < n_read; ++j)
+            SFT_CHECK(apart(written[i], read[j]), SFT_EINVAL, "%s: a written array overlaps an input", who);
+    }
+    return SFT_OK;
+}
+
+// The widths that each team serves, narrowest first.
+#define SFT_NORM_WIDTHS(go) \
+    go(16, 1) go(32, 1) go(64, 1) go(128, 1) go(256, 1) go(256, 2) go(512, 2) go(1024, 2)
+
+template <class X, class Y>
+void send_forward(const NormForward &a, hipStream_t st) {
+#define SFT_GO(lanes, groups)                                                                             \
+    if (a.C <= lanes * groups * 8) {                                                                      \
+        constexpr int kThreads = lanes < 256 ? 256 : lanes, kTeams = kThreads / lanes;                    \
+        const int64_t rounds = (int64_t(a.T) + kTeams - 1) / kTeams;                                      \
+        const uint32_t grid = static_cast<uint32_t>(std::min<int64_t>(rounds, 1 << 21));                  \
+        hipLaunchKernelGGL((k_norm_forward<X, Y, lanes, groups>), dim3(grid), dim3(kThreads), 0, st, a);  \
+        return;                                                                                           \
+    }
+    SFT_NORM_WIDTHS(SFT_GO)
+#undef SFT_GO
+}
+
+// Workgroups of the backward pass with sums over the rows: their number decides how many partial sums are written and
+// read again.
+int backward_groups(int64_t T, int teams, int threads) {
+    const int64_t rounds = int64_t(num_cus()) * std::max(1, 1024 / threads);
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((T + teams - 1) / teams, rounds)));
+}
+constexpr int backward_threads(int lanes) { return lanes < 512 ? 512 : lanes; }
+
+int backward_groups(int64_t T, int64_t C) {
+#define SFT_GO(lanes, groups) \
+    if (C <= lanes * groups * 8) return backward_groups(T, backward_threads(lanes) / lanes, backward_threads(lanes));
+    SFT_NORM_WIDTHS(SFT_GO)
+#undef SFT_GO
+    return 0;
+}
+
+template <class X, class Y>
+void send_backward(const NormBackward &a, int sums, hipStream_t st) {
+    const dim3 grid(static_cast<uint32_t>(backward_groups(a.T, a.C)));
+#define SFT_GO(lanes, groups)                                                                                       \
+    if (a.C <= lanes * groups * 8) {                                                                                \
+        constexpr int kT = backward_threads(lanes);                                                                 \
+        if (sums == 0) hipLaunchKernelGGL((k_norm_backward<X, Y, lanes, groups, kT, 0>), grid, dim3(kT), 0, st, a); \
+        if (sums == 1) hipLaunchKernelGGL((k_norm_backward<X, Y, lanes, groups, kT, 1>), grid, dim3(kT), 0, st, a); \
+        if (sums == 2) hipLaunchKernelGGL((k_norm_backward<X, Y, lanes, groups, kT, 2>), grid, dim3(kT), 0, st, a); \
+        return;                                                                                                     \
+    }
+    SFT_NORM_WIDTHS(SFT_GO)
+#undef SFT_GO
+}
+
+size_t backward_bytes(int64_t T, int64_t C, bool with_bias) {
+    return size_t(backward_groups(T, C)) * size_t(C) * sizeof(float) * (with_bias ? 2 : 1);
+}
+
+}  // namespace
+
+extern "C" {
+
+int sft_norm_forward(const sft_norm_args *v, void *stream) {
+    const char *const who = "sft_norm_forward";
+    clear_error();
+    SFT_CHECK(v, SFT_EINVAL, "%s: args is null", who);
+    if (int rc = check_sizes(v->T, v->C, who)) return rc;
+    if (int rc = check_types(v->kind, v->x_type, v->w_type, v->y_type, who)) return rc;
+    SFT_CHECK(v->eps >= 0.0f && std::isfinite(v->eps), SFT_EINVAL, "%s: eps is negative or not finite", who);
+    SFT_CHECK(!v->res == !v->H, SFT_EINVAL, "%s: one of res and H is null", who);
+    Block x, res{}, h{}, y;
+    if (int rc = check_rows(v->X, v->T, v->C, v->ldx, v->x_type, who, "X", &x)) return rc;
+    if (int rc = check_rows(v->Y, v->T, v->C, v->ldy, v->y_type, who, "Y", &y)) return rc;
+    if (v->res) {
+        if (int rc = check_rows(v->res, v->T, v->C, v->ldr, v->x_type, who, "res", &res)) return rc;
+        if (int rc = check_rows(v->H, v->T, v->C, v->ldh, v->x_type, who, "H", &h)) return rc;
+    }
+    const int64_t w = type_bytes(v->w_type);
+    SFT_CHECK(aligned_to(v->gain, w) && aligned_to(v->bias, w), SFT_EALIGN, "%s: gain or bias not aligned to its type",
+              who);
+    SFT_CHECK(aligned_to(v->mean, 4) && aligned_to(v->rstd, 4), SFT_EALIGN, "%s: mean or rstd not 4-byte aligned", who);
+    if (v->T == 0) return SFT_OK;
+    const Block gain = flat_block(v->gain, v->C * w), bias = flat_block(v->bias, v->C * w);
+    const Block mean = flat_block(v->mean, v->T * 4), rstd = flat_block(v->rstd, v->T * 4);
+    {
+        // H in the place of X or res: every lane has read what it writes there
+        Block read[4];
+        int n = 0;
+        if (!same(h, x)) read[n++] = x;
+        if (!same(h, res)) read[n++] = res;
+        read[n++] = gain;
+        read[n++] = bias;
+        if (int rc = check_apart(&h, 1, read, n, who)) return rc;
+        const Block written[] = {y, mean, rstd}, all[] = {x, res, h, gain, bias};
+        if (int rc = check_apart(written, 3, all, 5, who)) return rc;
+    }
+    NormForward a{};
+    a.x = v->X, a.res = v->res, a.h = v->H, a.gain = v->gain, a.bias = v->bias, a.y = v->Y;
+    a.mean = v->mean, a.rstd = v->rstd;
+    a.ldx = v->ldx, a.ldr = v->ldr, a.ldh = v->ldh, a.ldy = v->ldy;
+    a.T = static_cast<int32_t>(v->T), a.C = static_cast<int32_t>(v->C);
+    a.eps = v->eps;
+    a.layer = v->kind == SFT_NORM_LAYER;
+    a.w32 = v->w_type == SFT_F32;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    if (v->x_type == SFT_BF16)
+        send_forward<Bf16, Bf16>(a, st);
+    else if (v->y_type == SFT_BF16)
+        send_forward<Fp32, Bf16>(a, st);
+    else
+        send_forward<Fp32, Fp32>(a, st);
+    const hipError_t e = hipGetLastError();
+    SFT_CHECK(e == hipSuccess, SFT_EHIP, "%s: launch failed: %s", who, hipGetErrorString(e));
+    return SFT_OK;
+}
+
+size_t sft_norm_backward_workspace(int64_t T, int64_t C, int32_t with_bias) {
+    clear_error();
+    if (check_sizes(T, C, "sft_norm_backward_workspace")) return static_cast<size_t>(-1);
+    return T ? backward_bytes(T, C, with_bias) : 0;
+}
+
+int sft_norm_backward(const sft_norm_grad_args *v, void *ws, size_t ws_bytes, void *stream) {
+    const char *const who = "sft_norm_backward";
+    clear_error();
+    SFT_CHECK(v, SFT_EINVAL, "%s: args is null", who);
+    if (int rc = check_sizes(v->T, v->C, who)) return rc;
+    if (int rc = check_types(v->kind, v->x_type, v->w_type, v->y_type, who)) return rc;
+    SFT_CHECK(known(v->g_type), SFT_EINVAL, "%s: bad type", who);
+    SFT_CHECK(!v->accumulate || v->g_type == SFT_F32, SFT_EINVAL, "%s: accumulate asks for fp32 gradients", who);
+    const bool layer = v->kind == SFT_NORM_LAYER, sums = v->dgain || v->dbias;
+    SFT_CHECK(v->T == 0 || (v->rstd && (v->mean || !layer)), SFT_EINVAL, "%s: mean or rstd is null", who);
+    Block h, dy, dh{}, dx;
+    if (int rc = check_rows(v->H, v->T, v->C, v->ldh, v->x_type, who, "H", &h)) return rc;
+    if (int rc = check_rows(v->dY, v->T, v->C, v->ldy, v->y_type, who, "dY", &dy)) return rc;
+    if (int rc = check_rows(v->dX, v->T, v->C, v->ldx, v->x_type, who, "dX", &dx)) return rc;
+    if (v->dH)
+        if (int rc = check_rows(v->dH, v->T, v->C, v->ldr, v->x_type, who, "dH", &dh)) return rc;
+    const int64_t w = type_bytes(v->w_type), gs = type_bytes(v->g_type);
+    SFT_CHECK(aligned_to(v->gain, w), SFT_EALIGN, "%s: gain not aligned to its type", who);
+    SFT_CHECK(aligned_to(v->mean, 4) && aligned_to(v->rstd, 4), SFT_EALIGN, "%s: mean or rstd not 4-byte aligned", who);
+    SFT_CHECK(aligned_to(v->dgain, gs) && aligned_to(v->dbias, gs), SFT_EALIGN,
+              "%s: dgain or dbias not aligned to its type", who);
+    const size_t need = sums && v->T ? backward_bytes(v->T, v->C, v->dbias != nullptr) : 0;
+    SFT_CHECK(ws_bytes >= need, SFT_ECAPACITY, "%s: workspace %zu < %zu bytes", who, ws_bytes, need);
+    SFT_CHECK(need == 0 || ws, SFT_EINVAL, "%s: workspace is null", who);
+    SFT_CHECK(aligned16(ws), SFT_EALIGN, "%s: workspace not 16-byte aligned", who);
+    {
+        const Block gain = flat_block(v->gain, v->C * w), mean = flat_block(layer ? v->mean : nullptr, v->T * 4);
+        const Block rstd = flat_block(v->rstd, v->T * 4);
+        const Block written[] = {flat_block(v->dgain, v->C * gs), flat_block(v->dbias, v->C * gs),
+                                 flat_block(need ? ws : nullptr, static_cast<int64_t>(need))};
+        const Block all[] = {h, dy, dh, dx, gain, mean, rstd};
+        if (int rc = check_apart(written, 3, all, 7, who)) return rc;
+        // dX in the place of dY or dH: every lane has read what it writes there
+        Block read[6] = {h, gain, mean, rstd};
+        int n = 4;
+        if (!same(dx, dy)) read[n++] = dy;
+        if (!same(dx, dh)) read[n++] = dh;
+        if (int rc = check_apart(&dx, 1, read, n, who)) return rc;
+    }
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    int groups = 0;
+    if (v->T) {
+        NormBackward a{};
+        a.h = v->H, a.gain = v->gain, a.mean = v->mean, a.rstd = v->rstd, a.dy = v->dY, a.dh = v->dH, a.dx = v->dX;
+        a.part = static_cast<float *>(ws);
+        a.ldh = v->ldh, a.ldy = v->ldy, a.ldr = v->ldr, a.ldx = v->ldx;
+        a.T = static_cast<int32_t>(v->T), a.C = static_cast<int32_t>(v->C);
+        a.layer = layer;
+        a.w32 = v->w_type == SFT_F32;
+        groups = backward_groups(v->T, v->C);
+        const int kind = !sums ? 0 : v->dbias ? 2 : 1;
+        if (v->x_type == SFT_BF16)
+            send_backward<Bf16, Bf16>(a, kind, st);
+        else if (v->y_type == SFT_BF16)
+            send_backward<Fp32, Bf16>(a, kind, st);
+        else
+            send_backward<Fp32, Fp32>(a, kind, st);
+        const hipError_t e = hipGetLastError();
+        SFT_CHECK(e == hipSuccess, SFT_EHIP, "%s: launch failed: %s", who, hipGetErrorString(e));
+    }
+    if (sums) {
+        NormReduce r{};
+        r.part = static_cast<const float *>(ws);
+        r.out[0] = v->dgain, r.out[1] = v->dbias;
+        r.groups = groups, r.C = static_cast<int32_t>(v->C);
+        r.g32 = v->g_type == SFT_F32, r.accumulate = v->accumulate != 0;
+        const dim3 grid(static_cast<uint32_t>((v->C + kReduceColumns - 1) / kReduceColumns), v->dbias ? 2 : 1);
+        hipLaunchKernelGGL(k_norm_reduce, grid, dim3(kReduceColumns * kReduceShares), 0, st, r);
+        const hipError_t e = hipGetLastError();
+        SFT_CHECK(e == hipSuccess, SFT_EHIP, "%s: launch failed: %s", who, hipGetErrorString(e));
+    }
+    return SFT_OK;
+}
+
+}  // extern "C"

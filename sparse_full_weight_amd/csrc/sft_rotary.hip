@@ -1,0 +1,330 @@
+// sft_rotary.hip -- rotary positions: pairs of elements of queries and keys
+// turned by angles that grow with the token's position, and the table of those
+// angles.
+//
+// Every element is read and written once, so the call is bound by HBM.  The
+// sines are the same for all heads of a token: a workgroup takes whole tokens
+// and puts their sines into LDS once.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "sft_blocks.h"
+#include "sft_internal.h"
+#include "sft_vec.h"
+
+namespace {
+
+using namespace sft;
+
+constexpr int kThreads = 256;
+constexpr int kMaxMats = 8;
+constexpr int kMaxHead = 4096;
+// Items (16 elements of a head: 8 pairs, or 16 behind the turned part) that a
+// workgroup takes, unless one token has more: two a thread, whose loads are
+// under way while the sines are computed.
+constexpr int kItems = 2 * kThreads;
+
+// n / d for n < 2^31.
+struct Div {
+    uint32_t mul, shift, by;
+};
+Div div_by(uint32_t d) {
+    uint32_t s = 0;
+    while ((uint64_t(1) << s) < d) ++s;
+    return {static_cast<uint32_t>((uint64_t(1) << (31 + s)) / d + 1), 31 + s, d};
+}
+__device__ __forceinline__ uint32_t over(uint32_t n, const Div &d) {
+    return static_cast<uint32_t>(uint64_t(n) * d.mul >> d.shift);
+}
+
+struct RotaryMat {
+    const void *x;
+    void *y;
+    int64_t x_batch, x_row, x_head, y_batch, y_row, y_head;
+    Div units, heads;           // items of a head; heads
+    int32_t tokens;             // of a workgroup
+    uint32_t begin;             // the first of its workgroups
+};
+
+struct Rotary {
+    RotaryMat m[kMaxMats];
+    const double *freq;
+    const int32_t *pos;
+    int64_t pos_batch;
+    Div rows, pairs;            // tokens of a sequence; pairs of a head
+    int32_t n_mats, D, rot, total;    // total: tokens of all sequences
+    uint32_t blocks;
+    float amplitude;
+    bool inverse;
+};
+
+// One item: two groups of up to 8 elements, where they start in the head and how many there are.
+struct Item {
+    int64_t x, y;               // the head's first element in either array
+    int32_t at0, at1, n0, n1;
+    int32_t angle;              // place of its first pair's sine, or -1: to be copied
+};
+
+template <bool kHalf>
+__device__ __forceinline__ Item item_of(const Rotary &a, const RotaryMat &m, uint32_t i, uint32_t first) {
+    Item it;
+    const int half = a.rot / 2, pair_units = (half + 7) / 8;
+    const uint32_t q = over(i, m.units), t = over(q, m.heads);
+    const int u = static_cast<int>(i - q * m.units.by);
+    const int64_t head = q - t * m.heads.by;
+    const uint32_t token = first + t, b = over(token, a.rows);
+    const int64_t row = token - b * a.rows.by;
+    it.x = b * m.x_batch + row * m.x_row + head * m.x_head;
+    it.y = b * m.y_batch + row * m.y_row + head * m.y_head;
+    if (u < pair_units) {
+        const int n = min(8, half - 8 * u);
+        it.angle = static_cast<int32_t>(t) * half + 8 * u;
+        if constexpr (kHalf) {
+            it.at0 = 8 * u, it.at1 = half + 8 * u;
+            it.n0 = it.n1 = n;
+        } else {
+            it.at0 = 16 * u, it.at1 = 16 * u + 8;
+            it.n0 = min(8, 2 * n), it.n1 = 2 * n - it.n0;
+        }
+    } else {
+        it.angle = -1;
+        it.at0 = a.rot + 16 * (u - pair_units), it.at1 = it.at0 + 8;
+        it.n0 = min(8, a.D - it.at0), it.n1 = max(0, min(8, a.D - it.at1));
+    }
+    return it;
+}
+
+template <class E>
+__device__ __forceinline__ Raw<E> get_group(const typename E::type *p, int n) {
+    if (n >= 8) return get8<E>(p);
+    return n > 0 ? get_few<E>(p, n) : raw_zero<E>();
+}
+
+template <class E, bool kHalf>
+__device__ __forceinline__ void turn_item(const Item &it, const Raw<E> &r0, const Raw<E> &r1, const f32x4 *sines,
+                                          typename E::type *y) {
+    y += it.y;
+    if (it.angle < 0) {
+        put_group<E>(y + it.at0, r0, it.n0);
+        put_group<E>(y + it.at1, r1, it.n1);
+        return;
+    }
+    float u[8], v[8], c[8], s[8];
+    const float *at = reinterpret_cast<const float *>(sines) + 2 * it.angle;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = at[2 * i], s[i] = at[2 * i + 1];
+    open8<E>(r0, u);
+    open8<E>(r1, v);
+    if constexpr (kHalf) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float p = u[i], q = v[i];
+            u[i] = __builtin_fmaf(p, c[i], -(q * s[i]));
+            v[i] = __builtin_fmaf(p, s[i], q * c[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float p = u[2 * i], q = u[2 * i + 1], f = v[2 * i], g = v[2 * i + 1];
+            u[2 * i] = __builtin_fmaf(p, c[i], -(q * s[i]));
+            u[2 * i + 1] = __builtin_fmaf(p, s[i], q * c[i]);
+            v[2 * i] = __builtin_fmaf(f, c[4 + i], -(g * s[4 + i]));
+            v[2 * i + 1] = __builtin_fmaf(f, s[4 + i], g * c[4 + i]);
+        }
+    }
+    put_group<E>(y + it.at0, close8<E>(u), it.n0);
+    put_group<E>(y + it.at1, close8<E>(v), it.n1);
+}
+
+template <class E, bool kHalf>
+__global__ __launch_bounds__(kThreads) void k_rotary(const Rotary a) {
+    extern __shared__ f32x4 sines[];      // cosine and sine of each token's pairs, and room for a last partial item
+    typedef typename E::type type;
+    const int half = a.rot / 2;
+    for (uint32_t block = blockIdx.x; block < a.blocks; block += gridDim.x) {
+        int k = 0;
+        while (k + 1 < a.n_mats && a.m[k + 1].begin <= block) ++k;
+        const RotaryMat &m = a.m[k];
+        const uint32_t first = (block - m.begin) * uint32_t(m.tokens);
+        const uint32_t tokens = min(uint32_t(m.tokens), uint32_t(a.total) - first);
+        const uint32_t items = tokens * m.heads.by * m.units.by;
+        const type *x = static_cast<const type *>(m.x);
+        Item it[2];
+        Raw<E> r0[2], r1[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t i = threadIdx.x + j * kThreads;
+            if (i >= items) continue;
+            it[j] = item_of<kHalf>(a, m, i, first);
+            r0[j] = get_group<E>(x + it[j].x + it[j].at0, it[j].n0);
+            r1[j] = get_group<E>(x + it[j].x + it[j].at1, it[j].n1);
+        }
+        // in turns, of which whole ones do not matter: what is left is exact to fp32 however far the position
+        float *cs = reinterpret_cast<float *>(sines);
+        for (uint32_t i = threadIdx.x; i < tokens * uint32_t(half); i += kThreads) {
+            const uint32_t t = over(i, a.pairs), token = first + t, b = over(token, a.rows);
+            const int32_t pos = a.pos[b * a.pos_batch + (token - b * a.rows.by)];
+            double turns = a.freq[i - t * half] * 0.15915494309189533577 * pos;
+            turns -= __builtin_rint(turns);
+            float s, c;
+            sincospif(static_cast<float>(2.0 * turns), &s, &c);
+            cs[2 * i] = c * a.amplitude;
+            cs[2 * i + 1] = (a.inverse ? -s : s) * a.amplitude;
+        }
+        __syncthreads();
+        for (uint32_t base = 0;;) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (base + threadIdx.x + j * kThreads < items)
+                    turn_item<E, kHalf>(it[j], r0[j], r1[j], sines, static_cast<type *>(m.y));
+            base += kItems;
+            if (base >= items) break;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t i = base + threadIdx.x + j * kThreads;
+                if (i >= items) continue;
+                it[j] = item_of<kHalf>(a, m, i, first);
+                r0[j] = get_group<E>(x + it[j].x + it[j].at0, it[j].n0);
+                r1[j] = get_group<E>(x + it[j].x + it[j].at1, it[j].n1);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+Block heads_block(const void *p, int64_t B, int64_t T, int64_t heads, int64_t batch, int64_t row, int64_t head,
+                  int64_t D, int64_t size) {
+    return Block{p, D * size, {{B, batch * size}, {T, row * size}, {heads, head * size}}};
+}
+
+}  // namespace
+
+extern "C" {
+
+int sft_rotary_table(int64_t rot, double base, int32_t kind, double factor, double context, double low, double high,
+                     double *freq) {
+    const char *const who = "sft_rotary_table";
+    clear_error();
+    SFT_CHECK(freq, SFT_EINVAL, "%s: freq is null", who);
+    SFT_CHECK(kind >= SFT_ROTARY_PLAIN && kind <= SFT_ROTARY_BANDS, SFT_EINVAL, "%s: bad kind %d", who, kind);
+    SFT_CHECK(rot >= 2 && rot % 2 == 0, SFT_ESHAPE, "%s: rot is odd or below 2", who);
+    SFT_CHECK(std::isfinite(base) && base > 0.0, SFT_EINVAL, "%s: base is not positive and finite", who);
+    SFT_CHECK(std::isfinite(factor) && factor >= 1.0, SFT_EINVAL, "%s: factor is below 1 or not finite", who);
+    if (kind == SFT_ROTARY_BANDS) {
+        SFT_CHECK(std::isfinite(context) && context > 0.0, SFT_EINVAL, "%s: context is not positive and finite", who);
+        SFT_CHECK(std::isfinite(low) && std::isfinite(high) && high > low, SFT_EINVAL,
+                  "%s: low and high are not finite and ascending", who);
+    }
+    const double n = static_cast<double>(rot);
+    if (kind == SFT_ROTARY_BASE && rot > 2) base *= std::pow(factor, n / (n - 2.0));
+    SFT_CHECK(std::isfinite(base), SFT_EINVAL, "%s: base * factor^(rot/(rot-2)) is not finite", who);
+    for (int64_t j = 0; j < rot / 2; ++j) {
+        double f = std::pow(base, -2.0 * static_cast<double>(j) / n);
+        if (kind == SFT_ROTARY_LINEAR) f /= factor;
+        if (kind == SFT_ROTARY_BANDS) {
+            const double turns = context * f / 6.283185307179586477;
+            const double w = std::min(1.0, std::max(0.0, (turns - low) / (high - low)));
+            f *= w + (1.0 - w) / factor;
+        }
+        freq[j] = f;
+    }
+    return SFT_OK;
+}
+
+int sft_rotary(const sft_rotary_mat *mats, int32_t n_mats, int64_t B, int64_t T, int64_t D, int64_t rot,
+               const double *freq, const int32_t *pos, int64_t pos_batch, float amplitude, int32_t layout,
+               int32_t inverse, int32_t type, void *stream) {
+    const char *const who = "sft_rotary";
+    clear_error();
+    SFT_CHECK(n_mats >= 0 && (n_mats == 0 || mats), SFT_EINVAL, "%s: bad list", who);
+    SFT_CHECK(n_mats <= kMaxMats, SFT_ENOTSUP, "%s: more than %d arrays", who, kMaxMats);
+    SFT_CHECK(B >= 0 && T >= 0 && D >= 0 && pos_batch >= 0, SFT_EINVAL, "%s: negative size or distance", who);
+    SFT_CHECK(D <= kMaxHead, SFT_ENOTSUP, "%s: D > %d", who, kMaxHead);
+    SFT_CHECK(B < (int64_t(1) << 30) && T < (int64_t(1) << 30) && B * T < (int64_t(1) << 30), SFT_ENOTSUP,
+              "%s: 2^30 tokens or more", who);
+    SFT_CHECK(rot >= 2 && rot % 2 == 0 && rot <= D, SFT_ESHAPE, "%s: rot is odd, below 2 or above D", who);
+    SFT_CHECK(type == SFT_F32 || type == SFT_BF16, SFT_EINVAL, "%s: bad type %d", who, type);
+    SFT_CHECK(layout == SFT_ROTARY_HALF || layout == SFT_ROTARY_PAIRS, SFT_EINVAL, "%s: bad layout %d", who, layout);
+    SFT_CHECK(std::isfinite(amplitude), SFT_EINVAL, "%s: amplitude is not finite", who);
+    const int64_t total = B * T, size = type_bytes(type), most = int64_t(1) << 40;
+    const bool any = n_mats && total;
+    SFT_CHECK(!any || (freq && pos), SFT_EINVAL, "%s: freq or pos is null", who);
+    SFT_CHECK(aligned_to(freq, 8) && aligned_to(pos, 4), SFT_EALIGN, "%s: freq or pos not aligned to its type", who);
+    SFT_CHECK(pos_batch < most, SFT_ENOTSUP, "%s: a distance of 2^40 or more", who);
+    Block x[kMaxMats], y[kMaxMats];
+    for (int32_t i = 0; i < n_mats; ++i) {
+        const sft_rotary_mat &m = mats[i];
+        SFT_CHECK(m.heads >= 0, SFT_EINVAL, "%s: array %d: negative size", who, i);
+        SFT_CHECK(m.heads < (1 << 16), SFT_ENOTSUP, "%s: array %d: 2^16 heads or more", who, i);
+        for (int64_t d : {m.x_batch, m.x_row, m.x_head, m.y_batch, m.y_row, m.y_head}) {
+            SFT_CHECK(d >= 0, SFT_EINVAL, "%s: array %d: negative distance", who, i);
+            SFT_CHECK(d < most, SFT_ENOTSUP, "%s: array %d: a distance of 2^40 or more", who, i);
+        }
+        SFT_CHECK(m.heads == 0 || !any || (m.X && m.Y), SFT_EINVAL, "%s: array %d: null pointer", who, i);
+        SFT_CHECK(aligned_to(m.X, size) && aligned_to(m.Y, size), SFT_EALIGN, "%s: array %d not aligned to its type",
+                  who, i);
+        x[i] = heads_block(m.X, B, T, m.heads, m.x_batch, m.x_row, m.x_head, D, size);
+        y[i] = heads_block(m.Y, B, T, m.heads, m.y_batch, m.y_row, m.y_head, D, size);
+        SFT_CHECK(extent(x[i]) >= 0 && extent(y[i]) >= 0, SFT_ENOTSUP, "%s: array %d spans 2^46 bytes or more", who, i);
+        SFT_CHECK(apart_within(y[i]), SFT_EINVAL, "%s: array %d: heads of Y overlap", who, i);
+    }
+    const Block table = flat_block(freq, rot / 2 * 8);
+    const Block where{pos, T * 4, {{pos_batch ? B : 1, pos_batch * 4}, {1, 0}, {1, 0}}};
+    SFT_CHECK(extent(where) >= 0, SFT_ENOTSUP, "%s: pos spans 2^46 bytes or more", who);
+    for (int32_t i = 0; i < n_mats && total; ++i) {
+        SFT_CHECK(apart(y[i], table) && apart(y[i], where), SFT_EINVAL, "%s: array %d overlaps freq or pos", who, i);
+        for (int32_t j = 0; j < n_mats; ++j) {
+            SFT_CHECK(i == j || apart(y[i], y[j]), SFT_EINVAL, "%s: two written arrays overlap", who);
+            SFT_CHECK((i == j && same(y[i], x[j])) || apart(y[i], x[j]), SFT_EINVAL,
+                      "%s: a written array overlaps an input", who);
+        }
+    }
+    if (!any) return SFT_OK;
+    Rotary a{};
+    const int64_t half = rot / 2, pair_units = (half + 7) / 8;
+    int64_t blocks = 0, sines = 0;
+    for (int32_t i = 0; i < n_mats; ++i) {
+        const sft_rotary_mat &m = mats[i];
+        if (m.heads == 0) continue;
+        RotaryMat &r = a.m[a.n_mats++];
+        // what lies behind the turned part stays where it is when Y is X
+        const int64_t units = pair_units + (same(x[i], y[i]) ? 0 : (D - rot + 15) / 16);
+        r.x = m.X, r.y = m.Y;
+        r.x_batch = m.x_batch, r.x_row = m.x_row, r.x_head = m.x_head;
+        r.y_batch = m.y_batch, r.y_row = m.y_row, r.y_head = m.y_head;
+        r.units = div_by(static_cast<uint32_t>(units));
+        r.heads = div_by(static_cast<uint32_t>(m.heads));
+        const int64_t tokens = std::max<int64_t>(1, std::min<int64_t>(total, kItems / (units * m.heads)));
+        r.tokens = static_cast<int32_t>(tokens);
+        r.begin = static_cast<uint32_t>(blocks);
+        blocks += (total + tokens - 1) / tokens;
+        sines = std::max(sines, tokens * half);
+    }
+    SFT_CHECK(blocks < (int64_t(1) << 31), SFT_ENOTSUP, "%s: too many tokens and arrays", who);
+    if (!blocks) return SFT_OK;
+    a.freq = freq, a.pos = pos, a.pos_batch = pos_batch;
+    a.rows = div_by(static_cast<uint32_t>(T));
+    a.pairs = div_by(static_cast<uint32_t>(half));
+    a.D = static_cast<int32_t>(D), a.rot = static_cast<int32_t>(rot), a.total = static_cast<int32_t>(total);
+    a.blocks = static_cast<uint32_t>(blocks);
+    a.amplitude = amplitude;
+    a.inverse = inverse != 0;
+    const dim3 grid(static_cast<uint32_t>(std::min<int64_t>(blocks, 1 << 23))), block(kThreads);
+    const size_t lds = static_cast<size_t>(sines + 8) * 8;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const bool in_half = layout == SFT_ROTARY_HALF;
+    if (type == SFT_BF16) {
+        if (in_half) hipLaunchKernelGGL((k_rotary<Bf16, true>), grid, block, lds, st, a);
+        else hipLaunchKernelGGL((k_rotary<Bf16, false>), grid, block, lds, st, a);
+    } else {
+        if (in_half) hipLaunchKernelGGL((k_rotary<Fp32, true>), grid, block, lds, st, a);
+        else hipLaunchKernelGGL((k_rotary<Fp32, false>), grid, block, lds, st, a);
+    }
+    const hipError_t e = hipGetLastError();
+    SFT_CHECK(e == hipSuccess, SFT_EHIP, "%s: launch failed: %s", who, hipGetErrorString(e));
+    return SFT_OK;
+}
+
+}  // extern "C"
