@@ -46,6 +46,9 @@ __device__ __forceinline__ uint32_t order_of(float x) {
     const uint32_t b = float_bits(x + 0.0f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
+__device__ __forceinline__ float float_of(uint32_t order) {
+    return bits_float(order & 0x80000000u ? order & 0x7fffffffu : ~order);
+}
 // Larger for a larger logit, of equal ones for the lower index.
 __device__ __forceinline__ uint64_t key_of(float z, uint32_t at) { return uint64_t(order_of(z)) << 32 | (0xffffffffu - at); }
 
@@ -64,14 +67,12 @@ struct Running {
     float m, m2, sum, along;
 };
 
-// Takes up U groups of logits.
-template <bool kEntropy, int U>
-__device__ __forceinline__ void take_up(Running &r, const float (&z)[U][8], float c) {
+// Takes up n logits.
+template <bool kEntropy, int n>
+__device__ __forceinline__ void take_up(Running &r, const float (&z)[n], float c) {
     float m = r.m;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) m = max3(m, z[u][i], z[u][i + 1]);
+    for (int i = 0; i < n; i += 2) m = max3(m, z[i], z[i + 1]);
     const float m2 = __builtin_fmaxf(m * c, -kFar);       // (of minus infinity as well)
     const float less = limit(r.m2 - m2, kNothing, 0.0f), part = exp2_of(less);
     r.along = kEntropy ? part * __builtin_fmaf(r.sum, less, r.along) : 0.0f;
@@ -79,13 +80,11 @@ __device__ __forceinline__ void take_up(Running &r, const float (&z)[U][8], floa
     r.m = m;
     r.m2 = m2;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float d = __builtin_fmaf(z[u][i], c, -m2), e = exp2_of(d);
-            r.sum += e;
-            if (kEntropy) r.along = __builtin_fmaf(e, __builtin_fmaxf(d, kNothing), r.along);
-        }
+    for (int i = 0; i < n; ++i) {
+        const float d = __builtin_fmaf(z[i], c, -m2), e = exp2_of(d);
+        r.sum += e;
+        if (kEntropy) r.along = __builtin_fmaf(e, __builtin_fmaxf(d, kNothing), r.along);
+    }
 }
 
 template <class Op, int kThreads>
@@ -115,6 +114,16 @@ __device__ __forceinline__ float logit(const typename Z::type *z, int at) {
     return Z::up(z[at]);
 }
 
+// How a row's logits are shared out: those before the first whole cache line
+// one each to the first threads, then groups by turns, as many turns at a time
+// as make kRound logits of a thread.
+constexpr int kRound = 32;
+
+template <class Z, int kThreads>
+__device__ __forceinline__ int place_of(int head, int turn, int thread) {
+    return head + (turn * kThreads + thread) * Z::kGroup;
+}
+
 struct TopPlace {
     float threshold;
     int owners, found;
@@ -122,21 +131,25 @@ struct TopPlace {
 
 // The K likeliest of a row, of which every thread knows the largest logit that
 // it has seen.  The K-th largest of those is a bound that at least K logits
-// reach, so only threads whose own largest reaches it have alternatives; their
-// logits are read again (a few of them, by the whole workgroup, out of the
-// caches), those that reach the bound are collected and ranked by counting.
-// Where too many do, or a NaN may have hidden a thread's largest, the
-// alternatives are looked for one by one.
-template <class Z, int kThreads>
-__device__ void top_of(const Logprob &a, int64_t row, float mine, bool plain, float M, float L, float *most,
-                       int32_t *owner, uint64_t *found, TopPlace *place) {
+// reach, so only threads whose own largest reaches it have alternatives.  Their
+// logits that reach the bound are collected and ranked by counting; those of
+// rows of one round of turns are still at hand (kHeld), others are read again (a
+// few of them, by the whole workgroup, out of the caches).  Where too many
+// do, or a NaN may have hidden a thread's largest, the alternatives are looked
+// for one by one.
+template <class Z, int kThreads, bool kHeld>
+__device__ __forceinline__ void top_of(const Logprob &a, int64_t row, float mine, bool plain, float M, float L,
+                                       const float (&last)[kRound], int head, float *most, int32_t *owner,
+                                       uint64_t *found, TopPlace *place) {
+    constexpr int N = Z::kGroup, kSteps = kRound / N;
     const typename Z::type *z = static_cast<const typename Z::type *>(a.z) + row * a.ld;
     float *top_logp = a.top_logp ? a.top_logp + row * a.top : nullptr;
     int32_t *top_index = a.top_index + row * a.top;
     const auto tell = [&](int rank, uint64_t key) {
         const int at = static_cast<int>(0xffffffffu - static_cast<uint32_t>(key));
+        const uint32_t o = static_cast<uint32_t>(key >> 32);
         top_index[rank] = at;
-        if (top_logp) top_logp[rank] = a.scale * (logit<Z>(z, at) - M) - L;
+        if (top_logp) top_logp[rank] = a.scale * (float_of(o) - M) - L;
     };
     const auto nothing = [&](int rank) {
         top_index[rank] = -1;
@@ -153,27 +166,45 @@ __device__ void top_of(const Logprob &a, int64_t row, float mine, bool plain, fl
             for (int i = 1; i < kThreads / 64; ++i) x = __builtin_fmaxf(x, most[threadIdx.x + 64 * i]);
             const uint32_t o = order_of(x);
             uint32_t bound = 0;
-            for (uint32_t bit = 1u << 31; bit; bit >>= 1)
-                if (__builtin_popcountll(__ballot(o >= (bound | bit))) >= a.top) bound |= bit;
-            if (threadIdx.x == 0)
-                place->threshold = bits_float(bound & 0x80000000u ? bound & 0x7fffffffu : ~bound);
+            for (uint32_t bit = 1u << 31; bit; bit >>= 1) {
+                const int reach = __builtin_popcountll(__ballot(o >= (bound | bit)));
+                if (reach >= a.top) bound |= bit;
+                if (reach == a.top) break;
+            }
+            if (threadIdx.x == 0) place->threshold = float_of(max(bound, order_of(-kInf)));
         }
         __syncthreads();
         const float threshold = place->threshold;
-        if (mine >= threshold && mine > -kInf) owner[atomicAdd(&place->owners, 1)] = threadIdx.x;
-        __syncthreads();
-        const int owners = place->owners, groups = (a.V + kThreads * 8 - 1) / (kThreads * 8);
-        for (int p = threadIdx.x; p < owners * groups; p += kThreads) {
-            const int g = p / owners, at = (g * kThreads + owner[p - g * owners]) * 8, n = a.V - at;
-            if (n <= 0) continue;
-            float x[8];
-            open8<Z>(n >= 8 ? get8<Z>(z + at) : get_few<Z>(z + at, n), x);
+        const auto collect = [&](float x, int at) {
+            if (x >= threshold && x > -kInf) {
+                const int k = atomicAdd(&place->found, 1);
+                if (k < kCandidates) found[k] = key_of(x, at);
+            }
+        };
+        const bool has = mine >= threshold && mine > -kInf;
+        const int turns = (a.V - head + kThreads * N - 1) / (kThreads * N);
+        if (has && static_cast<int>(threadIdx.x) < head) collect(logit<Z>(z, threadIdx.x), threadIdx.x);
+        if constexpr (kHeld) {
+            if (has && turns > 0) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < n && x[i] >= threshold && x[i] > -kInf) {
-                    const int k = atomicAdd(&place->found, 1);
-                    if (k < kCandidates) found[k] = key_of(x[i], at + i);
-                }
+                for (int u = 0; u < kSteps; ++u)
+#pragma unroll
+                    for (int i = 0; i < N; ++i)       // -infinity behind the row's end
+                        collect(last[u * N + i], place_of<Z, kThreads>(head, u, threadIdx.x) + i);
+            }
+        } else {
+            if (has) owner[atomicAdd(&place->owners, 1)] = threadIdx.x;
+            __syncthreads();
+            const int owners = place->owners;
+            for (int p = threadIdx.x; p < owners * turns; p += kThreads) {
+                const int g = p / owners, at = place_of<Z, kThreads>(head, g, owner[p - g * owners]), n = a.V - at;
+                if (n <= 0) continue;
+                float x[N];
+                open<Z, N>(get_group<Z, N>(z + at, n), x);
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (i < n) collect(x[i], at + i);
+            }
         }
         __syncthreads();
         const int n = place->found;
@@ -188,17 +219,17 @@ __device__ void top_of(const Logprob &a, int64_t row, float mine, bool plain, fl
             return;
         }
     }
-    uint64_t last = ~uint64_t(0);
+    uint64_t before = ~uint64_t(0);
     for (int rank = 0; rank < a.top; ++rank) {
         uint64_t best = 0;
-        for (int at = threadIdx.x * 8; at < a.V; at += kThreads * 8) {
-            float x[8];
+        for (int at = threadIdx.x * N; at < a.V; at += kThreads * N) {
+            float x[N];
             const int n = a.V - at;
-            open8<Z>(n >= 8 ? get8<Z>(z + at) : get_few<Z>(z + at, n), x);
+            open<Z, N>(get_group<Z, N>(z + at, n), x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < N; ++i) {
                 const uint64_t key = key_of(x[i], at + i);
-                if (i < n && x[i] > -kInf && key < last && key > best) best = key;
+                if (i < n && x[i] > -kInf && key < before && key > best) best = key;
             }
         }
         best = wave_max(best);
@@ -213,42 +244,63 @@ __device__ void top_of(const Logprob &a, int64_t row, float mine, bool plain, fl
             else
                 nothing(rank);
         }
-        last = best;
+        before = best;
     }
 }
 
-template <class Z, int kThreads, bool kEntropy, bool kTop>
+// kTop: 0 = no alternatives, 1 = of rows of at most one round, 2 = of any.
+template <class Z, int kThreads, bool kEntropy, int kTop>
 __global__ __launch_bounds__(kThreads) void k_logprob(const Logprob a) {
-    constexpr int kWaves = kThreads / 64, U = 4;
+    constexpr int kWaves = kThreads / 64, N = Z::kGroup, kSteps = kRound / N;
     __shared__ float red[3][kWaves];
     __shared__ float most[kTop ? kThreads : 1];
     __shared__ int32_t owner[kTop ? kThreads : 1];
     __shared__ uint64_t found[kTop ? kCandidates : 1];
     __shared__ TopPlace place;
+    const int thread = static_cast<int>(threadIdx.x);
     for (int64_t row = blockIdx.x; row < a.N; row += gridDim.x) {
         const typename Z::type *z = static_cast<const typename Z::type *>(a.z) + row * a.ld;
         const int target = a.target ? a.target[row] : -1;
         const bool given = target >= 0 && target < a.V;
         const float at_target = given ? logit<Z>(z, target) : 0.0f;
+        const int head = kThreads > 64 ? before_line<Z>(z, a.V) : 0;     // (a short row's few loads may cross lines)
         Running r{-kInf, -kFar, 0.0f, 0.0f};
-        int at = threadIdx.x * 8;
-        for (int base = 0; base + U * kThreads * 8 <= a.V; base += U * kThreads * 8, at += U * kThreads * 8) {
-            Raw<Z> raw[U];
+        float x[kRound];
+        Raw<Z, N> raw[kSteps];
+        int turn = 0;
+        for (; place_of<Z, kThreads>(head, turn + kSteps, 0) <= a.V; turn += kSteps) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) raw[u] = get8<Z>(z + at + u * kThreads * 8);
-            float x[U][8];
+            for (int u = 0; u < kSteps; ++u) raw[u] = get<Z, N, true>(z + place_of<Z, kThreads>(head, turn + u, thread));
 #pragma unroll
-            for (int u = 0; u < U; ++u) open8<Z>(raw[u], x[u]);
-            take_up<kEntropy, U>(r, x, a.c);
+            for (int u = 0; u < kSteps; ++u) open<Z, N>(raw[u], x + u * N);
+            take_up<kEntropy>(r, x, a.c);
         }
-        for (; at < a.V; at += kThreads * 8) {
-            float x[1][8];
-            const int n = a.V - at;
-            open8<Z>(n >= 8 ? get8<Z>(z + at) : get_few<Z>(z + at, n), x[0]);
+        float first[2] = {-kInf, -kInf};
+        if (thread < head) first[0] = logit<Z>(z, thread);
+        if (place_of<Z, kThreads>(head, turn, 0) < a.V) {       // the last round
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[0][i] = i < n ? x[0][i] : -kInf;
-            take_up<kEntropy, 1>(r, x, a.c);
+            for (int u = 0; u < kSteps; ++u) {
+                const int at = place_of<Z, kThreads>(head, turn + u, thread);
+                raw[u] = raw_zero<Z, N>();
+                if (at + N <= a.V) raw[u] = get<Z, N, true>(z + at);
+            }
+#pragma unroll
+            for (int u = 0; u < kSteps; ++u) {
+                const int at = place_of<Z, kThreads>(head, turn + u, thread), n = a.V - at;
+                if (n > 0 && n < N) raw[u] = get_few<Z, N>(z + at, n);
+            }
+#pragma unroll
+            for (int u = 0; u < kSteps; ++u) {
+                const int n = a.V - place_of<Z, kThreads>(head, turn + u, thread);
+                open<Z, N>(raw[u], x + u * N);
+                if (n < N) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) x[u * N + i] = i < n ? x[u * N + i] : -kInf;
+                }
+            }
+            take_up<kEntropy>(r, x, a.c);
         }
+        if (head) take_up<kEntropy>(r, first, a.c);
         float M = block_of<Max, kThreads>(r.m, red[0]);
         const float m2 = __builtin_fmaxf(M * a.c, -kFar);
         const float less = limit(r.m2 - m2, kNothing, 0.0f), part = exp2_of(less);
@@ -259,7 +311,7 @@ __global__ __launch_bounds__(kThreads) void k_logprob(const Logprob a) {
         const bool finite = __builtin_fabsf(M) < kInf;
         if (finite && !(__builtin_fabsf(M * a.c) < kFar)) {
             sum = along = off = 0.0f;
-            for (int i = threadIdx.x; i < a.V; i += kThreads) {
+            for (int i = thread; i < a.V; i += kThreads) {
                 const float d = (logit<Z>(z, i) - M) * a.c, e = exp2_of(d);
                 sum += e;
                 along = __builtin_fmaf(e, __builtin_fmaxf(d, kNothing), along);
@@ -279,7 +331,7 @@ __global__ __launch_bounds__(kThreads) void k_logprob(const Logprob a) {
             L = none ? -kInf : nan;
             entropy = none ? 0.0f : nan;
         }
-        if (threadIdx.x == 0) {
+        if (thread == 0) {
             if (a.logp) a.logp[row] = !given ? 0.0f : none ? -kInf : a.scale * (at_target - M) - L;
             if (a.stats) {
                 a.stats[2 * row] = M;
@@ -287,7 +339,7 @@ __global__ __launch_bounds__(kThreads) void k_logprob(const Logprob a) {
             }
             if (kEntropy) a.entropy[row] = entropy;
         }
-        if constexpr (kTop) top_of<Z, kThreads>(a, row, r.m, sum == sum, M, L, most, owner, found, &place);
+        if constexpr (kTop) top_of<Z, kThreads, kTop == 1>(a, row, r.m, sum == sum, M, L, x, head, most, owner, found, &place);
         __syncthreads();
     }
 }
@@ -304,16 +356,23 @@ struct LogprobGrad {
     float scale, c;
 };
 
-constexpr int kGradThreads = 256, kGradGroups = 4, kPiece = kGradThreads * kGradGroups * 8;
+constexpr int kGradThreads = 256;
 
-template <class Z, class D, bool kEntropy>
+// A piece is kRound logits of each of kLanes threads; short rows (kLanes = 64)
+// are a piece each, without a head of their own.
+template <class Z, class D, bool kEntropy, int kLanes>
 __global__ __launch_bounds__(kGradThreads) void k_logprob_grad(const LogprobGrad a) {
     constexpr float kLog2e = 1.44269504088896340736f;
-    for (int64_t p = blockIdx.x; p < a.pieces; p += gridDim.x) {
-        const int64_t row = p / a.per_row;
-        const int begin = static_cast<int>(p - row * a.per_row) * kPiece;
+    constexpr int N = Z::kGroup, kGradGroups = kRound / N, kPiece = kLanes * kRound, kTeams = kGradThreads / kLanes;
+    const int lane = static_cast<int>(threadIdx.x) % kLanes, team = static_cast<int>(threadIdx.x) / kLanes;
+    for (int64_t p = int64_t(blockIdx.x) * kTeams + team; p < a.pieces; p += int64_t(gridDim.x) * kTeams) {
+        const int64_t row = kLanes == 64 ? p : a.pieces >> 31 ? p / a.per_row : uint32_t(p) / uint32_t(a.per_row);
+        const int piece = static_cast<int>(p - row * a.per_row);
         const typename Z::type *z = static_cast<const typename Z::type *>(a.z) + row * a.ld;
         typename D::type *dz = static_cast<typename D::type *>(a.dz) + row * a.ldd;
+        // pieces start on whole cache lines of Z; the logits before go to the first one's first threads
+        const int head = kLanes == 64 ? 0 : before_line<Z>(z, a.V), begin = head + piece * kPiece;
+        const bool mine = piece == 0 && lane < head;
         const int target = a.target ? a.target[row] : -1;
         const bool given = target >= 0 && target < a.V;
         const float own = given && a.dlogp ? a.dlogp[row] : 0.0f;
@@ -322,39 +381,43 @@ __global__ __launch_bounds__(kGradThreads) void k_logprob_grad(const LogprobGrad
         if ((own == 0.0f && by_entropy == 0.0f) || (M == -kInf && L == -kInf)) {
 #pragma unroll
             for (int g = 0; g < kGradGroups; ++g) {
-                const int at = begin + (g * kGradThreads + static_cast<int>(threadIdx.x)) * 8;
-                put_group<D>(dz + at, raw_zero<D>(), a.V - at);
+                const int at = begin + (g * kLanes + lane) * N;
+                put_group<D, N, true>(dz + at, raw_zero<D, N>(), a.V - at);
             }
+            if (mine) dz[lane] = D::down(0.0f);
             continue;
         }
-        Raw<Z> raw[kGradGroups];
+        Raw<Z, N> raw[kGradGroups];
 #pragma unroll
         for (int g = 0; g < kGradGroups; ++g) {
-            const int at = begin + (g * kGradThreads + static_cast<int>(threadIdx.x)) * 8, n = a.V - at;
-            raw[g] = n >= 8 ? get8<Z>(z + at) : n > 0 ? get_few<Z>(z + at, n) : raw_zero<Z>();
+            const int at = begin + (g * kLanes + lane) * N, n = a.V - at;
+            raw[g] = n >= N ? get<Z, N, true>(z + at) : n > 0 ? get_few<Z, N>(z + at, n) : raw_zero<Z, N>();
         }
+        const float first = mine ? logit<Z>(z, lane) : 0.0f;
         // scale * (dlogp + dentropy * (logp + entropy)) as a line in log2(p)
         const float l2 = L * kLog2e, slope = a.scale * by_entropy * kLn2;
         const float level = a.scale * (own + (kEntropy ? by_entropy * a.entropy[row] : 0.0f));
         const float extra = a.scale * own;
+        const auto slope_of = [&](float x) {
+            const float d = __builtin_fmaf(x - M, a.c, -l2);
+            const float weight = kEntropy ? __builtin_fmaf(__builtin_fmaxf(d, kNothing), slope, level) : level;
+            return -exp2_of(d) * weight;
+        };
 #pragma unroll
         for (int g = 0; g < kGradGroups; ++g) {
-            const int at = begin + (g * kGradThreads + static_cast<int>(threadIdx.x)) * 8;
-            float x[8];
-            open8<Z>(raw[g], x);
+            const int at = begin + (g * kLanes + lane) * N;
+            float x[N];
+            open<Z, N>(raw[g], x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float d = __builtin_fmaf(x[i] - M, a.c, -l2);
-                const float weight = kEntropy ? __builtin_fmaf(__builtin_fmaxf(d, kNothing), slope, level) : level;
-                x[i] = -exp2_of(d) * weight;
-            }
-            if (given && static_cast<uint32_t>(target - at) < 8u) {
+            for (int i = 0; i < N; ++i) x[i] = slope_of(x[i]);
+            if (given && static_cast<uint32_t>(target - at) < uint32_t(N)) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
+                for (int i = 0; i < N; ++i)
                     if (i == target - at) x[i] += extra;
             }
-            put_group<D>(dz + at, close8<D>(x), a.V - at);
+            put_group<D, N, true>(dz + at, close<D, N>(x), a.V - at);
         }
+        if (mine) dz[lane] = D::down(slope_of(first) + (target == lane ? extra : 0.0f));
     }
 }
 
@@ -381,20 +444,30 @@ constexpr int64_t kMaxGrid = 1 << 21;
 
 float scaled(float scale) { return static_cast<float>(double(scale) * 1.4426950408889634074); }
 
-template <class Z, int kThreads>
-void send(const Logprob &a, hipStream_t st) {
-    const dim3 grid(static_cast<uint32_t>(std::min<int64_t>(a.N, kMaxGrid))), block(kThreads);
-    if (a.entropy && a.top) hipLaunchKernelGGL((k_logprob<Z, kThreads, true, true>), grid, block, 0, st, a);
-    else if (a.entropy) hipLaunchKernelGGL((k_logprob<Z, kThreads, true, false>), grid, block, 0, st, a);
-    else if (a.top) hipLaunchKernelGGL((k_logprob<Z, kThreads, false, true>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((k_logprob<Z, kThreads, false, false>), grid, block, 0, st, a);
+template <class Z, int kThreads, int kTop>
+void send(const Logprob &a, int64_t most, hipStream_t st) {
+    const dim3 grid(static_cast<uint32_t>(std::min<int64_t>(a.N, most))), block(kThreads);
+    if (a.entropy) hipLaunchKernelGGL((k_logprob<Z, kThreads, true, kTop>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((k_logprob<Z, kThreads, false, kTop>), grid, block, 0, st, a);
 }
 
+// Short rows go to a wave each, as many at a time as the device holds: starting
+// a workgroup takes longer than reading one of them.  Few long rows go to 1024
+// threads.
 template <class Z>
 void send(const Logprob &a, hipStream_t st) {
-    if (a.V <= 2048) send<Z, 64>(a, st);
-    else if (a.N < 2 * num_cus() && a.V >= 16384) send<Z, 1024>(a, st);
-    else send<Z, 256>(a, st);
+    if (a.V <= 64 * kRound) {
+        const int64_t most = 32 * int64_t(num_cus());
+        if (a.top) send<Z, 64, 1>(a, most, st);
+        else send<Z, 64, 0>(a, most, st);
+    } else if (a.N < 2 * num_cus() && a.V >= 16384) {
+        if (!a.top) send<Z, 1024, 0>(a, kMaxGrid, st);
+        else if (a.V <= 1024 * kRound) send<Z, 1024, 1>(a, kMaxGrid, st);
+        else send<Z, 1024, 2>(a, kMaxGrid, st);
+    } else {
+        if (a.top) send<Z, 256, 2>(a, kMaxGrid, st);
+        else send<Z, 256, 0>(a, kMaxGrid, st);
+    }
 }
 
 }  // namespace
@@ -468,15 +541,19 @@ int sft_logprob_grad(const sft_logprob_grad_args *v, void *stream) {
     a.dlogp = v->dlogp, a.dentropy = v->dentropy, a.dz = v->dZ;
     a.ld = v->ldz, a.ldd = v->lddz;
     a.N = static_cast<int32_t>(v->N), a.V = static_cast<int32_t>(v->V);
-    a.per_row = static_cast<int32_t>((v->V + kPiece - 1) / kPiece);
+    const bool short_rows = v->V <= 64 * kRound;
+    a.per_row = short_rows ? 1 : static_cast<int32_t>((v->V + kGradThreads * kRound - 1) / (kGradThreads * kRound));
     a.pieces = v->N * a.per_row;
     a.scale = v->scale, a.c = scaled(v->scale);
-    const dim3 grid(static_cast<uint32_t>(std::min(a.pieces, kMaxGrid * 4))), block(kGradThreads);
+    const int64_t groups = short_rows ? std::min<int64_t>((a.pieces + 3) / 4, 8 * int64_t(num_cus())) : a.pieces;
+    const dim3 grid(static_cast<uint32_t>(std::min(groups, kMaxGrid * 4))), block(kGradThreads);
     const hipStream_t st = static_cast<hipStream_t>(stream);
-#define SFT_SEND(Z, D)                                                                                    \
-    do {                                                                                                  \
-        if (v->dentropy) hipLaunchKernelGGL((k_logprob_grad<Z, D, true>), grid, block, 0, st, a);         \
-        else hipLaunchKernelGGL((k_logprob_grad<Z, D, false>), grid, block, 0, st, a);                    \
+#define SFT_SEND(Z, D)                                                                                         \
+    do {                                                                                                       \
+        if (short_rows && v->dentropy) hipLaunchKernelGGL((k_logprob_grad<Z, D, true, 64>), grid, block, 0, st, a);  \
+        else if (short_rows) hipLaunchKernelGGL((k_logprob_grad<Z, D, false, 64>), grid, block, 0, st, a);     \
+        else if (v->dentropy) hipLaunchKernelGGL((k_logprob_grad<Z, D, true, 256>), grid, block, 0, st, a);    \
+        else hipLaunchKernelGGL((k_logprob_grad<Z, D, false, 256>), grid, block, 0, st, a);                    \
     } while (0)
     if (v->z_type == SFT_BF16) SFT_SEND(Bf16, Bf16);
     else if (v->dz_type == SFT_BF16) SFT_SEND(Fp32, Bf16);

@@ -18,8 +18,6 @@ namespace {
 
 using namespace sft;
 
-// Lanes of a team, and groups of 8 elements a lane, for rows of up to
-// kLanes * kGroups * 8 elements.  Below 64 lanes several rows share a wave.
 constexpr int kMaxWidth = 16384;
 
 // The sum over a team, in all of its lanes.  red: one float a wave, of its own
@@ -40,14 +38,12 @@ __device__ __forceinline__ float team_sum(float x, float *red) {
 }
 
 // Elements of the vectors gain and bias, of either type.
-__device__ __forceinline__ void vector8(const void *v, bool w32, int at, int n, float (&x)[8]) {
-    if (w32) {
-        const float *p = static_cast<const float *>(v) + at;
-        open8<Fp32>(n >= 8 ? get8<Fp32>(p) : get_few<Fp32>(p, n), x);
-    } else {
-        const uint16_t *p = static_cast<const uint16_t *>(v) + at;
-        open8<Bf16>(n >= 8 ? get8<Bf16>(p) : get_few<Bf16>(p, n), x);
-    }
+template <int N>
+__device__ __forceinline__ void get_vector(const void *v, bool w32, int at, int n, float *x) {
+    if (w32)
+        open<Fp32, N>(get_group<Fp32, N>(static_cast<const float *>(v) + at, n), x);
+    else
+        open<Bf16, N>(get_group<Bf16, N>(static_cast<const uint16_t *>(v) + at, n), x);
 }
 
 struct NormForward {
@@ -64,7 +60,7 @@ struct NormForward {
 
 template <class X, class Y, int kLanes, int kGroups>
 __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes) void k_norm_forward(const NormForward a) {
-    constexpr int kThreads = kLanes < 256 ? 256 : kLanes, kTeams = kThreads / kLanes;
+    constexpr int N = X::kGroup, kThreads = kLanes < 256 ? 256 : kLanes, kTeams = kThreads / kLanes;
     __shared__ float red[2][2][kThreads / 64];       // by turns, so that one barrier a sum is enough
     const int team = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
     const int C = a.C;
@@ -73,28 +69,28 @@ __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes) void k_norm_forward(co
     for (int64_t first = int64_t(blockIdx.x) * kTeams; first < a.T; first += int64_t(gridDim.x) * kTeams, turn ^= 1) {
         const bool live = first + team < a.T;
         const int64_t row = live ? first + team : a.T - 1;      // a team without a row stays for the barriers
-        Raw<X> raw[kGroups];
-        get_row<X, kLanes>(static_cast<const xt *>(a.x) + row * a.ldx, lane, C, raw);
-        float x[kGroups][8];
+        Raw<X, N> raw[kGroups];
+        get_row<X, N, kLanes>(static_cast<const xt *>(a.x) + row * a.ldx, lane, C, raw);
+        float x[kGroups][N];
         if (a.res) {
-            Raw<X> other[kGroups];
-            get_row<X, kLanes>(static_cast<const xt *>(a.res) + row * a.ldr, lane, C, other);
+            Raw<X, N> other[kGroups];
+            get_row<X, N, kLanes>(static_cast<const xt *>(a.res) + row * a.ldr, lane, C, other);
             xt *h = static_cast<xt *>(a.h) + row * a.ldh;
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) {
-                float y[8];
-                open8<X>(raw[g], x[g]);
-                open8<X>(other[g], y);
+                float y[N];
+                open<X, N>(raw[g], x[g]);
+                open<X, N>(other[g], y);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[g][i] += y[i];
-                const Raw<X> sum = close8<X>(x[g]);
-                open8<X>(sum, x[g]);                    // what is normed is what is kept
-                const int at = (g * kLanes + lane) * 8;
-                if (live) put_group<X>(h + at, sum, C - at);
+                for (int i = 0; i < N; ++i) x[g][i] += y[i];
+                const Raw<X, N> sum = close<X, N>(x[g]);
+                open<X, N>(sum, x[g]);                    // what is normed is what is kept
+                const int at = (g * kLanes + lane) * N;
+                if (live) put_group<X, N, true>(h + at, sum, C - at);
             }
         } else {
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g) open8<X>(raw[g], x[g]);
+            for (int g = 0; g < kGroups; ++g) open<X, N>(raw[g], x[g]);
         }
         float mean = 0.0f;
         if (a.layer) {
@@ -102,15 +98,15 @@ __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes) void k_norm_forward(co
 #pragma unroll
             for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum += x[g][i];       // zeros behind the row's end
+                for (int i = 0; i < N; ++i) sum += x[g][i];       // zeros behind the row's end
             mean = team_sum<kLanes>(sum, red[turn][0]) / static_cast<float>(C);
         }
         float squares = 0.0f;
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
-            const int n = C - (g * kLanes + lane) * 8;
+            const int n = C - (g * kLanes + lane) * N;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < N; ++i) {
                 x[g][i] -= mean;
                 if (i < n) squares = __builtin_fmaf(x[g][i], x[g][i], squares);
             }
@@ -125,27 +121,29 @@ __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes) void k_norm_forward(co
         typename Y::type *y = static_cast<typename Y::type *>(a.y) + row * a.ldy;
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
-            const int at = (g * kLanes + lane) * 8, n = C - at;
+            const int at = (g * kLanes + lane) * N, n = C - at;
             if (n <= 0) continue;
-            float w[8];
+            float w[N];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[g][i] *= rstd;
+            for (int i = 0; i < N; ++i) x[g][i] *= rstd;
             if (a.gain) {
-                vector8(a.gain, a.w32, at, n, w);
+                get_vector<N>(a.gain, a.w32, at, n, w);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[g][i] *= w[i];
+                for (int i = 0; i < N; ++i) x[g][i] *= w[i];
             }
             if (a.bias) {
-                vector8(a.bias, a.w32, at, n, w);
+                get_vector<N>(a.bias, a.w32, at, n, w);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[g][i] += w[i];
+                for (int i = 0; i < N; ++i) x[g][i] += w[i];
             }
-            put_group<Y>(y + at, close8<Y>(x[g]), n);
+            put_group<Y, N, true>(y + at, close<Y, N>(x[g]), n);
         }
     }
 }
 
 // ------------------------------------------------------------------ backward
+constexpr int kRowThreads = 1024;
+
 struct NormBackward {
     const void *h, *gain;
     const float *mean, *rstd;
@@ -157,50 +155,75 @@ struct NormBackward {
     bool layer, w32;
 };
 
-// Each team takes rows in turn, kTeams * gridDim.x apart, and keeps its share
-// of the sums over the rows in registers; a workgroup's teams are added at the
-// end, in order, and its sums go to its own place in the workspace.
-// kSums: 0 = no sums over rows, 1 = dgain, 2 = dgain and dbias.
-template <class X, class Y, int kLanes, int kGroups, int kThreads, int kSums>
-__global__ __launch_bounds__(kThreads) void k_norm_backward(const NormBackward a) {
-    constexpr int kTeams = kThreads / kLanes, kWidth = kLanes * kGroups * 8;
-    __shared__ float red[2][2][kThreads / 64];
-    __shared__ float total[kTeams > 1 && kSums ? kSums * kWidth : 1];
+// What a team reads of a row.
+template <class X, class Y, int kGroups>
+struct NormRow {
+    static constexpr int N = X::kGroup;
+    Raw<X, N> h[kGroups], dh[kGroups];
+    Raw<Y, N> dy[kGroups];
+    float mean, rstd;
+};
+
+template <class X, class Y, int kLanes, int kGroups>
+__device__ __forceinline__ void get_norm_row(const NormBackward &a, int64_t row, int lane, NormRow<X, Y, kGroups> &r) {
+    constexpr int N = X::kGroup;
+    get_row<X, N, kLanes>(static_cast<const typename X::type *>(a.h) + row * a.ldh, lane, a.C, r.h);
+    get_row<Y, N, kLanes>(static_cast<const typename Y::type *>(a.dy) + row * a.ldy, lane, a.C, r.dy);
+    if (a.dh) get_row<X, N, kLanes>(static_cast<const typename X::type *>(a.dh) + row * a.ldr, lane, a.C, r.dh);
+    r.rstd = a.rstd[row];
+    r.mean = a.layer ? a.mean[row] : 0.0f;
+}
+
+// Each team takes rows in turn, kTeams * gridDim.x apart, the next one's loads
+// under way while it works on one, and keeps its share of the sums over the
+// rows in registers; a workgroup's teams are added at the end, by halves, and
+// its sums go to its own place in the workspace.
+// kSums: 0 = no sums over rows, 1 = dgain, 2 = dgain and dbias.  The widest
+// rows leave no registers for a row ahead or for the gains.
+template <class X, class Y, int kLanes, int kGroups, int kSums>
+__device__ __forceinline__ void norm_rows(const NormBackward &a, uint32_t block, uint32_t blocks) {
+    constexpr int N = X::kGroup, kTeams = kRowThreads / kLanes, kWidth = kLanes * kGroups * N;
+    constexpr bool kAhead = kWidth <= 8192;
+    __shared__ float red[2][2][kRowThreads / 64];
+    __shared__ float total[kTeams > 1 && kSums ? kSums * kWidth * kTeams / 2 : 1];
     const int team = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
     const int C = a.C;
     typedef typename X::type xt;
-    typedef typename Y::type yt;
-    float dgain[kGroups][8], dbias[kGroups][8], gain[kGroups][8];
+    float dgain[kGroups][N], dbias[kGroups][N], gain[kGroups][N];
+    const int64_t stride = int64_t(blocks) * kTeams;
+    int64_t first = int64_t(block) * kTeams;           // there are never more workgroups than rows for them
+    NormRow<X, Y, kGroups> next;
+    if (kAhead) get_norm_row<X, Y, kLanes>(a, min(first + team, int64_t(a.T) - 1), lane, next);
+    const auto get_gain = [&](int g) {
+        const int at = (g * kLanes + lane) * N, n = C - at;
+#pragma unroll
+        for (int i = 0; i < N; ++i) gain[g][i] = 1.0f;
+        if (a.gain && n > 0) get_vector<N>(a.gain, a.w32, at, n, gain[g]);
+    };
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-        const int at = (g * kLanes + lane) * 8, n = C - at;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            dgain[g][i] = dbias[g][i] = 0.0f;
-            gain[g][i] = 1.0f;
-        }
-        if (a.gain && n > 0) vector8(a.gain, a.w32, at, n, gain[g]);
+        for (int i = 0; i < N; ++i) dgain[g][i] = dbias[g][i] = 0.0f;
+        if (kAhead) get_gain(g);
     }
     const float per = 1.0f / static_cast<float>(C);
-    int turn = 0;
-    for (int64_t first = int64_t(blockIdx.x) * kTeams; first < a.T; first += int64_t(gridDim.x) * kTeams, turn ^= 1) {
-        const bool live = first + team < a.T;
+    for (int turn = 0; first < a.T; first += stride, turn ^= 1) {
+        const bool live = first + team < a.T;           // a team without a row stays for the barriers
         const int64_t row = live ? first + team : a.T - 1;
-        Raw<X> rh[kGroups], rr[kGroups];
-        Raw<Y> ry[kGroups];
-        get_row<X, kLanes>(static_cast<const xt *>(a.h) + row * a.ldh, lane, C, rh);
-        get_row<Y, kLanes>(static_cast<const yt *>(a.dy) + row * a.ldy, lane, C, ry);
-        if (a.dh) get_row<X, kLanes>(static_cast<const xt *>(a.dh) + row * a.ldr, lane, C, rr);
-        const float rstd = a.rstd[row], mean = a.layer ? a.mean[row] : 0.0f;
-        float x[kGroups][8], d[kGroups][8];
+        if (!kAhead) get_norm_row<X, Y, kLanes>(a, row, lane, next);
+        const NormRow<X, Y, kGroups> r = next;
+        if (kAhead && first + stride < a.T)
+            get_norm_row<X, Y, kLanes>(a, min(first + stride + team, int64_t(a.T) - 1), lane, next);
+        float x[kGroups][N], d[kGroups][N];
         float along = 0.0f, flat = 0.0f;
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
-            open8<X>(rh[g], x[g]);
-            open8<Y>(ry[g], d[g]);          // zeros behind the row's end
+            open<X, N>(r.h[g], x[g]);
+            open<Y, N>(r.dy[g], d[g]);          // zeros behind the row's end
+            if (!kAhead) get_gain(g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[g][i] = (x[g][i] - mean) * rstd;
+            for (int i = 0; i < N; ++i) {
+                x[g][i] = (x[g][i] - r.mean) * r.rstd;
                 if (kSums && live) {
                     dgain[g][i] = __builtin_fmaf(d[g][i], x[g][i], dgain[g][i]);
                     if (kSums > 1) dbias[g][i] += d[g][i];
@@ -234,87 +257,142 @@ __global__ __launch_bounds__(kThreads) void k_norm_backward(const NormBackward a
         xt *dx = static_cast<xt *>(a.dx) + row * a.ldx;
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
-            const int at = (g * kLanes + lane) * 8;
+            const int at = (g * kLanes + lane) * N;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) d[g][i] = (d[g][i] - flat - x[g][i] * along) * rstd;
+            for (int i = 0; i < N; ++i) d[g][i] = (d[g][i] - flat - x[g][i] * along) * r.rstd;
             if (a.dh) {
-                float r[8];
-                open8<X>(rr[g], r);
+                float other[N];
+                open<X, N>(r.dh[g], other);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) d[g][i] += r[i];
+                for (int i = 0; i < N; ++i) d[g][i] += other[i];
             }
-            if (live) put_group<X>(dx + at, close8<X>(d[g]), C - at);
+            if (live) put_group<X, N, true>(dx + at, close<X, N>(d[g]), C - at);
         }
     }
     if constexpr (kSums > 0) {
-        if constexpr (kTeams > 1) {
-            for (int t = 0; t < kTeams - 1; ++t) {
-                __syncthreads();
 #pragma unroll
-                for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int at = (g * kLanes + lane) * 8 + i;
-                        if (team == t) {
-                            total[at] = t ? total[at] + dgain[g][i] : dgain[g][i];
-                            if (kSums > 1) total[kWidth + at] = t ? total[kWidth + at] + dbias[g][i] : dbias[g][i];
-                        }
-                    }
-            }
-            __syncthreads();
-            if (team != kTeams - 1) return;
+        for (int n = kTeams / 2; n; n /= 2) {
+            // teams n .. 2n - 1 hand theirs to teams 0 .. n - 1
+            const int place = (team - n) * kSums * kWidth, own = team * kSums * kWidth;
 #pragma unroll
             for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int at = (g * kLanes + lane) * 8 + i;
-                    dgain[g][i] += total[at];
-                    if (kSums > 1) dbias[g][i] += total[kWidth + at];
+                for (int i = 0; i < N; ++i) {
+                    const int at = (g * N + i) * kLanes + lane;      // of one lane's values apart: no bank conflicts
+                    if (team >= n && team < 2 * n) {
+                        total[place + at] = dgain[g][i];
+                        if (kSums > 1) total[place + kWidth + at] = dbias[g][i];
+                    }
                 }
+            __syncthreads();
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const int at = (g * N + i) * kLanes + lane;
+                    if (team < n) {
+                        dgain[g][i] += total[own + at];
+                        if (kSums > 1) dbias[g][i] += total[own + kWidth + at];
+                    }
+                }
+            __syncthreads();
         }
-        float *part = a.part + int64_t(blockIdx.x) * C;
+        if (team) return;
+        float *part = a.part + int64_t(block) * C;
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
-            const int at = (g * kLanes + lane) * 8;
-            put_group<Fp32>(part + at, close8<Fp32>(dgain[g]), C - at);
-            if (kSums > 1) put_group<Fp32>(part + int64_t(gridDim.x) * C + at, close8<Fp32>(dbias[g]), C - at);
+            const int at = (g * kLanes + lane) * N;
+            put_group<Fp32, N>(part + at, close<Fp32, N>(dgain[g]), C - at);
+            if (kSums > 1) put_group<Fp32, N>(part + int64_t(blocks) * C + at, close<Fp32, N>(dbias[g]), C - at);
         }
     }
 }
 
-// The workgroups' sums in a fixed order: 32 columns a workgroup, 8 shares of
-// the rows each.
-constexpr int kReduceColumns = 32, kReduceShares = 8;
-
-struct NormReduce {
+// Where the sums over the rows end up.
+struct NormSums {
     const float *part;
-    void *out[2];
+    void *out[2];                 // dgain, dbias
     int32_t groups, C;
     bool g32, accumulate;
 };
 
-__global__ __launch_bounds__(kReduceColumns *kReduceShares) void k_norm_reduce(const NormReduce a) {
-    __shared__ float s[kReduceShares][kReduceColumns];
-    const int column = threadIdx.x % kReduceColumns, share = threadIdx.x / kReduceColumns;
-    const int c = blockIdx.x * kReduceColumns + column;
+__device__ __forceinline__ void put_sum(const NormSums &s, int which, int c, float sum) {
+    if (!s.out[which]) return;
+    if (s.g32) {
+        float *out = static_cast<float *>(s.out[which]) + c;
+        *out = s.accumulate ? *out + sum : sum;
+    } else {
+        static_cast<uint16_t *>(s.out[which])[c] = Bf16::down(sum);
+    }
+}
+
+constexpr int kColumns = 32, kShares = kRowThreads / kColumns;
+
+// The shares' sums of a column, added in order by one of its threads.
+__device__ __forceinline__ float columns_sum(float sum, float *s) {
+    const int column = threadIdx.x % kColumns, share = threadIdx.x / kColumns;
+    s[share * kColumns + column] = sum;
+    __syncthreads();
+    sum = 0.0f;
+    if (share == 0)
+#pragma unroll
+        for (int i = 0; i < kShares; ++i) sum += s[i * kColumns + column];
+    __syncthreads();
+    return sum;
+}
+
+// The sums over few rows, of 32 columns a workgroup: the statistics are there
+// already, so they need not wait for the rows' own sums, and one launch does
+// for both.
+template <class X, class Y>
+__device__ __forceinline__ void norm_columns(const NormBackward &a, const NormSums &s, uint32_t block) {
+    __shared__ float places[kRowThreads];
+    const int c = block * kColumns + threadIdx.x % kColumns;
+    float dgain = 0.0f, dbias = 0.0f;
+    if (c < a.C) {
+        const typename X::type *h = static_cast<const typename X::type *>(a.h) + c;
+        const typename Y::type *dy = static_cast<const typename Y::type *>(a.dy) + c;
+#pragma unroll 8
+        for (int t = threadIdx.x / kColumns; t < a.T; t += kShares) {
+            const float d = Y::up(dy[t * a.ldy]), x = X::up(h[t * a.ldh]);
+            dgain = __builtin_fmaf(d, (x - (a.layer ? a.mean[t] : 0.0f)) * a.rstd[t], dgain);
+            dbias += d;
+        }
+    }
+    dgain = columns_sum(dgain, places);
+    dbias = columns_sum(dbias, places);
+    if (threadIdx.x >= kColumns || c >= a.C) return;
+    put_sum(s, 0, c, dgain);
+    put_sum(s, 1, c, dbias);
+}
+
+template <class X, class Y, int kLanes, int kGroups, int kSums>
+__global__ __launch_bounds__(kRowThreads) void k_norm_backward(const NormBackward a) {
+    norm_rows<X, Y, kLanes, kGroups, kSums>(a, blockIdx.x, gridDim.x);
+}
+
+// Rows and columns in one launch, the columns' workgroups first.
+template <class X, class Y, int kLanes, int kGroups>
+__global__ __launch_bounds__(kRowThreads) void k_norm_backward_few(const NormBackward a, const NormSums s,
+                                                                   uint32_t columns) {
+    if (blockIdx.x < columns)
+        norm_columns<X, Y>(a, s, blockIdx.x);
+    else
+        norm_rows<X, Y, kLanes, kGroups, 0>(a, blockIdx.x - columns, gridDim.x - columns);
+}
+
+// The workgroups' sums in a fixed order: 32 columns a workgroup, 32 shares of them.
+__global__ __launch_bounds__(kRowThreads) void k_norm_reduce(const NormSums a) {
+    __shared__ float places[kRowThreads];
+    const int c = blockIdx.x * kColumns + threadIdx.x % kColumns;
     float sum = 0.0f;
     if (c < a.C && a.out[blockIdx.y]) {
         const float *p = a.part + int64_t(blockIdx.y) * a.groups * a.C + c;
 #pragma unroll 8
-        for (int g = share; g < a.groups; g += kReduceShares) sum += p[int64_t(g) * a.C];
+        for (int g = threadIdx.x / kColumns; g < a.groups; g += kShares) sum += p[int64_t(g) * a.C];
     }
-    s[share][column] = sum;
-    __syncthreads();
-    if (share || c >= a.C || !a.out[blockIdx.y]) return;
-    sum = s[0][column];
-#pragma unroll
-    for (int i = 1; i < kReduceShares; ++i) sum += s[i][column];
-    if (a.g32) {
-        float *out = static_cast<float *>(a.out[blockIdx.y]) + c;
-        *out = a.accumulate ? *out + sum : sum;
-    } else {
-        static_cast<uint16_t *>(a.out[blockIdx.y])[c] = Bf16::down(sum);
-    }
+    sum = columns_sum(sum, places);
+    if (threadIdx.x < kColumns && c < a.C) put_sum(a, blockIdx.y, c, sum);
 }
 
 // ------------------------------------------------------------------ host
@@ -356,58 +434,78 @@ int check_apart(const Block *written, int n_written, const Block *read, int n_re
     return SFT_OK;
 }
 
-// The widths that each team serves, narrowest first.
-#define SFT_NORM_WIDTHS(go) \
-    go(16, 1) go(32, 1) go(64, 1) go(128, 1) go(256, 1) go(256, 2) go(512, 2) go(1024, 2)
+// Lanes of a team and eights of elements of a lane, narrowest first.  Forward,
+// 32 bytes a lane are best for either type: two eights in bf16 (with residual,
+// 16.8M values of rows of 512, 2048: 21.4 us, one eight 23.3, four 22.4), one in
+// fp32 (8.4M values of rows of 512, 4096: 12.9 and 13.5 us, two 13.9 and 15.8),
+// until there are 512 lanes.
+#define SFT_FORWARD_BF16(go) \
+    go(16, 1) go(16, 2) go(32, 2) go(64, 2) go(128, 2) go(256, 2) go(512, 2) go(512, 4)
+#define SFT_FORWARD_FP32(go) \
+    go(16, 1) go(32, 1) go(64, 1) go(128, 1) go(256, 1) go(512, 1) go(512, 2) go(1024, 2)
+#define SFT_BACKWARD_WIDTHS(go) \
+    go(16, 1) go(32, 1) go(64, 1) go(128, 1) go(256, 1) go(512, 1) go(1024, 1) go(1024, 2)
 
 template <class X, class Y>
 void send_forward(const NormForward &a, hipStream_t st) {
-#define SFT_GO(lanes, groups)                                                                             \
-    if (a.C <= lanes * groups * 8) {                                                                      \
+#define SFT_GO(lanes, eights)                                                                             \
+    if (a.C <= lanes * eights * 8) {                                                                      \
+        constexpr int kGroups = eights * 8 / X::kGroup;                                                   \
         constexpr int kThreads = lanes < 256 ? 256 : lanes, kTeams = kThreads / lanes;                    \
         const int64_t rounds = (int64_t(a.T) + kTeams - 1) / kTeams;                                      \
         const uint32_t grid = static_cast<uint32_t>(std::min<int64_t>(rounds, 1 << 21));                  \
-        hipLaunchKernelGGL((k_norm_forward<X, Y, lanes, groups>), dim3(grid), dim3(kThreads), 0, st, a);  \
+        hipLaunchKernelGGL((k_norm_forward<X, Y, lanes, kGroups>), dim3(grid), dim3(kThreads), 0, st, a);  \
         return;                                                                                           \
     }
-    SFT_NORM_WIDTHS(SFT_GO)
+    if constexpr (X::kType == SFT_BF16) {
+        SFT_FORWARD_BF16(SFT_GO)
+    } else {
+        SFT_FORWARD_FP32(SFT_GO)
+    }
 #undef SFT_GO
 }
 
-// Workgroups of the backward pass with sums over the rows: their number decides how many partial sums are written and
-// read again.
-int backward_groups(int64_t T, int teams, int threads) {
-    const int64_t rounds = int64_t(num_cus()) * std::max(1, 1024 / threads);
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((T + teams - 1) / teams, rounds)));
+int backward_teams(int64_t C) {
+#define SFT_GO(lanes, eights) \
+    if (C <= lanes * eights * 8) return kRowThreads / lanes;
+    SFT_BACKWARD_WIDTHS(SFT_GO)
+#undef SFT_GO
+    return 1;
 }
-constexpr int backward_threads(int lanes) { return lanes < 512 ? 512 : lanes; }
 
+// Workgroups of the rows' part: one on each CU, as each writes partial sums that are read again.
 int backward_groups(int64_t T, int64_t C) {
-#define SFT_GO(lanes, groups) \
-    if (C <= lanes * groups * 8) return backward_groups(T, backward_threads(lanes) / lanes, backward_threads(lanes));
-    SFT_NORM_WIDTHS(SFT_GO)
-#undef SFT_GO
-    return 0;
+    const int64_t teams = backward_teams(C);
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((T + teams - 1) / teams, num_cus())));
 }
 
 template <class X, class Y>
-void send_backward(const NormBackward &a, int sums, hipStream_t st) {
-    const dim3 grid(static_cast<uint32_t>(backward_groups(a.T, a.C)));
-#define SFT_GO(lanes, groups)                                                                                       \
-    if (a.C <= lanes * groups * 8) {                                                                                \
-        constexpr int kT = backward_threads(lanes);                                                                 \
-        if (sums == 0) hipLaunchKernelGGL((k_norm_backward<X, Y, lanes, groups, kT, 0>), grid, dim3(kT), 0, st, a); \
-        if (sums == 1) hipLaunchKernelGGL((k_norm_backward<X, Y, lanes, groups, kT, 1>), grid, dim3(kT), 0, st, a); \
-        if (sums == 2) hipLaunchKernelGGL((k_norm_backward<X, Y, lanes, groups, kT, 2>), grid, dim3(kT), 0, st, a); \
-        return;                                                                                                     \
+void send_backward(const NormBackward &a, const NormSums *few, int sums, hipStream_t st) {
+    const uint32_t rows = static_cast<uint32_t>(backward_groups(a.T, a.C));
+    const uint32_t columns = static_cast<uint32_t>((a.C + kColumns - 1) / kColumns);
+    const dim3 grid(rows), all(rows + columns), block(kRowThreads);
+#define SFT_GO(lanes, eights)                                                                                        \
+    if (a.C <= lanes * eights * 8) {                                                                                 \
+        constexpr int kGroups = eights * 8 / X::kGroup;                                                              \
+        if (few) hipLaunchKernelGGL((k_norm_backward_few<X, Y, lanes, kGroups>), all, block, 0, st, a, *few, columns); \
+        else if (sums == 0) hipLaunchKernelGGL((k_norm_backward<X, Y, lanes, kGroups, 0>), grid, block, 0, st, a);    \
+        else if (sums == 1) hipLaunchKernelGGL((k_norm_backward<X, Y, lanes, kGroups, 1>), grid, block, 0, st, a);    \
+        else hipLaunchKernelGGL((k_norm_backward<X, Y, lanes, kGroups, 2>), grid, block, 0, st, a);                   \
+        return;                                                                                                      \
     }
-    SFT_NORM_WIDTHS(SFT_GO)
+    SFT_BACKWARD_WIDTHS(SFT_GO)
 #undef SFT_GO
 }
 
 size_t backward_bytes(int64_t T, int64_t C, bool with_bias) {
     return size_t(backward_groups(T, C)) * size_t(C) * sizeof(float) * (with_bias ? 2 : 1);
 }
+
+// Where the sums over the rows are taken by columns in the same launch, which
+// reads two arrays again but saves a launch: 256 x 4096 5.2 us (with partial
+// sums 8.3), 512 x 1375 6.8 (9.5), 1024 x 300 6.6 (8.9), 512 x 4096 8.3 (8.7);
+// but 1024 x 4096 14.1 (10.6), 2048 x 4096 24.8 (15.5).
+bool few_rows(int64_t T, int64_t C) { return T <= 1024 && T * C <= (1 << 21); }
 
 }  // namespace
 
@@ -513,34 +611,34 @@ int sft_norm_backward(const sft_norm_grad_args *v, void *ws, size_t ws_bytes, vo
         if (int rc = check_apart(&dx, 1, read, n, who)) return rc;
     }
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    int groups = 0;
+    NormSums s{};
+    s.part = static_cast<const float *>(ws);
+    s.out[0] = v->dgain, s.out[1] = v->dbias;
+    s.groups = v->T ? backward_groups(v->T, v->C) : 0, s.C = static_cast<int32_t>(v->C);
+    s.g32 = v->g_type == SFT_F32, s.accumulate = v->accumulate != 0;
+    // (dX in dY's place is written while other workgroups would still read dY for the columns)
+    const bool few = sums && v->T > 0 && few_rows(v->T, v->C) && !same(dx, dy);
     if (v->T) {
         NormBackward a{};
         a.h = v->H, a.gain = v->gain, a.mean = v->mean, a.rstd = v->rstd, a.dy = v->dY, a.dh = v->dH, a.dx = v->dX;
         a.part = static_cast<float *>(ws);
         a.ldh = v->ldh, a.ldy = v->ldy, a.ldr = v->ldr, a.ldx = v->ldx;
-        a.T = static_cast<int32_t>(v->T), a.C = static_cast<int32_t>(v->C);
+        a.T = static_cast<int32_t>(v->T), a.C = s.C;
         a.layer = layer;
         a.w32 = v->w_type == SFT_F32;
-        groups = backward_groups(v->T, v->C);
         const int kind = !sums ? 0 : v->dbias ? 2 : 1;
         if (v->x_type == SFT_BF16)
-            send_backward<Bf16, Bf16>(a, kind, st);
+            send_backward<Bf16, Bf16>(a, few ? &s : nullptr, kind, st);
         else if (v->y_type == SFT_BF16)
-            send_backward<Fp32, Bf16>(a, kind, st);
+            send_backward<Fp32, Bf16>(a, few ? &s : nullptr, kind, st);
         else
-            send_backward<Fp32, Fp32>(a, kind, st);
+            send_backward<Fp32, Fp32>(a, few ? &s : nullptr, kind, st);
         const hipError_t e = hipGetLastError();
         SFT_CHECK(e == hipSuccess, SFT_EHIP, "%s: launch failed: %s", who, hipGetErrorString(e));
     }
-    if (sums) {
-        NormReduce r{};
-        r.part = static_cast<const float *>(ws);
-        r.out[0] = v->dgain, r.out[1] = v->dbias;
-        r.groups = groups, r.C = static_cast<int32_t>(v->C);
-        r.g32 = v->g_type == SFT_F32, r.accumulate = v->accumulate != 0;
-        const dim3 grid(static_cast<uint32_t>((v->C + kReduceColumns - 1) / kReduceColumns), v->dbias ? 2 : 1);
-        hipLaunchKernelGGL(k_norm_reduce, grid, dim3(kReduceColumns * kReduceShares), 0, st, r);
+    if (sums && !few) {
+        const dim3 grid(static_cast<uint32_t>((v->C + kColumns - 1) / kColumns), v->dbias ? 2 : 1);
+        hipLaunchKernelGGL(k_norm_reduce, grid, dim3(kRowThreads), 0, st, s);
         const hipError_t e = hipGetLastError();
         SFT_CHECK(e == hipSuccess, SFT_EHIP, "%s: launch failed: %s", who, hipGetErrorString(e));
     }

@@ -18,13 +18,14 @@ namespace {
 
 using namespace sft;
 
+// Threads of a workgroup, and items that it takes unless one token has more: an
+// item is two groups of elements of a head, whose loads are under way while the
+// sines are computed.  One item a thread keeps enough workgroups on a CU
+// (4096 tokens of 32 + 32 heads of 128 in bf16 23.4 us, two items 26.0; 512
+// threads 24.4).
 constexpr int kThreads = 256;
 constexpr int kMaxMats = 8;
 constexpr int kMaxHead = 4096;
-// Items (16 elements of a head: 8 pairs, or 16 behind the turned part) that a
-// workgroup takes, unless one token has more: two a thread, whose loads are
-// under way while the sines are computed.
-constexpr int kItems = 2 * kThreads;
 
 // n / d for n < 2^31.
 struct Div {
@@ -60,17 +61,21 @@ struct Rotary {
     bool inverse;
 };
 
-// One item: two groups of up to 8 elements, where they start in the head and how many there are.
+// One item: two groups of up to N elements, where they start in the head, how
+// many there are, and the places of their first pairs' sines.  The second group
+// is as far from the first as the units allow, so that a wave's accesses are
+// whole runs: with SFT_ROTARY_HALF the pairs' other elements, else the second
+// half of the groups.
 struct Item {
     int64_t x, y;               // the head's first element in either array
     int32_t at0, at1, n0, n1;
-    int32_t angle;              // place of its first pair's sine, or -1: to be copied
+    int32_t sine0, sine1;       // -1: to be copied
 };
 
-template <bool kHalf>
+template <int N, bool kHalf>
 __device__ __forceinline__ Item item_of(const Rotary &a, const RotaryMat &m, uint32_t i, uint32_t first) {
     Item it;
-    const int half = a.rot / 2, pair_units = (half + 7) / 8;
+    const int half = a.rot / 2, pair_units = (half + N - 1) / N;
     const uint32_t q = over(i, m.units), t = over(q, m.heads);
     const int u = static_cast<int>(i - q * m.units.by);
     const int64_t head = q - t * m.heads.by;
@@ -79,69 +84,66 @@ __device__ __forceinline__ Item item_of(const Rotary &a, const RotaryMat &m, uin
     it.x = b * m.x_batch + row * m.x_row + head * m.x_head;
     it.y = b * m.y_batch + row * m.y_row + head * m.y_head;
     if (u < pair_units) {
-        const int n = min(8, half - 8 * u);
-        it.angle = static_cast<int32_t>(t) * half + 8 * u;
+        const int sines = static_cast<int>(t) * half;
         if constexpr (kHalf) {
-            it.at0 = 8 * u, it.at1 = half + 8 * u;
-            it.n0 = it.n1 = n;
+            it.at0 = N * u, it.at1 = half + N * u;
+            it.n0 = it.n1 = min(N, half - N * u);
+            it.sine0 = it.sine1 = sines + N * u;
         } else {
-            it.at0 = 16 * u, it.at1 = 16 * u + 8;
-            it.n0 = min(8, 2 * n), it.n1 = 2 * n - it.n0;
+            it.at0 = N * u, it.at1 = N * (u + pair_units);
+            it.n0 = min(N, a.rot - it.at0), it.n1 = min(N, a.rot - it.at1);
+            it.sine0 = sines + it.at0 / 2, it.sine1 = sines + (it.n1 > 0 ? it.at1 / 2 : 0);
         }
     } else {
-        it.angle = -1;
-        it.at0 = a.rot + 16 * (u - pair_units), it.at1 = it.at0 + 8;
-        it.n0 = min(8, a.D - it.at0), it.n1 = max(0, min(8, a.D - it.at1));
+        it.sine0 = it.sine1 = -1;
+        const int copy_units = static_cast<int>(m.units.by) - pair_units;
+        it.at0 = a.rot + N * (u - pair_units), it.at1 = it.at0 + N * copy_units;
+        it.n0 = min(N, a.D - it.at0), it.n1 = min(N, a.D - it.at1);
     }
     return it;
 }
 
-template <class E>
-__device__ __forceinline__ Raw<E> get_group(const typename E::type *p, int n) {
-    if (n >= 8) return get8<E>(p);
-    return n > 0 ? get_few<E>(p, n) : raw_zero<E>();
-}
-
 template <class E, bool kHalf>
-__device__ __forceinline__ void turn_item(const Item &it, const Raw<E> &r0, const Raw<E> &r1, const f32x4 *sines,
-                                          typename E::type *y) {
+__device__ __forceinline__ void turn_item(const Item &it, const Raw<E, E::kGroup> &r0, const Raw<E, E::kGroup> &r1,
+                                          const float *sines, typename E::type *y) {
+    constexpr int N = E::kGroup;
     y += it.y;
-    if (it.angle < 0) {
-        put_group<E>(y + it.at0, r0, it.n0);
-        put_group<E>(y + it.at1, r1, it.n1);
+    if (it.sine0 < 0) {
+        put_group<E, N, true>(y + it.at0, r0, it.n0);
+        put_group<E, N, true>(y + it.at1, r1, it.n1);
         return;
     }
-    float u[8], v[8], c[8], s[8];
-    const float *at = reinterpret_cast<const float *>(sines) + 2 * it.angle;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = at[2 * i], s[i] = at[2 * i + 1];
-    open8<E>(r0, u);
-    open8<E>(r1, v);
+    float u[N], v[N];
+    open<E, N>(r0, u);
+    open<E, N>(r1, v);
+    const float *s0 = sines + 2 * it.sine0, *s1 = sines + 2 * it.sine1;
     if constexpr (kHalf) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float p = u[i], q = v[i];
-            u[i] = __builtin_fmaf(p, c[i], -(q * s[i]));
-            v[i] = __builtin_fmaf(p, s[i], q * c[i]);
+        for (int i = 0; i < N; ++i) {
+            const float p = u[i], q = v[i], c = s0[2 * i], s = s0[2 * i + 1];
+            u[i] = __builtin_fmaf(p, c, -(q * s));
+            v[i] = __builtin_fmaf(p, s, q * c);
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float p = u[2 * i], q = u[2 * i + 1], f = v[2 * i], g = v[2 * i + 1];
-            u[2 * i] = __builtin_fmaf(p, c[i], -(q * s[i]));
-            u[2 * i + 1] = __builtin_fmaf(p, s[i], q * c[i]);
-            v[2 * i] = __builtin_fmaf(f, c[4 + i], -(g * s[4 + i]));
-            v[2 * i + 1] = __builtin_fmaf(f, s[4 + i], g * c[4 + i]);
+        for (int i = 0; i < N; i += 2) {
+            const float p = u[i], q = u[i + 1], f = v[i], g = v[i + 1];
+            u[i] = __builtin_fmaf(p, s0[i], -(q * s0[i + 1]));
+            u[i + 1] = __builtin_fmaf(p, s0[i + 1], q * s0[i]);
+            v[i] = __builtin_fmaf(f, s1[i], -(g * s1[i + 1]));
+            v[i + 1] = __builtin_fmaf(f, s1[i + 1], g * s1[i]);
         }
     }
-    put_group<E>(y + it.at0, close8<E>(u), it.n0);
-    put_group<E>(y + it.at1, close8<E>(v), it.n1);
+    put_group<E, N, true>(y + it.at0, close<E, N>(u), it.n0);
+    put_group<E, N, true>(y + it.at1, close<E, N>(v), it.n1);
 }
 
 template <class E, bool kHalf>
 __global__ __launch_bounds__(kThreads) void k_rotary(const Rotary a) {
-    extern __shared__ f32x4 sines[];      // cosine and sine of each token's pairs, and room for a last partial item
+    extern __shared__ f32x4 room[];       // cosine and sine of each token's pairs, and 8 pairs more for a last short group
+    constexpr int N = E::kGroup;
     typedef typename E::type type;
+    float *const sines = reinterpret_cast<float *>(room);
     const int half = a.rot / 2;
     for (uint32_t block = blockIdx.x; block < a.blocks; block += gridDim.x) {
         int k = 0;
@@ -151,18 +153,15 @@ __global__ __launch_bounds__(kThreads) void k_rotary(const Rotary a) {
         const uint32_t tokens = min(uint32_t(m.tokens), uint32_t(a.total) - first);
         const uint32_t items = tokens * m.heads.by * m.units.by;
         const type *x = static_cast<const type *>(m.x);
-        Item it[2];
-        Raw<E> r0[2], r1[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t i = threadIdx.x + j * kThreads;
-            if (i >= items) continue;
-            it[j] = item_of<kHalf>(a, m, i, first);
-            r0[j] = get_group<E>(x + it[j].x + it[j].at0, it[j].n0);
-            r1[j] = get_group<E>(x + it[j].x + it[j].at1, it[j].n1);
-        }
+        Item it;
+        Raw<E, N> r0, r1;
+        const auto fetch = [&](uint32_t i) {
+            it = item_of<N, kHalf>(a, m, i, first);
+            r0 = get_group<E, N>(x + it.x + it.at0, it.n0);
+            r1 = get_group<E, N>(x + it.x + it.at1, it.n1);
+        };
+        if (threadIdx.x < items) fetch(threadIdx.x);
         // in turns, of which whole ones do not matter: what is left is exact to fp32 however far the position
-        float *cs = reinterpret_cast<float *>(sines);
         for (uint32_t i = threadIdx.x; i < tokens * uint32_t(half); i += kThreads) {
             const uint32_t t = over(i, a.pairs), token = first + t, b = over(token, a.rows);
             const int32_t pos = a.pos[b * a.pos_batch + (token - b * a.rows.by)];
@@ -170,25 +169,14 @@ __global__ __launch_bounds__(kThreads) void k_rotary(const Rotary a) {
             turns -= __builtin_rint(turns);
             float s, c;
             sincospif(static_cast<float>(2.0 * turns), &s, &c);
-            cs[2 * i] = c * a.amplitude;
-            cs[2 * i + 1] = (a.inverse ? -s : s) * a.amplitude;
+            sines[2 * i] = c * a.amplitude;
+            sines[2 * i + 1] = (a.inverse ? -s : s) * a.amplitude;
         }
         __syncthreads();
-        for (uint32_t base = 0;;) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                if (base + threadIdx.x + j * kThreads < items)
-                    turn_item<E, kHalf>(it[j], r0[j], r1[j], sines, static_cast<type *>(m.y));
-            base += kItems;
-            if (base >= items) break;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint32_t i = base + threadIdx.x + j * kThreads;
-                if (i >= items) continue;
-                it[j] = item_of<kHalf>(a, m, i, first);
-                r0[j] = get_group<E>(x + it[j].x + it[j].at0, it[j].n0);
-                r1[j] = get_group<E>(x + it[j].x + it[j].at1, it[j].n1);
-            }
+        for (uint32_t i = threadIdx.x; i < items;) {
+            turn_item<E, kHalf>(it, r0, r1, sines, static_cast<type *>(m.y));
+            i += kThreads;
+            if (i < items) fetch(i);
         }
         __syncthreads();
     }
@@ -283,20 +271,20 @@ int sft_rotary(const sft_rotary_mat *mats, int32_t n_mats, int64_t B, int64_t T,
     }
     if (!any) return SFT_OK;
     Rotary a{};
-    const int64_t half = rot / 2, pair_units = (half + 7) / 8;
+    const int64_t half = rot / 2, group = 16 / size, pair_units = (half + group - 1) / group;
     int64_t blocks = 0, sines = 0;
     for (int32_t i = 0; i < n_mats; ++i) {
         const sft_rotary_mat &m = mats[i];
         if (m.heads == 0) continue;
         RotaryMat &r = a.m[a.n_mats++];
         // what lies behind the turned part stays where it is when Y is X
-        const int64_t units = pair_units + (same(x[i], y[i]) ? 0 : (D - rot + 15) / 16);
+        const int64_t units = pair_units + (same(x[i], y[i]) ? 0 : (D - rot + 2 * group - 1) / (2 * group));
         r.x = m.X, r.y = m.Y;
         r.x_batch = m.x_batch, r.x_row = m.x_row, r.x_head = m.x_head;
         r.y_batch = m.y_batch, r.y_row = m.y_row, r.y_head = m.y_head;
         r.units = div_by(static_cast<uint32_t>(units));
         r.heads = div_by(static_cast<uint32_t>(m.heads));
-        const int64_t tokens = std::max<int64_t>(1, std::min<int64_t>(total, kItems / (units * m.heads)));
+        const int64_t tokens = std::max<int64_t>(1, std::min<int64_t>(total, kThreads / (units * m.heads)));
         r.tokens = static_cast<int32_t>(tokens);
         r.begin = static_cast<uint32_t>(blocks);
         blocks += (total + tokens - 1) / tokens;

@@ -1,4 +1,4 @@
-// sft_vec.h -- groups of 8 neighbouring elements between memory and registers,
+// sft_vec.h -- groups of neighbouring elements between memory and registers,
 // from any element's address, and sums and maxima over the lanes that share a
 // row.  Shared by the row-wise kernels; not part of the public ABI.
 #pragma once
@@ -21,62 +21,70 @@ __device__ __forceinline__ uint32_t bf16_bits(float x) {
     return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));     // to nearest even
 }
 
-// The two storage types.  16 bytes are loaded at a time whatever the address:
-// memory takes accesses of that width from any address of an element, so rows
-// of odd width or distance go the same way as aligned ones.
+// The two storage types.  Groups are of 16 bytes where both sides have the
+// same type (kGroup elements): a wave's loads and stores then are whole runs of
+// a kilobyte.  They go to any element's address: memory takes accesses of that
+// width from all of them, so rows of odd width or distance go the same way.
 struct Fp32 {
     typedef float type;
-    static constexpr int kWords = 8;      // of 8 elements
+    static constexpr int kGroup = 4;
     static constexpr int32_t kType = SFT_F32;
     typedef u32x4 __attribute__((aligned(4))) quad;
     static __device__ __forceinline__ float up(float x) { return x; }
     static __device__ __forceinline__ float down(float x) { return x; }
-    static __device__ __forceinline__ float held(float x) { return x; }
 };
 struct Bf16 {
     typedef uint16_t type;
-    static constexpr int kWords = 4;
+    static constexpr int kGroup = 8;
     static constexpr int32_t kType = SFT_BF16;
     typedef u32x4 __attribute__((aligned(2))) quad;
+    typedef u32x2 __attribute__((aligned(2))) twin;
     static __device__ __forceinline__ float up(uint16_t x) { return bits_float(uint32_t(x) << 16); }
     static __device__ __forceinline__ uint16_t down(float x) { return static_cast<uint16_t>(bf16_bits(x)); }
-    static __device__ __forceinline__ float held(float x) { return bits_float(bf16_bits(x) << 16); }
 };
 
-// 8 elements as they are in memory.
-template <class E>
+// N elements (4 or 8) as they are in memory.
+template <class E, int N>
+constexpr int words_of = N * int(sizeof(typename E::type)) / 4;
+template <class E, int N>
 struct Raw {
-    uint32_t w[E::kWords];
+    uint32_t w[words_of<E, N>];
 };
 
-template <class E>
-__device__ __forceinline__ Raw<E> raw_zero() {
-    Raw<E> r;
+template <class E, int N>
+__device__ __forceinline__ Raw<E, N> raw_zero() {
+    Raw<E, N> r;
 #pragma unroll
-    for (int i = 0; i < E::kWords; ++i) r.w[i] = 0;
+    for (int i = 0; i < words_of<E, N>; ++i) r.w[i] = 0;
     return r;
 }
 
-template <class E>
-__device__ __forceinline__ Raw<E> get8(const typename E::type *p) {
-    Raw<E> r;
-    const typename E::quad *q = reinterpret_cast<const typename E::quad *>(p);
+// kPast: what is read once and lies on whole cache lines need not stay in L2.
+template <class E, int N, bool kPast = false>
+__device__ __forceinline__ Raw<E, N> get(const typename E::type *p) {
+    Raw<E, N> r;
+    if constexpr (words_of<E, N> == 2) {
+        const u32x2 a = *reinterpret_cast<const typename E::twin *>(p);
+        r.w[0] = a.x, r.w[1] = a.y;
+    } else {
+        const typename E::quad *q = reinterpret_cast<const typename E::quad *>(p);
 #pragma unroll
-    for (int i = 0; i < E::kWords / 4; ++i) {
-        const u32x4 a = q[i];
-        r.w[4 * i] = a.x, r.w[4 * i + 1] = a.y, r.w[4 * i + 2] = a.z, r.w[4 * i + 3] = a.w;
+        for (int i = 0; i < words_of<E, N> / 4; ++i) {
+            const u32x4 a = kPast ? __builtin_nontemporal_load(q + i) : q[i];
+            r.w[4 * i] = a.x, r.w[4 * i + 1] = a.y, r.w[4 * i + 2] = a.z, r.w[4 * i + 3] = a.w;
+        }
     }
     return r;
 }
 
-// The first n < 8 of them, zeros behind.
-template <class E>
-__device__ __forceinline__ Raw<E> get_few(const typename E::type *p, int n) {
-    Raw<E> r = raw_zero<E>();
+// The first n < N of them, zeros behind.
+template <class E, int N>
+__device__ __forceinline__ Raw<E, N> get_few(const typename E::type *p, int n) {
+    Raw<E, N> r = raw_zero<E, N>();
 #pragma unroll
-    for (int i = 0; i < 7; ++i) {
+    for (int i = 0; i < N - 1; ++i) {
         if (i >= n) continue;
-        if constexpr (E::kWords == 8)
+        if constexpr (words_of<E, N> == N)
             r.w[i] = float_bits(p[i]);
         else
             r.w[i / 2] |= uint32_t(p[i]) << (16 * (i & 1));
@@ -84,23 +92,30 @@ __device__ __forceinline__ Raw<E> get_few(const typename E::type *p, int n) {
     return r;
 }
 
-template <class E>
-__device__ __forceinline__ void open8(const Raw<E> &r, float (&x)[8]) {
+// n of them (whole from N on, none up to 0).
+template <class E, int N>
+__device__ __forceinline__ Raw<E, N> get_group(const typename E::type *p, int n) {
+    if (n >= N) return get<E, N>(p);
+    return n > 0 ? get_few<E, N>(p, n) : raw_zero<E, N>();
+}
+
+template <class E, int N>
+__device__ __forceinline__ void open(const Raw<E, N> &r, float *x) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if constexpr (E::kWords == 8)
+    for (int i = 0; i < N; ++i) {
+        if constexpr (words_of<E, N> == N)
             x[i] = bits_float(r.w[i]);
         else
             x[i] = bits_float(i & 1 ? r.w[i / 2] & 0xffff0000u : r.w[i / 2] << 16);
     }
 }
 
-template <class E>
-__device__ __forceinline__ Raw<E> close8(const float (&x)[8]) {
-    Raw<E> r;
+template <class E, int N>
+__device__ __forceinline__ Raw<E, N> close(const float *x) {
+    Raw<E, N> r;
 #pragma unroll
-    for (int i = 0; i < E::kWords; ++i) {
-        if constexpr (E::kWords == 8)
+    for (int i = 0; i < words_of<E, N>; ++i) {
+        if constexpr (words_of<E, N> == N)
             r.w[i] = float_bits(x[i]);
         else
             r.w[i] = bf16_bits(x[2 * i]) | bf16_bits(x[2 * i + 1]) << 16;
@@ -108,51 +123,73 @@ __device__ __forceinline__ Raw<E> close8(const float (&x)[8]) {
     return r;
 }
 
-template <class E>
-__device__ __forceinline__ void put8(typename E::type *p, const Raw<E> &r) {
-    typename E::quad *q = reinterpret_cast<typename E::quad *>(p);
+// kPast: results that nothing near reads go past L2, which leaves it to what is still to be read.
+template <class E, int N, bool kPast = false>
+__device__ __forceinline__ void put(typename E::type *p, const Raw<E, N> &r) {
+    if constexpr (words_of<E, N> == 2) {
+        typename E::twin *q = reinterpret_cast<typename E::twin *>(p);
+        const typename E::twin a = u32x2{r.w[0], r.w[1]};
+        if constexpr (kPast)
+            __builtin_nontemporal_store(a, q);
+        else
+            *q = a;
+    } else {
+        typename E::quad *q = reinterpret_cast<typename E::quad *>(p);
 #pragma unroll
-    for (int i = 0; i < E::kWords / 4; ++i)
-        q[i] = u32x4{r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]};
+        for (int i = 0; i < words_of<E, N> / 4; ++i) {
+            const typename E::quad a = u32x4{r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]};
+            if constexpr (kPast)
+                __builtin_nontemporal_store(a, q + i);
+            else
+                q[i] = a;
+        }
+    }
 }
 
-template <class E>
-__device__ __forceinline__ void put_few(typename E::type *p, const Raw<E> &r, int n) {
+template <class E, int N>
+__device__ __forceinline__ void put_few(typename E::type *p, const Raw<E, N> &r, int n) {
 #pragma unroll
-    for (int i = 0; i < 7; ++i) {
+    for (int i = 0; i < N - 1; ++i) {
         if (i >= n) continue;
-        if constexpr (E::kWords == 8)
+        if constexpr (words_of<E, N> == N)
             p[i] = bits_float(r.w[i]);
         else
             p[i] = static_cast<uint16_t>(r.w[i / 2] >> (16 * (i & 1)));
     }
 }
 
-// A group of n elements (up to 8, whole above).
-template <class E>
-__device__ __forceinline__ void put_group(typename E::type *p, const Raw<E> &r, int n) {
-    if (n >= 8)
-        put8<E>(p, r);
+// n of them (whole from N on, none up to 0).
+template <class E, int N, bool kPast = false>
+__device__ __forceinline__ void put_group(typename E::type *p, const Raw<E, N> &r, int n) {
+    if (n >= N)
+        put<E, N, kPast>(p, r);
     else if (n > 0)
-        put_few<E>(p, r, n);
+        put_few<E, N>(p, r, n);
+}
+
+// Elements of a row of n up to the first one at the start of a cache line.
+template <class E>
+__device__ __forceinline__ int before_line(const typename E::type *p, int n) {
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 127u;
+    return min(n, static_cast<int>(((128u - off) & 127u) / sizeof(typename E::type)));
 }
 
 // The groups of a row of n elements that lane `lane` of kLanes takes: group g
-// starts at (g * kLanes + lane) * 8.  Whole groups first, so that their loads
+// starts at (g * kLanes + lane) * N.  Whole groups first, so that their loads
 // are all under way before the one that ends inside is looked at.
-template <class E, int kLanes, int kGroups>
-__device__ __forceinline__ void get_row(const typename E::type *p, int lane, int n, Raw<E> (&r)[kGroups]) {
+template <class E, int N, int kLanes, int kGroups>
+__device__ __forceinline__ void get_row(const typename E::type *p, int lane, int n, Raw<E, N> (&r)[kGroups]) {
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-        const int at = (g * kLanes + lane) * 8;
-        r[g] = raw_zero<E>();
-        if (at + 8 <= n) r[g] = get8<E>(p + at);
+        const int at = (g * kLanes + lane) * N;
+        r[g] = raw_zero<E, N>();
+        if (at + N <= n) r[g] = get<E, N>(p + at);
     }
-    if (n & 7) {
+    if (n & (N - 1)) {
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
-            const int at = (g * kLanes + lane) * 8;
-            if (at < n && at + 8 > n) r[g] = get_few<E>(p + at, n - at);
+            const int at = (g * kLanes + lane) * N;
+            if (at < n && at + N > n) r[g] = get_few<E, N>(p + at, n - at);
         }
     }
 }
