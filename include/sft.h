@@ -1072,6 +1072,7 @@ typedef struct sft_rotary_mat {
  * with inverse != 0 the angle is -a, which is the backward pass: Y takes the
  * gradient of X from that of Y, given as X.  Elements from rot on are copied
  * (left as they are where Y is X).
+ *   mats, n_mats   the arrays
  *   B, T        sequences, and tokens of each
  *   D           elements of a head, rot of them turned (even, 2 <= rot <= D)
  *   pos         device int32, position of token t of sequence b at
@@ -1090,9 +1091,17 @@ typedef struct sft_rotary_mat {
  * or type, amplitude not finite, arrays that overlap), SFT_ESHAPE (rot),
  * SFT_EALIGN, SFT_ENOTSUP (beyond the limits), SFT_EHIP.
  */
-int sft_rotary(const sft_rotary_mat *mats, int32_t n_mats, int64_t B, int64_t T, int64_t D, int64_t rot,
-               const double *freq, const int32_t *pos, int64_t pos_batch, float amplitude, int32_t layout,
-               int32_t inverse, int32_t type, void *stream);
+typedef struct sft_rotary_args {
+    const sft_rotary_mat *mats;
+    int64_t B, T, D, rot;
+    const double *freq;
+    const int32_t *pos;
+    int64_t pos_batch;
+    float amplitude;
+    int32_t n_mats, layout, inverse, type;
+} sft_rotary_args;
+
+int sft_rotary(const sft_rotary_args *args, void *stream);
 
 /* ======================================================================= */
 /* device: log probabilities of given tokens                                */

@@ -170,6 +170,12 @@ class CRotaryMat(C.Structure):
         (n, C.c_int64) for n in ("heads", "x_batch", "x_row", "x_head", "y_batch", "y_row", "y_head")]
 
 
+class CRotaryArgs(C.Structure):
+    _fields_ = [("mats", C.POINTER(CRotaryMat))] + [(n, C.c_int64) for n in ("B", "T", "D", "rot")] + [
+        ("freq", C.c_void_p), ("pos", C.c_void_p), ("pos_batch", C.c_int64), ("amplitude", C.c_float)] + [
+        (n, C.c_int32) for n in ("n_mats", "layout", "inverse", "type")]
+
+
 class CLogprobArgs(C.Structure):
     _fields_ = [(n, C.c_int64) for n in ("N", "V", "ldz")] + [
         (n, C.c_void_p) for n in ("Z", "target", "logp", "stats", "entropy", "top_logp", "top_index")] + [
@@ -242,7 +248,7 @@ def lib() -> C.CDLL:
         L.sft_norm_backward.argtypes = [C.POINTER(CNormGradArgs), p, C.c_size_t, p]
         f64 = C.c_double
         L.sft_rotary_table.argtypes = [i64, f64, i32, f64, f64, f64, f64, p]
-        L.sft_rotary.argtypes = [C.POINTER(CRotaryMat), i32, i64, i64, i64, i64, p, p, i64, f32, i32, i32, i32, p]
+        L.sft_rotary.argtypes = [C.POINTER(CRotaryArgs), p]
         L.sft_logprob.argtypes = [C.POINTER(CLogprobArgs), p]
         L.sft_logprob_grad.argtypes = [C.POINTER(CLogprobGradArgs), p]
         L.sft_probe_grid.argtypes = []
@@ -1380,9 +1386,10 @@ def prepare_rotary(arrays, pos, freq, rot: int, *, layout: str = "half", inverse
         _shape(pos, (B, T), "pos")
         at, pos_batch = _rows(pos, "pos", torch.int32)
     arr = (CRotaryMat * len(mats))(*mats)
-    args = (arr, len(mats), B, T, D, rot, _vector(freq, rot // 2, "freq", torch.float64), at, pos_batch,
-            float(amplitude), _of(ROTARY_LAYOUTS, layout, "layout"), int(bool(inverse)), _type(arrays[0][0], "X"))
-    return PreparedHere(lib().sft_rotary, args, (arr, list(arrays), pos, freq))
+    args = CRotaryArgs(arr, B, T, D, rot, _vector(freq, rot // 2, "freq", torch.float64), at, pos_batch,
+                       float(amplitude), len(mats), _of(ROTARY_LAYOUTS, layout, "layout"), int(bool(inverse)),
+                       _type(arrays[0][0], "X"))
+    return PreparedHere(lib().sft_rotary, (C.byref(args),), (args, arr, list(arrays), pos, freq))
 
 
 def sft_rotary(arrays, pos, freq, rot: int, *, layout: str = "half", inverse: bool = False, amplitude: float = 1.0,

@@ -438,11 +438,13 @@ int check_apart(const Block *written, int n_written, const Block *read, int n_re
 // 32 bytes a lane are best for either type: two eights in bf16 (with residual,
 // 16.8M values of rows of 512, 2048: 21.4 us, one eight 23.3, four 22.4), one in
 // fp32 (8.4M values of rows of 512, 4096: 12.9 and 13.5 us, two 13.9 and 15.8),
-// until there are 512 lanes.
+// until there are 512 lanes.  Narrow rows take several turns of 16 workgroups a
+// CU, as starting one takes longer than its few rows (131072 x 128: 22.3 ->
+// 21.5 us).
 #define SFT_FORWARD_BF16(go) \
-    go(16, 1) go(16, 2) go(32, 2) go(64, 2) go(128, 2) go(256, 2) go(512, 2) go(512, 4)
+    go(8, 1) go(16, 1) go(16, 2) go(32, 2) go(64, 2) go(128, 2) go(256, 2) go(512, 2) go(512, 4)
 #define SFT_FORWARD_FP32(go) \
-    go(16, 1) go(32, 1) go(64, 1) go(128, 1) go(256, 1) go(512, 1) go(512, 2) go(1024, 2)
+    go(8, 1) go(16, 1) go(32, 1) go(64, 1) go(128, 1) go(256, 1) go(512, 1) go(512, 2) go(1024, 2)
 #define SFT_BACKWARD_WIDTHS(go) \
     go(16, 1) go(32, 1) go(64, 1) go(128, 1) go(256, 1) go(512, 1) go(1024, 1) go(1024, 2)
 
@@ -453,7 +455,7 @@ void send_forward(const NormForward &a, hipStream_t st) {
         constexpr int kGroups = eights * 8 / X::kGroup;                                                   \
         constexpr int kThreads = lanes < 256 ? 256 : lanes, kTeams = kThreads / lanes;                    \
         const int64_t rounds = (int64_t(a.T) + kTeams - 1) / kTeams;                                      \
-        const uint32_t grid = static_cast<uint32_t>(std::min<int64_t>(rounds, 1 << 21));                  \
+        const uint32_t grid = static_cast<uint32_t>(std::min<int64_t>(rounds, 16 * num_cus()));           \
         hipLaunchKernelGGL((k_norm_forward<X, Y, lanes, kGroups>), dim3(grid), dim3(kThreads), 0, st, a);  \
         return;                                                                                           \
     }

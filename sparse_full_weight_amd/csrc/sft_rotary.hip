@@ -221,11 +221,15 @@ int sft_rotary_table(int64_t rot, double base, int32_t kind, double factor, doub
     return SFT_OK;
 }
 
-int sft_rotary(const sft_rotary_mat *mats, int32_t n_mats, int64_t B, int64_t T, int64_t D, int64_t rot,
-               const double *freq, const int32_t *pos, int64_t pos_batch, float amplitude, int32_t layout,
-               int32_t inverse, int32_t type, void *stream) {
+int sft_rotary(const sft_rotary_args *v, void *stream) {
     const char *const who = "sft_rotary";
     clear_error();
+    SFT_CHECK(v, SFT_EINVAL, "%s: args is null", who);
+    const sft_rotary_mat *const mats = v->mats;
+    const int32_t n_mats = v->n_mats, layout = v->layout, type = v->type;
+    const int64_t B = v->B, T = v->T, D = v->D, rot = v->rot, pos_batch = v->pos_batch;
+    const double *const freq = v->freq;
+    const int32_t *const pos = v->pos;
     SFT_CHECK(n_mats >= 0 && (n_mats == 0 || mats), SFT_EINVAL, "%s: bad list", who);
     SFT_CHECK(n_mats <= kMaxMats, SFT_ENOTSUP, "%s: more than %d arrays", who, kMaxMats);
     SFT_CHECK(B >= 0 && T >= 0 && D >= 0 && pos_batch >= 0, SFT_EINVAL, "%s: negative size or distance", who);
@@ -235,7 +239,7 @@ int sft_rotary(const sft_rotary_mat *mats, int32_t n_mats, int64_t B, int64_t T,
     SFT_CHECK(rot >= 2 && rot % 2 == 0 && rot <= D, SFT_ESHAPE, "%s: rot is odd, below 2 or above D", who);
     SFT_CHECK(type == SFT_F32 || type == SFT_BF16, SFT_EINVAL, "%s: bad type %d", who, type);
     SFT_CHECK(layout == SFT_ROTARY_HALF || layout == SFT_ROTARY_PAIRS, SFT_EINVAL, "%s: bad layout %d", who, layout);
-    SFT_CHECK(std::isfinite(amplitude), SFT_EINVAL, "%s: amplitude is not finite", who);
+    SFT_CHECK(std::isfinite(v->amplitude), SFT_EINVAL, "%s: amplitude is not finite", who);
     const int64_t total = B * T, size = type_bytes(type), most = int64_t(1) << 40;
     const bool any = n_mats && total;
     SFT_CHECK(!any || (freq && pos), SFT_EINVAL, "%s: freq or pos is null", who);
@@ -284,7 +288,9 @@ int sft_rotary(const sft_rotary_mat *mats, int32_t n_mats, int64_t B, int64_t T,
         r.y_batch = m.y_batch, r.y_row = m.y_row, r.y_head = m.y_head;
         r.units = div_by(static_cast<uint32_t>(units));
         r.heads = div_by(static_cast<uint32_t>(m.heads));
-        const int64_t tokens = std::max<int64_t>(1, std::min<int64_t>(total, kThreads / (units * m.heads)));
+        // as many tokens as give every thread an item, and at most two sines
+        const int64_t tokens = std::max<int64_t>(
+            1, std::min({total, kThreads / (units * m.heads), 2 * kThreads / half}));
         r.tokens = static_cast<int32_t>(tokens);
         r.begin = static_cast<uint32_t>(blocks);
         blocks += (total + tokens - 1) / tokens;
@@ -297,8 +303,8 @@ int sft_rotary(const sft_rotary_mat *mats, int32_t n_mats, int64_t B, int64_t T,
     a.pairs = div_by(static_cast<uint32_t>(half));
     a.D = static_cast<int32_t>(D), a.rot = static_cast<int32_t>(rot), a.total = static_cast<int32_t>(total);
     a.blocks = static_cast<uint32_t>(blocks);
-    a.amplitude = amplitude;
-    a.inverse = inverse != 0;
+    a.amplitude = v->amplitude;
+    a.inverse = v->inverse != 0;
     const dim3 grid(static_cast<uint32_t>(std::min<int64_t>(blocks, 1 << 23))), block(kThreads);
     const size_t lds = static_cast<size_t>(sines + 8) * 8;
     const hipStream_t st = static_cast<hipStream_t>(stream);

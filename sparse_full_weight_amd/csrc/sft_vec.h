@@ -209,10 +209,15 @@ struct Max {
     static __device__ __forceinline__ float of(float a, float b) { return __builtin_fmaxf(a, b); }
 };
 
-// Over each run of kLanes (a power of two from 2 to 64) neighbouring lanes, the same bits in all of them.
+// Over each run of kLanes (8, 16, 32 or 64) neighbouring lanes, the same bits in all of them.
 template <class Op, int kLanes>
 __device__ __forceinline__ float lanes_of(float x) {
-    if constexpr (kLanes >= 16) {          // rotations within 16 lanes
+    static_assert(kLanes == 8 || kLanes == 16 || kLanes == 32 || kLanes == 64, "lanes of a run");
+    if constexpr (kLanes == 8) {           // neighbours, pairs, and the halves of 8 lanes mirrored
+        x = Op::of(x, dpp<0xb1>(x));
+        x = Op::of(x, dpp<0x4e>(x));
+        x = Op::of(x, dpp<0x141>(x));
+    } else {                               // rotations within 16 lanes
         x = Op::of(x, dpp<0x128>(x));
         x = Op::of(x, dpp<0x124>(x));
         x = Op::of(x, dpp<0x122>(x));

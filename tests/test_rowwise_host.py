@@ -121,7 +121,8 @@ HEADS = dict(X=BASE, Y=BASE + 4096, heads=2, x_batch=48, x_row=16, x_head=8, y_b
 def _rotary(mats=(HEADS,), B=2, T=3, D=8, rot=8, freq=BASE + 8192, pos=BASE + 12288, pos_batch=3, amplitude=1.0, layout=0,
             type=0):
     arr = (_lib.CRotaryMat * max(len(mats), 1))(*[_struct(_lib.CRotaryMat, m) for m in mats])
-    return _lib.lib().sft_rotary(arr, len(mats), B, T, D, rot, freq, pos, pos_batch, amplitude, layout, 0, type, None)
+    args = _lib.CRotaryArgs(arr, B, T, D, rot, freq, pos, pos_batch, amplitude, len(mats), layout, 0, type)
+    return _lib.lib().sft_rotary(C.byref(args), None)
 
 
 def _one(**kw):
