@@ -334,7 +334,7 @@ __global__ __launch_bounds__(kThreads) void k_logprob(const Logprob a) {
 #pragma unroll
             for (int u = 0; u < kSteps; ++u) {
                 const int at = place_of<Z, kThreads>(head, turn + u, thread), n = a.V - at;
-                if (n > 0 && n < N) raw[u] = get_few<Z, N>(z + at, n);
+                if (n > 0 && n < N) raw[u] = get_group<Z, N>(z + at, n);
             }
 #pragma unroll
             for (int u = 0; u < kSteps; ++u) {
@@ -444,7 +444,7 @@ __global__ __launch_bounds__(kGradThreads) void k_logprob_grad(const LogprobGrad
 #pragma unroll
         for (int g = 0; g < kGradGroups; ++g) {
             const int at = begin + (g * kLanes + lane) * N, n = a.V - at;
-            raw[g] = n >= N ? get<Z, N, true>(z + at) : n > 0 ? get_few<Z, N>(z + at, n) : raw_zero<Z, N>();
+            raw[g] = n >= N ? get<Z, N, true>(z + at) : get_group<Z, N>(z + at, n);
         }
         const float first = mine ? logit<Z>(z, lane) : 0.0f;
         // scale * (dlogp + dentropy * (logp + entropy)) as a line in log2(p)

@@ -38,12 +38,12 @@ __device__ __forceinline__ float team_sum(float x, float *red) {
 }
 
 // Elements of the vectors gain and bias, of either type.
-template <int N>
+template <int N, bool kEven>
 __device__ __forceinline__ void get_vector(const void *v, bool w32, int at, int n, float *x) {
     if (w32)
-        open<Fp32, N>(get_group<Fp32, N>(static_cast<const float *>(v) + at, n), x);
+        open<Fp32, N>(get_group<Fp32, N, kEven>(static_cast<const float *>(v) + at, n), x);
     else
-        open<Bf16, N>(get_group<Bf16, N>(static_cast<const uint16_t *>(v) + at, n), x);
+        open<Bf16, N>(get_group<Bf16, N, kEven>(static_cast<const uint16_t *>(v) + at, n), x);
 }
 
 struct NormForward {
@@ -58,7 +58,8 @@ struct NormForward {
     bool layer, w32;
 };
 
-template <class X, class Y, int kLanes, int kGroups>
+// kEven: C is a multiple of a group.
+template <class X, class Y, int kLanes, int kGroups, bool kEven>
 __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes) void k_norm_forward(const NormForward a) {
     constexpr int N = X::kGroup, kThreads = kLanes < 256 ? 256 : kLanes, kTeams = kThreads / kLanes;
     __shared__ float red[2][2][kThreads / 64];       // by turns, so that one barrier a sum is enough
@@ -70,11 +71,15 @@ __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes) void k_norm_forward(co
         const bool live = first + team < a.T;
         const int64_t row = live ? first + team : a.T - 1;      // a team without a row stays for the barriers
         Raw<X, N> raw[kGroups];
-        get_row<X, N, kLanes>(static_cast<const xt *>(a.x) + row * a.ldx, lane, C, raw);
+        Few<X, N> few;
+        get_row<X, N, kLanes, kEven>(static_cast<const xt *>(a.x) + row * a.ldx, lane, C, raw, few);
         float x[kGroups][N];
         if (a.res) {
             Raw<X, N> other[kGroups];
-            get_row<X, N, kLanes>(static_cast<const xt *>(a.res) + row * a.ldr, lane, C, other);
+            Few<X, N> other_few;
+            get_row<X, N, kLanes, kEven>(static_cast<const xt *>(a.res) + row * a.ldr, lane, C, other, other_few);
+            join_row<X, N, kLanes, kEven>(lane, C, raw, few);
+            join_row<X, N, kLanes, kEven>(lane, C, other, other_few);
             xt *h = static_cast<xt *>(a.h) + row * a.ldh;
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) {
@@ -86,9 +91,10 @@ __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes) void k_norm_forward(co
                 const Raw<X, N> sum = close<X, N>(x[g]);
                 open<X, N>(sum, x[g]);                    // what is normed is what is kept
                 const int at = (g * kLanes + lane) * N;
-                if (live) put_group<X, N, true>(h + at, sum, C - at);
+                if (live) put_group<X, N, true, kEven>(h + at, sum, C - at);
             }
         } else {
+            join_row<X, N, kLanes, kEven>(lane, C, raw, few);
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) open<X, N>(raw[g], x[g]);
         }
@@ -127,16 +133,16 @@ __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes) void k_norm_forward(co
 #pragma unroll
             for (int i = 0; i < N; ++i) x[g][i] *= rstd;
             if (a.gain) {
-                get_vector<N>(a.gain, a.w32, at, n, w);
+                get_vector<N, kEven>(a.gain, a.w32, at, n, w);
 #pragma unroll
                 for (int i = 0; i < N; ++i) x[g][i] *= w[i];
             }
             if (a.bias) {
-                get_vector<N>(a.bias, a.w32, at, n, w);
+                get_vector<N, kEven>(a.bias, a.w32, at, n, w);
 #pragma unroll
                 for (int i = 0; i < N; ++i) x[g][i] += w[i];
             }
-            put_group<Y, N, true>(y + at, close<Y, N>(x[g]), n);
+            put_group<Y, N, true, kEven>(y + at, close<Y, N>(x[g]), n);
         }
     }
 }
@@ -161,15 +167,17 @@ struct NormRow {
     static constexpr int N = X::kGroup;
     Raw<X, N> h[kGroups], dh[kGroups];
     Raw<Y, N> dy[kGroups];
+    Few<X, N> few_h, few_dh;
+    Few<Y, N> few_dy;
     float mean, rstd;
 };
 
-template <class X, class Y, int kLanes, int kGroups>
+template <class X, class Y, int kLanes, bool kEven, int kGroups>
 __device__ __forceinline__ void get_norm_row(const NormBackward &a, int64_t row, int lane, NormRow<X, Y, kGroups> &r) {
     constexpr int N = X::kGroup;
-    get_row<X, N, kLanes>(static_cast<const typename X::type *>(a.h) + row * a.ldh, lane, a.C, r.h);
-    get_row<Y, N, kLanes>(static_cast<const typename Y::type *>(a.dy) + row * a.ldy, lane, a.C, r.dy);
-    if (a.dh) get_row<X, N, kLanes>(static_cast<const typename X::type *>(a.dh) + row * a.ldr, lane, a.C, r.dh);
+    get_row<X, N, kLanes, kEven>(static_cast<const typename X::type *>(a.h) + row * a.ldh, lane, a.C, r.h, r.few_h);
+    get_row<Y, N, kLanes, kEven>(static_cast<const typename Y::type *>(a.dy) + row * a.ldy, lane, a.C, r.dy, r.few_dy);
+    if (a.dh) get_row<X, N, kLanes, kEven>(static_cast<const typename X::type *>(a.dh) + row * a.ldr, lane, a.C, r.dh, r.few_dh);
     r.rstd = a.rstd[row];
     r.mean = a.layer ? a.mean[row] : 0.0f;
 }
@@ -180,7 +188,7 @@ __device__ __forceinline__ void get_norm_row(const NormBackward &a, int64_t row,
 // its sums go to its own place in the workspace.
 // kSums: 0 = no sums over rows, 1 = dgain, 2 = dgain and dbias.  The widest
 // rows leave no registers for a row ahead or for the gains.
-template <class X, class Y, int kLanes, int kGroups, int kSums>
+template <class X, class Y, int kLanes, int kGroups, bool kEven, int kSums>
 __device__ __forceinline__ void norm_rows(const NormBackward &a, uint32_t block, uint32_t blocks) {
     constexpr int N = X::kGroup, kTeams = kRowThreads / kLanes, kWidth = kLanes * kGroups * N;
     constexpr bool kAhead = kWidth <= 8192;
@@ -193,12 +201,12 @@ __device__ __forceinline__ void norm_rows(const NormBackward &a, uint32_t block,
     const int64_t stride = int64_t(blocks) * kTeams;
     int64_t first = int64_t(block) * kTeams;           // there are never more workgroups than rows for them
     NormRow<X, Y, kGroups> next;
-    if (kAhead) get_norm_row<X, Y, kLanes>(a, min(first + team, int64_t(a.T) - 1), lane, next);
+    if (kAhead) get_norm_row<X, Y, kLanes, kEven>(a, min(first + team, int64_t(a.T) - 1), lane, next);
     const auto get_gain = [&](int g) {
         const int at = (g * kLanes + lane) * N, n = C - at;
 #pragma unroll
         for (int i = 0; i < N; ++i) gain[g][i] = 1.0f;
-        if (a.gain && n > 0) get_vector<N>(a.gain, a.w32, at, n, gain[g]);
+        if (a.gain && n > 0) get_vector<N, kEven>(a.gain, a.w32, at, n, gain[g]);
     };
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
@@ -210,10 +218,13 @@ __device__ __forceinline__ void norm_rows(const NormBackward &a, uint32_t block,
     for (int turn = 0; first < a.T; first += stride, turn ^= 1) {
         const bool live = first + team < a.T;           // a team without a row stays for the barriers
         const int64_t row = live ? first + team : a.T - 1;
-        if (!kAhead) get_norm_row<X, Y, kLanes>(a, row, lane, next);
-        const NormRow<X, Y, kGroups> r = next;
+        if (!kAhead) get_norm_row<X, Y, kLanes, kEven>(a, row, lane, next);
+        NormRow<X, Y, kGroups> r = next;
+        join_row<X, N, kLanes, kEven>(lane, C, r.h, r.few_h);
+        join_row<Y, N, kLanes, kEven>(lane, C, r.dy, r.few_dy);
+        if (a.dh) join_row<X, N, kLanes, kEven>(lane, C, r.dh, r.few_dh);
         if (kAhead && first + stride < a.T)
-            get_norm_row<X, Y, kLanes>(a, min(first + stride + team, int64_t(a.T) - 1), lane, next);
+            get_norm_row<X, Y, kLanes, kEven>(a, min(first + stride + team, int64_t(a.T) - 1), lane, next);
         float x[kGroups][N], d[kGroups][N];
         float along = 0.0f, flat = 0.0f;
 #pragma unroll
@@ -266,7 +277,7 @@ __device__ __forceinline__ void norm_rows(const NormBackward &a, uint32_t block,
 #pragma unroll
                 for (int i = 0; i < N; ++i) d[g][i] += other[i];
             }
-            if (live) put_group<X, N, true>(dx + at, close<X, N>(d[g]), C - at);
+            if (live) put_group<X, N, true, kEven>(dx + at, close<X, N>(d[g]), C - at);
         }
     }
     if constexpr (kSums > 0) {
@@ -302,8 +313,8 @@ __device__ __forceinline__ void norm_rows(const NormBackward &a, uint32_t block,
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
             const int at = (g * kLanes + lane) * N;
-            put_group<Fp32, N>(part + at, close<Fp32, N>(dgain[g]), C - at);
-            if (kSums > 1) put_group<Fp32, N>(part + int64_t(blocks) * C + at, close<Fp32, N>(dbias[g]), C - at);
+            put_group<Fp32, N, false, kEven>(part + at, close<Fp32, N>(dgain[g]), C - at);
+            if (kSums > 1) put_group<Fp32, N, false, kEven>(part + int64_t(blocks) * C + at, close<Fp32, N>(dbias[g]), C - at);
         }
     }
 }
@@ -366,19 +377,19 @@ __device__ __forceinline__ void norm_columns(const NormBackward &a, const NormSu
     put_sum(s, 1, c, dbias);
 }
 
-template <class X, class Y, int kLanes, int kGroups, int kSums>
+template <class X, class Y, int kLanes, int kGroups, bool kEven, int kSums>
 __global__ __launch_bounds__(kRowThreads) void k_norm_backward(const NormBackward a) {
-    norm_rows<X, Y, kLanes, kGroups, kSums>(a, blockIdx.x, gridDim.x);
+    norm_rows<X, Y, kLanes, kGroups, kEven, kSums>(a, blockIdx.x, gridDim.x);
 }
 
 // Rows and columns in one launch, the columns' workgroups first.
-template <class X, class Y, int kLanes, int kGroups>
+template <class X, class Y, int kLanes, int kGroups, bool kEven>
 __global__ __launch_bounds__(kRowThreads) void k_norm_backward_few(const NormBackward a, const NormSums s,
                                                                    uint32_t columns) {
     if (blockIdx.x < columns)
         norm_columns<X, Y>(a, s, blockIdx.x);
     else
-        norm_rows<X, Y, kLanes, kGroups, 0>(a, blockIdx.x - columns, gridDim.x - columns);
+        norm_rows<X, Y, kLanes, kGroups, kEven, 0>(a, blockIdx.x - columns, gridDim.x - columns);
 }
 
 // The workgroups' sums in a fixed order: 32 columns a workgroup, 32 shares of them.
@@ -448,16 +459,16 @@ int check_apart(const Block *written, int n_written, const Block *read, int n_re
 #define SFT_BACKWARD_WIDTHS(go) \
     go(16, 1) go(32, 1) go(64, 1) go(128, 1) go(256, 1) go(512, 1) go(1024, 1) go(1024, 2)
 
-template <class X, class Y>
+template <class X, class Y, bool kEven>
 void send_forward(const NormForward &a, hipStream_t st) {
-#define SFT_GO(lanes, eights)                                                                             \
-    if (a.C <= lanes * eights * 8) {                                                                      \
-        constexpr int kGroups = eights * 8 / X::kGroup;                                                   \
-        constexpr int kThreads = lanes < 256 ? 256 : lanes, kTeams = kThreads / lanes;                    \
-        const int64_t rounds = (int64_t(a.T) + kTeams - 1) / kTeams;                                      \
-        const uint32_t grid = static_cast<uint32_t>(std::min<int64_t>(rounds, 16 * num_cus()));           \
-        hipLaunchKernelGGL((k_norm_forward<X, Y, lanes, kGroups>), dim3(grid), dim3(kThreads), 0, st, a);  \
-        return;                                                                                           \
+#define SFT_GO(lanes, eights)                                                                                   \
+    if (a.C <= lanes * eights * 8) {                                                                            \
+        constexpr int kGroups = eights * 8 / X::kGroup;                                                         \
+        constexpr int kThreads = lanes < 256 ? 256 : lanes, kTeams = kThreads / lanes;                          \
+        const int64_t rounds = (int64_t(a.T) + kTeams - 1) / kTeams;                                            \
+        const uint32_t grid = static_cast<uint32_t>(std::min<int64_t>(rounds, 16 * num_cus()));                 \
+        hipLaunchKernelGGL((k_norm_forward<X, Y, lanes, kGroups, kEven>), dim3(grid), dim3(kThreads), 0, st, a); \
+        return;                                                                                                 \
     }
     if constexpr (X::kType == SFT_BF16) {
         SFT_FORWARD_BF16(SFT_GO)
@@ -465,6 +476,12 @@ void send_forward(const NormForward &a, hipStream_t st) {
         SFT_FORWARD_FP32(SFT_GO)
     }
 #undef SFT_GO
+}
+
+template <class X, class Y>
+void send_forward(const NormForward &a, hipStream_t st) {
+    if (a.C % X::kGroup) send_forward<X, Y, false>(a, st);
+    else send_forward<X, Y, true>(a, st);
 }
 
 int backward_teams(int64_t C) {
@@ -481,22 +498,28 @@ int backward_groups(int64_t T, int64_t C) {
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((T + teams - 1) / teams, num_cus())));
 }
 
-template <class X, class Y>
+template <class X, class Y, bool kEven>
 void send_backward(const NormBackward &a, const NormSums *few, int sums, hipStream_t st) {
     const uint32_t rows = static_cast<uint32_t>(backward_groups(a.T, a.C));
     const uint32_t columns = static_cast<uint32_t>((a.C + kColumns - 1) / kColumns);
-    const dim3 grid(rows), all(rows + columns), block(kRowThreads);
-#define SFT_GO(lanes, eights)                                                                                        \
-    if (a.C <= lanes * eights * 8) {                                                                                 \
-        constexpr int kGroups = eights * 8 / X::kGroup;                                                              \
-        if (few) hipLaunchKernelGGL((k_norm_backward_few<X, Y, lanes, kGroups>), all, block, 0, st, a, *few, columns); \
-        else if (sums == 0) hipLaunchKernelGGL((k_norm_backward<X, Y, lanes, kGroups, 0>), grid, block, 0, st, a);    \
-        else if (sums == 1) hipLaunchKernelGGL((k_norm_backward<X, Y, lanes, kGroups, 1>), grid, block, 0, st, a);    \
-        else hipLaunchKernelGGL((k_norm_backward<X, Y, lanes, kGroups, 2>), grid, block, 0, st, a);                   \
-        return;                                                                                                      \
+    const dim3 grid(few ? rows + columns : rows), block(kRowThreads);
+#define SFT_GO(lanes, eights)                                                                                           \
+    if (a.C <= lanes * eights * 8) {                                                                                    \
+        constexpr int kGroups = eights * 8 / X::kGroup;                                                                 \
+        if (few) hipLaunchKernelGGL((k_norm_backward_few<X, Y, lanes, kGroups, kEven>), grid, block, 0, st, a, *few, columns); \
+        else if (sums == 0) hipLaunchKernelGGL((k_norm_backward<X, Y, lanes, kGroups, kEven, 0>), grid, block, 0, st, a); \
+        else if (sums == 1) hipLaunchKernelGGL((k_norm_backward<X, Y, lanes, kGroups, kEven, 1>), grid, block, 0, st, a); \
+        else hipLaunchKernelGGL((k_norm_backward<X, Y, lanes, kGroups, kEven, 2>), grid, block, 0, st, a);                \
+        return;                                                                                                         \
     }
     SFT_BACKWARD_WIDTHS(SFT_GO)
 #undef SFT_GO
+}
+
+template <class X, class Y>
+void send_backward(const NormBackward &a, const NormSums *few, int sums, hipStream_t st) {
+    if (a.C % X::kGroup) send_backward<X, Y, false>(a, few, sums, st);
+    else send_backward<X, Y, true>(a, few, sums, st);
 }
 
 size_t backward_bytes(int64_t T, int64_t C, bool with_bias) {

@@ -30,8 +30,12 @@ struct Fp32 {
     static constexpr int kGroup = 4;
     static constexpr int32_t kType = SFT_F32;
     typedef u32x4 __attribute__((aligned(4))) quad;
+    typedef u32x2 __attribute__((aligned(4))) twin;
+    typedef uint32_t word;
     static __device__ __forceinline__ float up(float x) { return x; }
     static __device__ __forceinline__ float down(float x) { return x; }
+    static __device__ __forceinline__ uint32_t bits(float x) { return float_bits(x); }
+    static __device__ __forceinline__ float of_bits(uint32_t x) { return bits_float(x); }
 };
 struct Bf16 {
     typedef uint16_t type;
@@ -39,8 +43,11 @@ struct Bf16 {
     static constexpr int32_t kType = SFT_BF16;
     typedef u32x4 __attribute__((aligned(2))) quad;
     typedef u32x2 __attribute__((aligned(2))) twin;
+    typedef uint32_t __attribute__((aligned(2))) word;
     static __device__ __forceinline__ float up(uint16_t x) { return bits_float(uint32_t(x) << 16); }
     static __device__ __forceinline__ uint16_t down(float x) { return static_cast<uint16_t>(bf16_bits(x)); }
+    static __device__ __forceinline__ uint32_t bits(uint16_t x) { return x; }
+    static __device__ __forceinline__ uint16_t of_bits(uint32_t x) { return static_cast<uint16_t>(x); }
 };
 
 // N elements (4 or 8) as they are in memory.
@@ -77,26 +84,77 @@ __device__ __forceinline__ Raw<E, N> get(const typename E::type *p) {
     return r;
 }
 
-// The first n < N of them, zeros behind.
+// The first n < N of them, in pieces of half a group, a quarter and so on: n in
+// binary.  Few holds the pieces as loaded, so that waiting for them can wait;
+// whole() puts them together, zeros behind.
 template <class E, int N>
-__device__ __forceinline__ Raw<E, N> get_few(const typename E::type *p, int n) {
-    Raw<E, N> r = raw_zero<E, N>();
+struct Few {
+    static constexpr int kWords = words_of<E, N> > N / 2 ? N - 1 : N / 2;      // a lone bf16 takes a word
+    uint32_t w[kWords];
+};
+
+template <class E, int N>
+__device__ __forceinline__ Few<E, N> few_zero() {
+    Few<E, N> f;
 #pragma unroll
-    for (int i = 0; i < N - 1; ++i) {
-        if (i >= n) continue;
-        if constexpr (words_of<E, N> == N)
-            r.w[i] = float_bits(p[i]);
-        else
-            r.w[i / 2] |= uint32_t(p[i]) << (16 * (i & 1));
+    for (int i = 0; i < Few<E, N>::kWords; ++i) f.w[i] = 0;
+    return f;
+}
+
+template <class E, int N>
+__device__ __forceinline__ void get_few(const typename E::type *p, int n, Few<E, N> &f) {
+    int k = 0;
+#pragma unroll
+    for (int half = N / 2; half; half /= 2) {
+        const int words = half * int(sizeof(typename E::type)) / 4;
+        if (n & half) {
+            if (words == 4) {
+                const u32x4 a = *reinterpret_cast<const typename E::quad *>(p);
+                f.w[k] = a.x, f.w[k + 1] = a.y, f.w[k + 2] = a.z, f.w[k + 3] = a.w;
+            } else if (words == 2) {
+                const u32x2 a = *reinterpret_cast<const typename E::twin *>(p);
+                f.w[k] = a.x, f.w[k + 1] = a.y;
+            } else if (words == 1) {
+                f.w[k] = *reinterpret_cast<const typename E::word *>(p);
+            } else {
+                f.w[k] = E::bits(*p);
+            }
+            p += half;
+        }
+        k += words ? words : 1;
+    }
+}
+
+template <class E, int N>
+__device__ __forceinline__ Raw<E, N> whole(const Few<E, N> &f, int n) {
+    // the pieces from the last one on, each before what is there already
+    constexpr int size = sizeof(typename E::type), W = words_of<E, N>;
+    Raw<E, N> r = raw_zero<E, N>();
+    int k = Few<E, N>::kWords;
+#pragma unroll
+    for (int half = 1; half < N; half *= 2) {
+        const int words = half * size / 4;
+        k -= words ? words : 1;
+        if (n & half) {
+            if (words == 0) {
+                r.w[0] = f.w[k];
+            } else {
+#pragma unroll
+                for (int i = W - 1; i >= 0; --i) r.w[i] = i >= words ? r.w[i - words] : f.w[k + i];
+            }
+        }
     }
     return r;
 }
 
 // n of them (whole from N on, none up to 0).
-template <class E, int N>
+template <class E, int N, bool kEven = false>
 __device__ __forceinline__ Raw<E, N> get_group(const typename E::type *p, int n) {
     if (n >= N) return get<E, N>(p);
-    return n > 0 ? get_few<E, N>(p, n) : raw_zero<E, N>();
+    if (n <= 0 || kEven) return raw_zero<E, N>();
+    Few<E, N> f = few_zero<E, N>();
+    get_few<E, N>(p, n, f);
+    return whole<E, N>(f, n);
 }
 
 template <class E, int N>
@@ -147,23 +205,32 @@ __device__ __forceinline__ void put(typename E::type *p, const Raw<E, N> &r) {
 }
 
 template <class E, int N>
-__device__ __forceinline__ void put_few(typename E::type *p, const Raw<E, N> &r, int n) {
+__device__ __forceinline__ void put_few(typename E::type *p, Raw<E, N> r, int n) {
+    constexpr int size = sizeof(typename E::type), W = words_of<E, N>;
 #pragma unroll
-    for (int i = 0; i < N - 1; ++i) {
-        if (i >= n) continue;
-        if constexpr (words_of<E, N> == N)
-            p[i] = bits_float(r.w[i]);
+    for (int half = N / 2; half; half /= 2) {
+        const int words = half * size / 4;
+        if (!(n & half)) continue;
+        if (words == 4)
+            *reinterpret_cast<typename E::quad *>(p) = u32x4{r.w[0], r.w[1], r.w[2], r.w[W - 1 < 3 ? W - 1 : 3]};
+        else if (words == 2)
+            *reinterpret_cast<typename E::twin *>(p) = u32x2{r.w[0], r.w[W - 1 < 1 ? W - 1 : 1]};
+        else if (words == 1)
+            *reinterpret_cast<typename E::word *>(p) = r.w[0];
         else
-            p[i] = static_cast<uint16_t>(r.w[i / 2] >> (16 * (i & 1)));
+            *p = E::of_bits(r.w[0]);
+        p += half;
+#pragma unroll
+        for (int i = 0; i < W; ++i) r.w[i] = i + words < W ? r.w[i + words] : 0;
     }
 }
 
 // n of them (whole from N on, none up to 0).
-template <class E, int N, bool kPast = false>
+template <class E, int N, bool kPast = false, bool kEven = false>
 __device__ __forceinline__ void put_group(typename E::type *p, const Raw<E, N> &r, int n) {
     if (n >= N)
         put<E, N, kPast>(p, r);
-    else if (n > 0)
+    else if (n > 0 && !kEven)
         put_few<E, N>(p, r, n);
 }
 
@@ -175,23 +242,31 @@ __device__ __forceinline__ int before_line(const typename E::type *p, int n) {
 }
 
 // The groups of a row of n elements that lane `lane` of kLanes takes: group g
-// starts at (g * kLanes + lane) * N.  Whole groups first, so that their loads
-// are all under way before the one that ends inside is looked at.
-template <class E, int N, int kLanes, int kGroups>
-__device__ __forceinline__ void get_row(const typename E::type *p, int lane, int n, Raw<E, N> (&r)[kGroups]) {
+// starts at (g * kLanes + lane) * N.  The pieces of the one that ends inside wait
+// in `few` for join_row, so that nothing here waits for a load; kEven: there is
+// none, n is a multiple of N.
+template <class E, int N, int kLanes, bool kEven, int kGroups>
+__device__ __forceinline__ void get_row(const typename E::type *p, int lane, int n, Raw<E, N> (&r)[kGroups],
+                                        Few<E, N> &few) {
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
         const int at = (g * kLanes + lane) * N;
         r[g] = raw_zero<E, N>();
         if (at + N <= n) r[g] = get<E, N>(p + at);
     }
-    if (n & (N - 1)) {
+    if (kEven) return;
+    const int last = n & (N - 1);
+    few = few_zero<E, N>();
+    if (last && (n / N) % kLanes == lane) get_few<E, N>(p + (n - last), last, few);
+}
+
+template <class E, int N, int kLanes, bool kEven, int kGroups>
+__device__ __forceinline__ void join_row(int lane, int n, Raw<E, N> (&r)[kGroups], const Few<E, N> &few) {
+    const int last = n & (N - 1);
+    if (kEven || !last) return;
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-            const int at = (g * kLanes + lane) * N;
-            if (at < n && at + N > n) r[g] = get_few<E, N>(p + at, n - at);
-        }
-    }
+    for (int g = 0; g < kGroups; ++g)
+        if (n / N == g * kLanes + lane) r[g] = whole<E, N>(few, last);
 }
 
 // ---- over the lanes of a wave
