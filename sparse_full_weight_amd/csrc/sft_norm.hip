@@ -240,7 +240,7 @@ __device__ __forceinline__ void norm_rows(const NormBackward &a, uint32_t block,
                     if (kSums > 1) dbias[g][i] += d[g][i];
                 }
                 d[g][i] *= gain[g][i];
-                along = __builtin_fmaf(d[g][i], x[g][i], along);
+                along += d[g][i] * x[g][i];
                 flat += d[g][i];
             }
         }
@@ -270,7 +270,7 @@ __device__ __forceinline__ void norm_rows(const NormBackward &a, uint32_t block,
         for (int g = 0; g < kGroups; ++g) {
             const int at = (g * kLanes + lane) * N;
 #pragma unroll
-            for (int i = 0; i < N; ++i) d[g][i] = (d[g][i] - flat - x[g][i] * along) * r.rstd;
+            for (int i = 0; i < N; ++i) d[g][i] = (d[g][i] - x[g][i] * along - flat) * r.rstd;
             if (a.dh) {
                 float other[N];
                 open<X, N>(r.dh[g], other);

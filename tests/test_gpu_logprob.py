@@ -110,6 +110,23 @@ def test_many_rows_of_long_vocabularies(gpu_lib, dtype):
     check(z, torch.randint(0, 20011, (530,), generator=gen(3)), 1.0, 7)
 
 
+def test_rows_of_several_rounds_a_block(gpu_lib):
+    # 256 threads a row, nine rounds of 32 logits a thread in eight blocks
+    N, V, K = 520, 70001, 11
+    z = torch.randn(N, V, device="cuda", generator=torch.Generator("cuda").manual_seed(4)) * 2.5
+    target = torch.arange(N, device="cuda") * 130
+    logp, index = torch.zeros(N, device="cuda"), torch.zeros(N, K, dtype=torch.int32, device="cuda")
+    top = torch.zeros(N, K, device="cuda")
+    _lib.sft_logprob(z, target.int(), logp, top_logp=top, top_index=index)
+    lp = torch.log_softmax(z.double(), 1)
+    want = torch.sort(z, dim=1, descending=True, stable=True)[1][:, :K]
+    assert torch.equal(index.long(), want)
+    # as in exact(): the sum's additions, and roundings relative to differences from the largest logit (25 at most)
+    bound = (V / 256 * 1.125 + 48 + 3 * 12 + 5 * 25) * U
+    assert (logp.double() - lp.gather(1, target[:, None])[:, 0]).abs().max() <= bound
+    assert (top.double() - lp.gather(1, want)).abs().max() <= bound
+
+
 def test_targets_that_are_none_or_not_allowed(gpu_lib):
     z = logits(6, 1000, 4)
     z[2, 17] = -INF
@@ -184,7 +201,7 @@ def test_rows_that_are_not_finite(gpu_lib, V):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("V,N", [(700, 2), (40000, 2), (20000, 520)])
+@pytest.mark.parametrize("V,N", [(300, 3), (700, 2), (5000, 3), (20000, 2), (40000, 2), (300000, 2), (20000, 520)])
 def test_alternatives_of_equal_logits(gpu_lib, dtype, V, N):
     # rows of few different values; of one value; ascending, descending; the two zeros; all large ones with few threads
     z = torch.round(normal((N, V), 1.2, V))
