@@ -137,29 +137,55 @@ template <int kThreads, int kTop>
 struct TopPlace {
     static constexpr int kFound = kThreads == 64 ? 512 : 1024;
     static constexpr int kItems = kTop == 1 || kThreads == 64 ? kSlots : 1024;
-    float mine[kThreads], block[kTop == 2 ? kBlocks<kThreads> : 1][kTop == 2 ? kThreads : 1];
-    float held[kTop == 1 ? kSlots * kRound : 1];
+    f32x4 held[kTop == 1 ? kSlots * kRound / 4 : 1];
     uint64_t found[kFound];
+    float mine[kThreads], block[kTop == 2 ? kBlocks<kThreads> : 1][kTop == 2 ? kThreads : 1];
     int32_t item[kItems];
-    float threshold;
+    float threshold, M, L;
+    bool plain;
     int items, n;
 };
 
-// The K likeliest of a row, of which every thread knows the largest logit that
-// it has seen.  The K-th largest of those is a bound that at least K logits
-// reach, so only threads whose own largest reaches it have alternatives.  Their
-// logits that reach the bound are collected, by the whole workgroup, and ranked by
+struct Or {
+    static __device__ __forceinline__ float of(float a, float b) { return bits_float(float_bits(a) | float_bits(b)); }
+};
+
+// A bound that at least K of the threads' largest logits reach (K <= 64): the
+// K-th largest of 64, each of them the largest of every 64th thread, found by
+// halving from the first bit on in which they differ.  By one wave.
+template <int kThreads>
+__device__ __forceinline__ float bound_of(const float *mine, int K) {
+    const int lane = static_cast<int>(threadIdx.x);
+    float x = mine[lane];
+#pragma unroll
+    for (int i = 1; i < kThreads / 64; ++i) x = __builtin_fmaxf(x, mine[lane + 64 * i]);
+    const uint32_t o = order_of(x), one = __builtin_amdgcn_readfirstlane(o);
+    const uint32_t differ = __builtin_amdgcn_readfirstlane(float_bits(lanes_of<Or, 64>(bits_float(o ^ one))));
+    if (differ == 0) return float_of(one);
+    const uint32_t top = 31u - static_cast<uint32_t>(__builtin_clz(differ));
+    uint32_t bound = one & ~((2u << top) - 1u);
+    for (uint32_t bit = 1u << top; bit; bit >>= 1) {
+        const int reach = __builtin_popcountll(__ballot(o >= (bound | bit)));
+        if (reach >= K) bound |= bit;
+        if (reach == K) break;
+    }
+    return float_of(max(bound, order_of(-kInf)));
+}
+
+// The K likeliest of a row, given a bound that at least K logits reach: only
+// threads whose own largest logit reaches it have alternatives.  Their logits
+// that reach the bound are collected, by the whole workgroup, and ranked by
 // counting; those of rows of one round (kTop = 1) are still at hand, else the
-// blocks that reach the bound are read again.  Where too much reaches it,
-// or a NaN may have hidden a thread's largest, the alternatives are looked for
-// one by one.
+// blocks that reach the bound are read again.  Where too much reaches it, or a
+// NaN may have hidden a thread's largest, the alternatives are looked for one
+// by one, the row read again for each.
 template <class Z, int kThreads, int kTop, int R>
-__device__ __forceinline__ void top_of(const Logprob &a, int64_t row, float mine, bool plain, float M, float L,
-                                       const float (&last)[R], int head, int turns, int rounds,
-                                       TopPlace<kThreads, kTop> &s) {
+__device__ __forceinline__ void top_of(const Logprob &a, int64_t row, float mine, const float (&last)[R], int head,
+                                       int turns, int rounds, TopPlace<kThreads, kTop> &s) {
     constexpr int N = Z::kGroup, kSteps = R / N, kFound = TopPlace<kThreads, kTop>::kFound;
     constexpr int kItems = TopPlace<kThreads, kTop>::kItems;
     const int thread = static_cast<int>(threadIdx.x);
+    const float M = s.M, L = s.L;
     const typename Z::type *z = static_cast<const typename Z::type *>(a.z) + row * a.ld;
     float *top_logp = a.top_logp ? a.top_logp + row * a.top : nullptr;
     int32_t *top_index = a.top_index + row * a.top;
@@ -173,25 +199,7 @@ __device__ __forceinline__ void top_of(const Logprob &a, int64_t row, float mine
         top_index[rank] = -1;
         if (top_logp) top_logp[rank] = -kInf;
     };
-    if (plain) {
-        s.mine[thread] = mine;
-        if (thread == 0) s.items = s.n = 0;
-        __syncthreads();
-        if (thread < 64) {
-            // of every 64th thread the largest, then the K-th largest of those 64 by halving
-            float x = s.mine[thread];
-#pragma unroll
-            for (int i = 1; i < kThreads / 64; ++i) x = __builtin_fmaxf(x, s.mine[thread + 64 * i]);
-            const uint32_t o = order_of(x);
-            uint32_t bound = 0;
-            for (uint32_t bit = 1u << 31; bit; bit >>= 1) {
-                const int reach = __builtin_popcountll(__ballot(o >= (bound | bit)));
-                if (reach >= a.top) bound |= bit;
-                if (reach == a.top) break;
-            }
-            if (thread == 0) s.threshold = float_of(max(bound, order_of(-kInf)));
-        }
-        __syncthreads();
+    if (s.plain) {
         const float threshold = s.threshold;
         const auto reaches = [&](float x) { return x >= threshold && x > -kInf; };
         const auto collect = [&](float x, int at) {
@@ -208,7 +216,8 @@ __device__ __forceinline__ void top_of(const Logprob &a, int64_t row, float mine
                 if (k < kItems) {
                     s.item[k] = thread;
 #pragma unroll
-                    for (int i = 0; i < R; ++i) s.held[k * R + i] = last[i];      // (-infinity behind the row's end)
+                    for (int i = 0; i < R; i += 4)      // (-infinity behind the row's end)
+                        s.held[(k * R + i) / 4] = f32x4{last[i], last[i + 1], last[i + 2], last[i + 3]};
                 }
             } else {
                 const int blocks = (turns + kSteps * rounds - 1) / (kSteps * rounds);
@@ -225,7 +234,8 @@ __device__ __forceinline__ void top_of(const Logprob &a, int64_t row, float mine
             if constexpr (kTop == 1) {
                 for (int p = thread; p < items * R; p += kThreads) {
                     const int k = p / R, i = p % R;
-                    if (reaches(s.held[p])) collect(s.held[p], place_of<Z, kThreads>(head, i / N, s.item[k]) + i % N);
+                    const float x = reinterpret_cast<const float *>(s.held)[p];
+                    if (reaches(x)) collect(x, place_of<Z, kThreads>(head, i / N, s.item[k]) + i % N);
                 }
             } else {
                 const int each = kSteps * rounds;            // turns of a block
@@ -355,8 +365,7 @@ __global__ __launch_bounds__(kThreads) void k_logprob(const Logprob a) {
         float M = block_of<Max, kThreads>(r.m, red[0]);
         const float m2 = __builtin_fmaxf(M * a.c, -kFar);
         const float less = limit(r.m2 - m2, kNothing, 0.0f), part = exp2_of(less);
-        float along = kEntropy ? block_of<Sum, kThreads>(part * __builtin_fmaf(r.sum, less, r.along), red[1]) : 0.0f;
-        float sum = block_of<Sum, kThreads>(r.sum * part, red[2]);
+        float along = part * __builtin_fmaf(r.sum, less, r.along), sum = r.sum * part;
         // what m2 is off M * c by
         float off = __builtin_fmaf(M, a.c, -m2);
         const bool finite = __builtin_fabsf(M) < kInf;
@@ -367,31 +376,60 @@ __global__ __launch_bounds__(kThreads) void k_logprob(const Logprob a) {
                 sum += e;
                 along = __builtin_fmaf(e, __builtin_fmaxf(d, kNothing), along);
             }
-            __syncthreads();
-            along = block_of<Sum, kThreads>(along, red[1]);
-            sum = block_of<Sum, kThreads>(sum, red[2]);
         }
-        const bool none = M == -kInf && sum == 0.0f;      // a row without an allowed token
-        float L = logf(sum), entropy = 0.0f;
-        // neither is below 0, whatever the roundings
-        if (kEntropy) entropy = __builtin_fmaxf(L - kLn2 * (along / sum), 0.0f);
-        L = __builtin_fmaxf(L - kLn2 * off, 0.0f);
-        if (!finite || sum != sum) {
-            const float nan = __builtin_nanf("");
-            M = none ? -kInf : nan;
-            L = none ? -kInf : nan;
-            entropy = none ? 0.0f : nan;
+        sum = lanes_of<Sum, 64>(sum);
+        if (kEntropy) along = lanes_of<Sum, 64>(along);
+        if (kWaves > 1 && (thread & 63) == 0) {
+            red[1][thread >> 6] = sum;
+            if (kEntropy) red[2][thread >> 6] = along;
         }
-        if (thread == 0) {
-            if (a.logp) a.logp[row] = !given ? 0.0f : none ? -kInf : a.scale * (at_target - M) - L;
-            if (a.stats) {
-                a.stats[2 * row] = M;
-                a.stats[2 * row + 1] = L;
+        if constexpr (kTop > 0) {
+            top.mine[thread] = r.m;
+            if (thread == 0) top.items = top.n = 0;
+        }
+        __syncthreads();
+        if (thread < 64) {        // one wave finishes the row
+            if constexpr (kWaves > 1) {
+                sum = red[1][0];
+                if (kEntropy) along = red[2][0];
+#pragma unroll
+                for (int i = 1; i < kWaves; ++i) {
+                    sum += red[1][i];
+                    if (kEntropy) along += red[2][i];
+                }
             }
-            if (kEntropy) a.entropy[row] = entropy;
+            const bool none = M == -kInf && sum == 0.0f;      // a row without an allowed token
+            float L = logf(sum), entropy = 0.0f;
+            // neither is below 0, whatever the roundings
+            if (kEntropy) entropy = __builtin_fmaxf(L - kLn2 * (along / sum), 0.0f);
+            L = __builtin_fmaxf(L - kLn2 * off, 0.0f);
+            if (!finite || sum != sum) {
+                const float nan = __builtin_nanf("");
+                M = none ? -kInf : nan;
+                L = none ? -kInf : nan;
+                entropy = none ? 0.0f : nan;
+            }
+            if (thread == 0) {
+                if (a.logp) a.logp[row] = !given ? 0.0f : none ? -kInf : a.scale * (at_target - M) - L;
+                if (a.stats) {
+                    a.stats[2 * row] = M;
+                    a.stats[2 * row + 1] = L;
+                }
+                if (kEntropy) a.entropy[row] = entropy;
+            }
+            if constexpr (kTop > 0) {
+                const float bound = bound_of<kThreads>(top.mine, a.top);
+                if (thread == 0) {
+                    top.threshold = bound;
+                    top.M = M, top.L = L;
+                    top.plain = sum == sum;
+                }
+            }
         }
-        if constexpr (kTop > 0)
-            top_of<Z, kThreads, kTop, R>(a, row, r.m, sum == sum, M, L, x, head, turns, rounds, top);
+        if constexpr (kTop > 0) {
+            __syncthreads();
+            top_of<Z, kThreads, kTop, R>(a, row, r.m, x, head, turns, rounds, top);
+        }
         __syncthreads();
     }
 }
@@ -410,9 +448,8 @@ struct LogprobGrad {
 
 constexpr int kGradThreads = 256;
 
-
-// A piece is kGradGroups groups of each of kLanes threads; short rows (kLanes = 64) are a
-// piece each, without a head of their own.
+// A piece is kGradGroups groups of each of kLanes threads; short rows (kLanes =
+// 64) are a piece each, without a head of their own.
 template <class Z, class D, bool kEntropy, int kLanes, int kGradGroups>
 __global__ __launch_bounds__(kGradThreads) void k_logprob_grad(const LogprobGrad a) {
     constexpr float kLog2e = 1.44269504088896340736f;

@@ -363,7 +363,7 @@ __device__ __forceinline__ void norm_columns(const NormBackward &a, const NormSu
     if (c < a.C) {
         const typename X::type *h = static_cast<const typename X::type *>(a.h) + c;
         const typename Y::type *dy = static_cast<const typename Y::type *>(a.dy) + c;
-#pragma unroll 8
+#pragma unroll 16
         for (int t = threadIdx.x / kColumns; t < a.T; t += kShares) {
             const float d = Y::up(dy[t * a.ldy]), x = X::up(h[t * a.ldh]);
             dgain = __builtin_fmaf(d, (x - (a.layer ? a.mean[t] : 0.0f)) * a.rstd[t], dgain);
@@ -527,9 +527,9 @@ size_t backward_bytes(int64_t T, int64_t C, bool with_bias) {
 }
 
 // Where the sums over the rows are taken by columns in the same launch, which
-// reads two arrays again but saves a launch: 256 x 4096 5.2 us (with partial
-// sums 8.3), 512 x 1375 6.8 (9.5), 1024 x 300 6.6 (8.9), 512 x 4096 8.3 (8.7);
-// but 1024 x 4096 14.1 (10.6), 2048 x 4096 24.8 (15.5).
+// reads two arrays again but saves a launch: bf16, 256 x 4096 5.7 us (with
+// partial sums 8.3), 512 x 1375 4.8 (9.5), 1024 x 300 5.9 (8.9), 512 x 4096 7.2
+// (8.7); but 1024 x 4096 14.1 (10.6), 2048 x 4096 24.8 (15.5).
 bool few_rows(int64_t T, int64_t C) { return T <= 1024 && T * C <= (1 << 21); }
 
 }  // namespace
