@@ -18,11 +18,11 @@ namespace {
 
 using namespace sft;
 
-// Threads of a workgroup, and items that it takes unless one token has more: an
-// item is two groups of elements of a head, whose loads are under way while the
-// sines are computed.  One item a thread keeps enough workgroups on a CU
-// (4096 tokens of 32 + 32 heads of 128 in bf16 23.4 us, two items 26.0; 512
-// threads 24.4).
+// Threads of a workgroup.  An item is two groups of elements of a head, whose
+// loads are under way while the sines are computed; a workgroup takes an item a
+// thread, of several tokens or of a part of one token's heads.  More items a
+// thread leave too few workgroups on a CU (4096 tokens of 32 + 32 heads of 128
+// in bf16, at the time: 23.4 us, two items 26.0; 512 threads 24.4).
 constexpr int kThreads = 256;
 constexpr int kMaxMats = 8;
 constexpr int kMaxHead = 4096;
@@ -44,8 +44,8 @@ struct RotaryMat {
     const void *x;
     void *y;
     int64_t x_batch, x_row, x_head, y_batch, y_row, y_head;
-    Div units, heads;           // items of a head; heads
-    int32_t tokens;             // of a workgroup
+    Div units, heads, parts;    // items of a head; heads; parts of a token's heads
+    int32_t tokens, items;      // of a workgroup
     uint32_t begin;             // the first of its workgroups
 };
 
@@ -149,35 +149,31 @@ __global__ __launch_bounds__(kThreads) void k_rotary(const Rotary a) {
         int k = 0;
         while (k + 1 < a.n_mats && a.m[k + 1].begin <= block) ++k;
         const RotaryMat &m = a.m[k];
-        const uint32_t first = (block - m.begin) * uint32_t(m.tokens);
+        const uint32_t at = over(block - m.begin, m.parts), first = at * uint32_t(m.tokens);
         const uint32_t tokens = min(uint32_t(m.tokens), uint32_t(a.total) - first);
-        const uint32_t items = tokens * m.heads.by * m.units.by;
+        const uint32_t i = (block - m.begin - at * m.parts.by) * uint32_t(m.items) + threadIdx.x;
+        const bool live = threadIdx.x < uint32_t(m.items) && i < tokens * m.heads.by * m.units.by;
         const type *x = static_cast<const type *>(m.x);
         Item it;
         Raw<E, N> r0, r1;
-        const auto fetch = [&](uint32_t i) {
+        if (live) {
             it = item_of<N, kHalf>(a, m, i, first);
             r0 = get_group<E, N>(x + it.x + it.at0, it.n0);
             r1 = get_group<E, N>(x + it.x + it.at1, it.n1);
-        };
-        if (threadIdx.x < items) fetch(threadIdx.x);
+        }
         // in turns, of which whole ones do not matter: what is left is exact to fp32 however far the position
-        for (uint32_t i = threadIdx.x; i < tokens * uint32_t(half); i += kThreads) {
-            const uint32_t t = over(i, a.pairs), token = first + t, b = over(token, a.rows);
+        for (uint32_t k = threadIdx.x; k < tokens * uint32_t(half); k += kThreads) {
+            const uint32_t t = over(k, a.pairs), token = first + t, b = over(token, a.rows);
             const int32_t pos = a.pos[b * a.pos_batch + (token - b * a.rows.by)];
-            double turns = a.freq[i - t * half] * 0.15915494309189533577 * pos;
+            double turns = a.freq[k - t * half] * 0.15915494309189533577 * pos;
             turns -= __builtin_rint(turns);
             float s, c;
             sincospif(static_cast<float>(2.0 * turns), &s, &c);
-            sines[2 * i] = c * a.amplitude;
-            sines[2 * i + 1] = (a.inverse ? -s : s) * a.amplitude;
+            sines[2 * k] = c * a.amplitude;
+            sines[2 * k + 1] = (a.inverse ? -s : s) * a.amplitude;
         }
         __syncthreads();
-        for (uint32_t i = threadIdx.x; i < items;) {
-            turn_item<E, kHalf>(it, r0, r1, sines, static_cast<type *>(m.y));
-            i += kThreads;
-            if (i < items) fetch(i);
-        }
+        if (live) turn_item<E, kHalf>(it, r0, r1, sines, static_cast<type *>(m.y));
         __syncthreads();
     }
 }
@@ -291,9 +287,13 @@ int sft_rotary(const sft_rotary_args *v, void *stream) {
         // as many tokens as give every thread an item, and at most two sines
         const int64_t tokens = std::max<int64_t>(
             1, std::min({total, kThreads / (units * m.heads), 2 * kThreads / half}));
+        // a single token's heads in even parts
+        const int64_t parts = (tokens * units * m.heads + kThreads - 1) / kThreads;
+        r.parts = div_by(static_cast<uint32_t>(parts));
         r.tokens = static_cast<int32_t>(tokens);
+        r.items = static_cast<int32_t>((tokens * units * m.heads + parts - 1) / parts);
         r.begin = static_cast<uint32_t>(blocks);
-        blocks += (total + tokens - 1) / tokens;
+        blocks += (total + tokens - 1) / tokens * parts;
         sines = std::max(sines, tokens * half);
     }
     SFT_CHECK(blocks < (int64_t(1) << 31), SFT_ENOTSUP, "%s: too many tokens and arrays", who);
