@@ -103,14 +103,14 @@ __device__ __forceinline__ Item item_of(const Rotary &a, const RotaryMat &m, uin
     return it;
 }
 
-template <class E, bool kHalf>
+template <class E, bool kHalf, bool kPast>
 __device__ __forceinline__ void turn_item(const Item &it, const Raw<E, E::kGroup> &r0, const Raw<E, E::kGroup> &r1,
                                           const float *sines, typename E::type *y) {
     constexpr int N = E::kGroup;
     y += it.y;
     if (it.sine0 < 0) {
-        put_group<E, N, true>(y + it.at0, r0, it.n0);
-        put_group<E, N, true>(y + it.at1, r1, it.n1);
+        put_group<E, N, kPast>(y + it.at0, r0, it.n0);
+        put_group<E, N, kPast>(y + it.at1, r1, it.n1);
         return;
     }
     float u[N], v[N];
@@ -134,11 +134,11 @@ __device__ __forceinline__ void turn_item(const Item &it, const Raw<E, E::kGroup
             v[i + 1] = __builtin_fmaf(f, s1[i + 1], g * s1[i]);
         }
     }
-    put_group<E, N, true>(y + it.at0, close<E, N>(u), it.n0);
-    put_group<E, N, true>(y + it.at1, close<E, N>(v), it.n1);
+    put_group<E, N, kPast>(y + it.at0, close<E, N>(u), it.n0);
+    put_group<E, N, kPast>(y + it.at1, close<E, N>(v), it.n1);
 }
 
-template <class E, bool kHalf>
+template <class E, bool kHalf, bool kPast>
 __global__ __launch_bounds__(kThreads) void k_rotary(const Rotary a) {
     extern __shared__ f32x4 room[];       // cosine and sine of each token's pairs, and 8 pairs more for a last short group
     constexpr int N = E::kGroup;
@@ -173,7 +173,7 @@ __global__ __launch_bounds__(kThreads) void k_rotary(const Rotary a) {
             sines[2 * k + 1] = (a.inverse ? -s : s) * a.amplitude;
         }
         __syncthreads();
-        if (live) turn_item<E, kHalf>(it, r0, r1, sines, static_cast<type *>(m.y));
+        if (live) turn_item<E, kHalf, kPast>(it, r0, r1, sines, static_cast<type *>(m.y));
         __syncthreads();
     }
 }
@@ -308,14 +308,23 @@ int sft_rotary(const sft_rotary_args *v, void *stream) {
     const dim3 grid(static_cast<uint32_t>(std::min<int64_t>(blocks, 1 << 23))), block(kThreads);
     const size_t lds = static_cast<size_t>(sines + 8) * 8;
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    const bool in_half = layout == SFT_ROTARY_HALF;
+    // Results go past L2 where a wave's stores are whole pieces of 64 bytes or long ones; short pieces, and heads that
+    // start between, are put together in L2 (134 MB in bf16: heads of 128, 64, 32 21.6, 26.8, 37.1 us past it, 26.0,
+    // 26.6, 27.8 through it; 48 of 128 turned in pairs 47.6 and 30.1)
+    const bool past = D * size % 16 == 0 && (pair_units % 4 == 0 || pair_units >= 12);
+#define SFT_SEND(E, half)                                                                        \
+    do {                                                                                         \
+        if (past) hipLaunchKernelGGL((k_rotary<E, half, true>), grid, block, lds, st, a);        \
+        else hipLaunchKernelGGL((k_rotary<E, half, false>), grid, block, lds, st, a);            \
+    } while (0)
     if (type == SFT_BF16) {
-        if (in_half) hipLaunchKernelGGL((k_rotary<Bf16, true>), grid, block, lds, st, a);
-        else hipLaunchKernelGGL((k_rotary<Bf16, false>), grid, block, lds, st, a);
+        if (layout == SFT_ROTARY_HALF) SFT_SEND(Bf16, true);
+        else SFT_SEND(Bf16, false);
     } else {
-        if (in_half) hipLaunchKernelGGL((k_rotary<Fp32, true>), grid, block, lds, st, a);
-        else hipLaunchKernelGGL((k_rotary<Fp32, false>), grid, block, lds, st, a);
+        if (layout == SFT_ROTARY_HALF) SFT_SEND(Fp32, true);
+        else SFT_SEND(Fp32, false);
     }
+#undef SFT_SEND
     const hipError_t e = hipGetLastError();
     SFT_CHECK(e == hipSuccess, SFT_EHIP, "%s: launch failed: %s", who, hipGetErrorString(e));
     return SFT_OK;
