@@ -137,7 +137,7 @@ template <int kThreads, int kTop>
 struct TopPlace {
     static constexpr int kFound = kThreads == 64 ? 512 : 1024;
     static constexpr int kItems = kTop == 1 || kThreads == 64 ? kSlots : 1024;
-    f32x4 held[kTop == 1 ? kSlots * kRound / 4 : 1];
+    f32x4 held[kTop == 1 && kThreads > 64 ? kSlots * kRound / 4 : 1];
     uint64_t found[kFound];
     float mine[kThreads], block[kTop == 2 ? kBlocks<kThreads> : 1][kTop == 2 ? kThreads : 1];
     int32_t item[kItems];
@@ -176,7 +176,9 @@ __device__ __forceinline__ float bound_of(const float *mine, int K) {
 // threads whose own largest logit reaches it have alternatives.  Their logits
 // that reach the bound are collected, by the whole workgroup, and ranked by
 // counting; those of rows of one round (kTop = 1) are still at hand, else the
-// blocks that reach the bound are read again.  Where too much reaches it, or a
+// blocks that reach the bound are read again.  A wave counts what it holds of a
+// row without atomics (50000 x 300 in bf16, 5 alternatives: 58 us, by the blocks
+// 72; rows of 512 to 2048 lose by it, 30000 x 2000 62 us for 48).  Where too much reaches it, or a
 // NaN may have hidden a thread's largest, the alternatives are looked for one
 // by one, the row read again for each.
 template <class Z, int kThreads, int kTop, int R>
@@ -184,6 +186,7 @@ __device__ __forceinline__ void top_of(const Logprob &a, int64_t row, float mine
                                        int turns, int rounds, TopPlace<kThreads, kTop> &s) {
     constexpr int N = Z::kGroup, kSteps = R / N, kFound = TopPlace<kThreads, kTop>::kFound;
     constexpr int kItems = TopPlace<kThreads, kTop>::kItems;
+    constexpr bool kWave = kThreads == 64 && kTop == 1;
     const int thread = static_cast<int>(threadIdx.x);
     const float M = s.M, L = s.L;
     const typename Z::type *z = static_cast<const typename Z::type *>(a.z) + row * a.ld;
@@ -206,7 +209,19 @@ __device__ __forceinline__ void top_of(const Logprob &a, int64_t row, float mine
             const int k = atomicAdd(&s.n, 1);
             if (k < kFound) s.found[k] = key_of(x, at);
         };
-        if (reaches(mine)) {
+        if constexpr (kWave) {
+            static_assert(64 * R <= kFound);
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const uint64_t which = __ballot(reaches(last[i]));      // (-infinity behind the row's end)
+                if (which == 0) continue;
+                const int k = n + __builtin_popcountll(which & ((uint64_t(1) << thread) - 1));
+                if (reaches(last[i])) s.found[k] = key_of(last[i], place_of<Z, 64>(0, i / N, thread) + i % N);
+                n += __builtin_popcountll(which);
+            }
+            if (thread == 0) s.n = n;
+        } else if (reaches(mine)) {
             if (thread < head) {
                 const float x = logit<Z>(z, thread);
                 if (reaches(x)) collect(x, thread);
@@ -229,8 +244,8 @@ __device__ __forceinline__ void top_of(const Logprob &a, int64_t row, float mine
             }
         }
         __syncthreads();
-        const int items = s.items;
-        if (items <= kItems) {
+        const int items = kWave ? 0 : s.items;
+        if (!kWave && items <= kItems) {
             if constexpr (kTop == 1) {
                 for (int p = thread; p < items * R; p += kThreads) {
                     const int k = p / R, i = p % R;
@@ -542,18 +557,21 @@ void send(const Logprob &a, int64_t most, hipStream_t st) {
 }
 
 // Short rows go to a wave each, as many at a time as the device holds: starting
-// a workgroup takes longer than reading one of them.  Few long rows go to 1024
-// threads.
+// a workgroup takes longer than reading one of them.  Long rows go to 1024
+// threads where there is at most one for each CU (250 x 50001 in bf16, with 20
+// alternatives: 12.1 us, by 256 threads 14.8), else to 256 (272 of them: 16.1,
+// by 1024 threads 21.6); from 16384 logits on (16 x 20000, 5 alternatives in
+// fp32: 6.8, by 256 threads 7.7; 16 x 5000: 7.3 and 6.4).
 template <class Z>
 void send(const Logprob &a, hipStream_t st) {
     const int64_t waves = 32 * int64_t(num_cus());
     if (a.V <= 64 * 8) {
-        if (a.top) send<Z, 64, 8, 2>(a, waves, st);
+        if (a.top) send<Z, 64, 8, 1>(a, waves, st);
         else send<Z, 64, 8, 0>(a, waves, st);
     } else if (a.V <= 64 * kRound) {
         if (a.top) send<Z, 64, kRound, 2>(a, waves, st);
         else send<Z, 64, kRound, 0>(a, waves, st);
-    } else if (a.N < 2 * num_cus() && a.V >= 16384) {
+    } else if (a.N <= num_cus() && a.V >= 16384) {
         if (!a.top) send<Z, 1024, kRound, 0>(a, kMaxGrid, st);
         else if (a.V <= 1024 * kRound) send<Z, 1024, kRound, 1>(a, kMaxGrid, st);
         else send<Z, 1024, kRound, 2>(a, kMaxGrid, st);
