@@ -30,7 +30,7 @@ def _refused(rc, code, word=b""):
 
 
 # 4 rows of 8 floats (128 bytes), every array 1024 bytes from the next
-NORM = dict(T=4, C=8, X=BASE, res=BASE + 1024, H=BASE + 2048, gain=BASE + 3072, bias=BASE + 4096, Y=BASE + 5120,
+NORM = dict(T=4, C=8, X=BASE, res=BASE + 1024, H=BASE + 2048, gain=BASE + 3 * 1024, bias=BASE + 4096, Y=BASE + 5120,
             mean=BASE + 6144, rstd=BASE + 7168, ldx=8, ldr=8, ldh=8, ldy=8, eps=1e-5, kind=0, x_type=0, w_type=0, y_type=0)
 
 
@@ -55,7 +55,7 @@ def test_norm_forward_refuses(what, code):
 @pytest.mark.parametrize("what", [
     dict(Y=BASE), dict(Y=BASE + 124), dict(Y=BASE + 1024), dict(Y=BASE + 2048), dict(Y=BASE + 3100),
     dict(Y=BASE + 4096 - 100), dict(mean=BASE + 5120), dict(rstd=BASE + 124), dict(mean=BASE + 7168),
-    dict(H=BASE + 4), dict(H=BASE, ldh=9), dict(H=BASE + 1024 + 32), dict(H=BASE + 3072), dict(H=BASE + 5120),
+    dict(H=BASE + 4), dict(H=BASE, ldh=9), dict(H=BASE + 1024 + 32), dict(H=BASE + 3 * 1024), dict(H=BASE + 5120),
     dict(H=BASE, ldx=16, ldh=12),                                         # the same address, another distance
     dict(Y=BASE + 28, ldx=16, ldy=16),                                    # side by side, but one element of each row
     dict(Y=BASE + 32, ldx=16, ldy=17),                                    # side by side at first only
@@ -71,7 +71,7 @@ def test_rows_side_by_side_are_apart():
     assert _norm(T=0, Y=BASE + 32, ldx=16, ldy=16) == _lib.SFT_OK
 
 
-GRAD = dict(T=4, C=8, H=BASE, gain=BASE + 1024, mean=BASE + 2048, rstd=BASE + 3072, dY=BASE + 4096, dH=BASE + 5120,
+GRAD = dict(T=4, C=8, H=BASE, gain=BASE + 1024, mean=BASE + 2048, rstd=BASE + 3 * 1024, dY=BASE + 4096, dH=BASE + 5120,
             dX=BASE + 6144, dgain=BASE + 7168, dbias=BASE + 8192, ldh=8, ldy=8, ldr=8, ldx=8, kind=0, x_type=0, w_type=0,
             y_type=0, g_type=0, accumulate=0)
 NEED = 4 * 8 * 4 * 2             # at most 4 partial sums of 8 gains and 8 biases
@@ -95,8 +95,8 @@ def test_norm_backward_refuses(what, code):
 
 @pytest.mark.parametrize("what", [
     dict(dX=BASE), dict(dX=BASE + 4096, ldx=9), dict(dX=BASE + 4100), dict(dX=BASE + 5120, ldx=12, ldr=16),
-    dict(dX=BASE + 1024), dict(dX=BASE + 3072 - 100), dict(dgain=BASE), dict(dgain=BASE + 8192), dict(dbias=BASE + 6144),
-    dict(dgain=BASE + 1024), dict(dbias=BASE + 3072), dict(ws=BASE), dict(ws=BASE + 6144), dict(ws=BASE + 7168),
+    dict(dX=BASE + 1024), dict(dX=BASE + 3 * 1024 - 100), dict(dgain=BASE), dict(dgain=BASE + 8192), dict(dbias=BASE + 6144),
+    dict(dgain=BASE + 1024), dict(dbias=BASE + 3 * 1024), dict(ws=BASE), dict(ws=BASE + 6144), dict(ws=BASE + 7168),
     dict(dX=BASE + 4096, x_type=0, y_type=1, ldx=8, ldy=16),              # dY's place, another type
 ])
 def test_norm_backward_refuses_arrays_that_overlap(what):
