@@ -14,7 +14,7 @@
 // logit), its gradient 82 us (5.8 TB/s, rows without one only written); 1003 x
 // 50001 in fp32 with 5 alternatives 36.5 us.  Few long rows are bound by their
 // CUs instead, about 70 ps a logit in bf16: 8 x 32000 takes 4.5 us, with 20
-// alternatives 7.3, of which about 1.4 are passing over the logits that reach
+// alternatives 7.0, of which about 1.2 are passing over the logits that reach
 // their bound.  Where the alternatives are looked for one by one, all logits
 // equal, 4096 x 32000 with 20 takes about 1 ms, not 54 us.
 #include <hip/hip_runtime.h>
@@ -31,7 +31,7 @@ namespace {
 
 using namespace sft;
 
-constexpr float kInf = __builtin_huge_valf();
+constexpr float kInf = __builtin_huge_valf(), kLargest = __FLT_MAX__;
 constexpr float kLn2 = 0.693147180559945309f;
 // Powers of two below this one are 0 in fp32; a bound for exponents that may
 // be minus infinity and get multiplied by 0.
@@ -185,13 +185,13 @@ __device__ __forceinline__ float bound_of(const float *mine, int K) {
         if (r3 >= want) bound = b3, reach = r3;
         bit >>= 2;
     } while ((bit >= least) & (reach - want > more));
-    return float_of(max(bound, order_of(-kInf)));
+    return float_of(bound);
 }
 
 // Logits of a row that reach the bound: those of rows of one round (kTop = 1)
 // from the registers that still hold them, of others the blocks of a thread's
 // turns that have one.  A wave on its own counts without atomics (50000 x 300
-// in bf16, 5 alternatives: 57 us, with them 72; where the wave holds 2048 it
+// in bf16, 5 alternatives: 55 us, with them 72; where the wave holds 2048 it
 // loses, 30000 x 2000 62 us, by blocks 48).
 template <class Z, int kThreads, int kTop, int R>
 __device__ __forceinline__ void collect(const float (&last)[R], float first, float mine, int head, int turns, int rounds,
@@ -200,7 +200,6 @@ __device__ __forceinline__ void collect(const float (&last)[R], float first, flo
     constexpr int kItems = TopPlace<kThreads, kTop>::kItems;
     const int thread = static_cast<int>(threadIdx.x);
     const float threshold = s.threshold;
-    const auto reaches = [&](float x) { return x >= threshold && x > -kInf; };
     const auto keep = [&](float x, int at) {
         const int k = atomicAdd(&s.n, 1);
         if (k < kFound) s.found[k] = key_of(x, at);
@@ -210,15 +209,15 @@ __device__ __forceinline__ void collect(const float (&last)[R], float first, flo
         int n = 0;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const uint64_t which = __ballot(reaches(last[i]));      // (-infinity behind the row's end)
+            const uint64_t which = __ballot(last[i] >= threshold);      // (-infinity behind the row's end)
             if (which == 0) continue;
             const int k = n + __builtin_popcountll(which & ((uint64_t(1) << thread) - 1));
-            if (reaches(last[i])) s.found[k] = key_of(last[i], place_of<Z, 64>(0, i / N, thread) + i % N);
+            if (last[i] >= threshold) s.found[k] = key_of(last[i], place_of<Z, 64>(0, i / N, thread) + i % N);
             n += __builtin_popcountll(which);
         }
         if (thread == 0) s.n = n;
-    } else if (reaches(mine)) {
-        if (reaches(first)) keep(first, thread);
+    } else if (mine >= threshold) {
+        if (first >= threshold) keep(first, thread);
         if constexpr (kTop == 1) {
             if (turns == 0) return;
 #pragma unroll
@@ -226,18 +225,21 @@ __device__ __forceinline__ void collect(const float (&last)[R], float first, flo
                 float most = last[g];
 #pragma unroll
                 for (int i = 1; i < 8; ++i) most = __builtin_fmaxf(most, last[g + i]);
-                if (!reaches(most)) continue;
+                if (!(most >= threshold)) continue;
 #pragma unroll
                 for (int i = g; i < g + 8; ++i)
-                    if (reaches(last[i])) keep(last[i], place_of<Z, kThreads>(head, i / N, thread) + i % N);
+                    if (last[i] >= threshold) keep(last[i], place_of<Z, kThreads>(head, i / N, thread) + i % N);
             }
         } else {
+            uint32_t hits = 0;
             const int blocks = (turns + kSteps * rounds - 1) / (kSteps * rounds);
-            for (int b = 0; b < blocks; ++b)
-                if (reaches(s.block[b][thread])) {
-                    const int k = atomicAdd(&s.items, 1);
-                    if (k < kItems) s.item[k] = b * kThreads + thread;
-                }
+#pragma unroll
+            for (int b = kBlocks<kThreads> - 1; b >= 0; --b)
+                hits += hits + (b < blocks && s.block[b][thread] >= threshold);
+            for (; hits; hits &= hits - 1) {
+                const int k = atomicAdd(&s.items, 1);
+                if (k < kItems) s.item[k] = __builtin_ctz(hits) * kThreads + thread;
+            }
         }
     }
 }
@@ -282,7 +284,7 @@ __device__ __forceinline__ void top_of(const Logprob &a, int64_t row, int head, 
                     open<Z, N>(get_group<Z, N>(z + at, n), x);
 #pragma unroll
                     for (int i = 0; i < N; ++i)
-                        if (i < n && x[i] >= threshold && x[i] > -kInf) {
+                        if (i < n && x[i] >= threshold) {
                             const int k = atomicAdd(&s.n, 1);
                             if (k < kFound) s.found[k] = key_of(x[i], at + i);
                         }
@@ -422,7 +424,7 @@ __global__ __launch_bounds__(kThreads) void k_logprob(const Logprob a) {
         if constexpr (kTop > 0) {       // meanwhile one wave looks for the bound
             if (kThreads == 64 || thread >> 6 == 1) {
                 const float bound = bound_of<kThreads>(top.mine, a.top);
-                if ((thread & 63) == 0) top.threshold = bound;
+                if ((thread & 63) == 0) top.threshold = __builtin_fmaxf(bound, -kLargest);      // (not minus infinity)
             }
         }
         const float m2 = __builtin_fmaxf(M * a.c, -kFar);
