@@ -347,45 +347,55 @@ __device__ __forceinline__ void put_sum(const NormSums &s, int which, int c, flo
     }
 }
 
-constexpr int kColumns = 32, kShares = kRowThreads / kColumns;
+constexpr int kPartColumns = 32;    // whole cache lines of partial sums
 
-// The shares' sums of a column, added in order by one of its threads.
+// The sum of a column over its shares, in a fixed order, in the first of its threads.
+template <int kColumns>
 __device__ __forceinline__ float columns_sum(float sum, float *s) {
-    const int column = threadIdx.x % kColumns, share = threadIdx.x / kColumns;
-    s[share * kColumns + column] = sum;
+    constexpr int kWaves = kRowThreads / 64;
+    const int column = threadIdx.x % kColumns;
+#pragma unroll
+    for (int d = kColumns; d < 64; d *= 2) sum += __shfl_xor(sum, d);
+    if (threadIdx.x % 64 < kColumns) s[threadIdx.x / 64 * kColumns + column] = sum;
     __syncthreads();
     sum = 0.0f;
-    if (share == 0)
+    if (threadIdx.x < kColumns)
 #pragma unroll
-        for (int i = 0; i < kShares; ++i) sum += s[i * kColumns + column];
+        for (int i = 0; i < kWaves; ++i) sum += s[i * kColumns + column];
     __syncthreads();
     return sum;
 }
 
-// The sums over few rows, of 32 columns a workgroup: the statistics are there
-// already, so they need not wait for the rows' own sums, and one launch does
-// for both.
-template <class X, class Y>
+// The sums over few rows, of kColumns columns a workgroup: the statistics are
+// there already, so they need not wait for the rows' own sums, and one launch
+// does for both.
+template <class X, class Y, int kColumns>
 __device__ __forceinline__ void norm_columns(const NormBackward &a, const NormSums &s, uint32_t block) {
-    __shared__ float places[kRowThreads];
+    __shared__ float places[kRowThreads / 64 * kColumns];
     const int c = block * kColumns + threadIdx.x % kColumns;
     float dgain = 0.0f, dbias = 0.0f;
     if (c < a.C) {
         const typename X::type *h = static_cast<const typename X::type *>(a.h) + c;
         const typename Y::type *dy = static_cast<const typename Y::type *>(a.dy) + c;
 #pragma unroll 16
-        for (int t = threadIdx.x / kColumns; t < a.T; t += kShares) {
+        for (int t = threadIdx.x / kColumns; t < a.T; t += kRowThreads / kColumns) {
             const float d = Y::up(dy[t * a.ldy]), x = X::up(h[t * a.ldh]);
             dgain = __builtin_fmaf(d, (x - (a.layer ? a.mean[t] : 0.0f)) * a.rstd[t], dgain);
             dbias += d;
         }
     }
-    dgain = columns_sum(dgain, places);
-    dbias = columns_sum(dbias, places);
+    dgain = columns_sum<kColumns>(dgain, places);
+    dbias = columns_sum<kColumns>(dbias, places);
     if (threadIdx.x >= kColumns || c >= a.C) return;
     put_sum(s, 0, c, dgain);
     put_sum(s, 1, c, dbias);
 }
+
+// Columns a workgroup takes beside rows of up to `width` values: of narrow rows
+// fewer, as their columns make few workgroups (1024 x 128 in bf16: 8 columns 3.9
+// us, 32 6.2; 1024 x 700: 16 6.1, 32 6.6, and in fp32 7.2 and 9.6; 1024 x 2048: 16
+// 9.7, 32 9.0).
+constexpr int few_columns(int width) { return width <= 256 ? 8 : width <= 1024 ? 16 : 32; }
 
 template <class X, class Y, int kLanes, int kGroups, bool kEven, int kSums>
 __global__ __launch_bounds__(kRowThreads) void k_norm_backward(const NormBackward a) {
@@ -397,23 +407,23 @@ template <class X, class Y, int kLanes, int kGroups, bool kEven>
 __global__ __launch_bounds__(kRowThreads) void k_norm_backward_few(const NormBackward a, const NormSums s,
                                                                    uint32_t columns) {
     if (blockIdx.x < columns)
-        norm_columns<X, Y>(a, s, blockIdx.x);
+        norm_columns<X, Y, few_columns(kLanes * kGroups * X::kGroup)>(a, s, blockIdx.x);
     else
         norm_rows<X, Y, kLanes, kGroups, kEven, 0>(a, blockIdx.x - columns, gridDim.x - columns);
 }
 
-// The workgroups' sums in a fixed order: 32 columns a workgroup, 32 shares of them.
+// The workgroups' sums in a fixed order.
 __global__ __launch_bounds__(kRowThreads) void k_norm_reduce(const NormSums a) {
-    __shared__ float places[kRowThreads];
-    const int c = blockIdx.x * kColumns + threadIdx.x % kColumns;
+    __shared__ float places[kRowThreads / 64 * kPartColumns];
+    const int c = blockIdx.x * kPartColumns + threadIdx.x % kPartColumns;
     float sum = 0.0f;
     if (c < a.C && a.out[blockIdx.y]) {
         const float *p = a.part + int64_t(blockIdx.y) * a.groups * a.C + c;
 #pragma unroll 8
-        for (int g = threadIdx.x / kColumns; g < a.groups; g += kShares) sum += p[int64_t(g) * a.C];
+        for (int g = threadIdx.x / kPartColumns; g < a.groups; g += kRowThreads / kPartColumns) sum += p[int64_t(g) * a.C];
     }
-    sum = columns_sum(sum, places);
-    if (threadIdx.x < kColumns && c < a.C) put_sum(a, blockIdx.y, c, sum);
+    sum = columns_sum<kPartColumns>(sum, places);
+    if (threadIdx.x < kPartColumns && c < a.C) put_sum(a, blockIdx.y, c, sum);
 }
 
 // ------------------------------------------------------------------ host
@@ -511,11 +521,12 @@ int backward_groups(int64_t T, int64_t C) {
 template <class X, class Y, bool kEven>
 void send_backward(const NormBackward &a, const NormSums *few, int sums, hipStream_t st) {
     const uint32_t rows = static_cast<uint32_t>(backward_groups(a.T, a.C));
-    const uint32_t columns = static_cast<uint32_t>((a.C + kColumns - 1) / kColumns);
-    const dim3 grid(few ? rows + columns : rows), block(kRowThreads);
+    const dim3 block(kRowThreads);
 #define SFT_GO(lanes, eights)                                                                                           \
     if (a.C <= lanes * eights * 8) {                                                                                    \
-        constexpr int kGroups = eights * 8 / X::kGroup;                                                                 \
+        constexpr int kGroups = eights * 8 / X::kGroup, kColumns = few_columns(lanes * eights * 8);                     \
+        const uint32_t columns = few ? static_cast<uint32_t>((a.C + kColumns - 1) / kColumns) : 0;                      \
+        const dim3 grid(rows + columns);                                                                                \
         if (few) hipLaunchKernelGGL((k_norm_backward_few<X, Y, lanes, kGroups, kEven>), grid, block, 0, st, a, *few, columns); \
         else if (sums == 0) hipLaunchKernelGGL((k_norm_backward<X, Y, lanes, kGroups, kEven, 0>), grid, block, 0, st, a); \
         else if (sums == 1) hipLaunchKernelGGL((k_norm_backward<X, Y, lanes, kGroups, kEven, 1>), grid, block, 0, st, a); \
@@ -538,9 +549,10 @@ size_t backward_bytes(int64_t T, int64_t C, bool with_bias) {
 
 // Where the sums over the rows are taken by columns in the same launch, which
 // reads two arrays again but saves a launch: bf16, 256 x 4096 5.7 us (with
-// partial sums 8.3), 512 x 1375 4.8 (9.5), 1024 x 300 5.9 (8.9), 512 x 4096 7.2
-// (8.7); but 1024 x 4096 14.1 (10.6), 2048 x 4096 24.8 (15.5).
-bool few_rows(int64_t T, int64_t C) { return T <= 1024 && T * C <= (1 << 21); }
+// partial sums 8.3), 512 x 1375 4.8 (9.5), 1024 x 300 4.6 (8.9), 512 x 4096 7.2
+// (8.7), 2048 x 128 5.1 (8.1), 4096 x 33 6.3 (8.6); but 1024 x 4096 14.1 (10.6),
+// 2048 x 256 9.7 (7.9), 4096 x 95 13.1 (9.5), 8192 x 8 9.5 (8.1).
+bool few_rows(int64_t T, int64_t C) { return (T <= 1024 && T * C <= (1 << 21)) || (T <= 4096 && T * C <= (1 << 18)); }
 
 }  // namespace
 
@@ -672,7 +684,7 @@ int sft_norm_backward(const sft_norm_grad_args *v, void *ws, size_t ws_bytes, vo
         SFT_CHECK(e == hipSuccess, SFT_EHIP, "%s: launch failed: %s", who, hipGetErrorString(e));
     }
     if (sums && !few) {
-        const dim3 grid(static_cast<uint32_t>((v->C + kColumns - 1) / kColumns), v->dbias ? 2 : 1);
+        const dim3 grid(static_cast<uint32_t>((v->C + kPartColumns - 1) / kPartColumns), v->dbias ? 2 : 1);
         hipLaunchKernelGGL(k_norm_reduce, grid, dim3(kRowThreads), 0, st, s);
         const hipError_t e = hipGetLastError();
         SFT_CHECK(e == hipSuccess, SFT_EHIP, "%s: launch failed: %s", who, hipGetErrorString(e));

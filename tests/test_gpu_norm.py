@@ -159,7 +159,8 @@ def backward64(h, gain, mean, rstd, dy, dh, kind, rows_depth):
 
 def depth(T):
     """Additions behind one another in the sums over T <= 2048 rows: a team's rows, 32 teams, 64 workgroups a share, 8
-    shares, the accumulation; never more than T - 1 and the last."""
+    shares, the accumulation; never more than T - 1 and the last.  (Narrow rows, T <= 20000: at most 32 of a share, or 4
+    of a team of 64 and 8 workgroups a share, and 30 to join them.)"""
     return min(T, 4 + 32 + 64 + 8) + 1
 
 
@@ -208,6 +209,12 @@ def test_backward_of_every_width(gpu_lib, kind, x_type, y_type):
 def test_backward_of_many_rows(gpu_lib, T, C):
     for kind in ("layer", "rms"):
         run_backward(T, C, kind, BF16, BF16, seed=T)
+
+
+@pytest.mark.parametrize("T,C", [(1025, 7), (4096, 64), (4097, 64), (2048, 128), (2049, 128), (9000, 20), (20000, 96)])
+def test_backward_of_thousands_of_narrow_rows(gpu_lib, T, C):
+    run_backward(T, C, "layer", BF16, BF16, seed=T)
+    run_backward(T, C, "rms", F32, F32, seed=T, pad=1)
 
 
 @pytest.mark.parametrize("dgain,dbias", [(True, False), (False, True), (False, False)])
