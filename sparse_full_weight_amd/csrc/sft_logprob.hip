@@ -176,7 +176,7 @@ __device__ __forceinline__ float bound_of(const float *mine, int K) {
     const uint32_t top = (31u - static_cast<uint32_t>(__builtin_clz(differ))) | 1u, least = differ & (0u - differ);
     const auto reached = [&](uint32_t b) { return static_cast<uint32_t>(__builtin_popcountll(__ballot(o >= b))); };
     uint32_t bound = one & ~((2u << top) - 1u), bit = 1u << top, reach = 64;
-    const uint32_t want = K, more = want / 4;
+    const uint32_t want = K, most = min(want + want / 4, 63u);      // (64 reach the prefix alone)
     do {                                      // two bits at a time
         const uint32_t b1 = bound | bit >> 1, b2 = bound | bit, b3 = b1 | b2;
         const uint32_t r1 = reached(b1), r2 = reached(b2), r3 = reached(b3);
@@ -184,7 +184,7 @@ __device__ __forceinline__ float bound_of(const float *mine, int K) {
         if (r2 >= want) bound = b2, reach = r2;
         if (r3 >= want) bound = b3, reach = r3;
         bit >>= 2;
-    } while ((bit >= least) & (reach - want > more));
+    } while ((bit >= least) & (reach > most));
     return float_of(bound);
 }
 
