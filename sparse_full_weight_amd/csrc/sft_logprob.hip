@@ -158,26 +158,27 @@ struct Or {
     static __device__ __forceinline__ float of(float a, float b) { return bits_float(float_bits(a) | float_bits(b)); }
 };
 
-// A bound that at least K and hardly more of the threads' largest logits reach
-// (K <= 64), by one wave: about the K-th largest of 64, each of them the largest
-// of every 64th thread, found by halving from the first bit on in which they
-// differ to the last (in bf16 the lower half never does), two bits at a time.
-// With the statistics computed meanwhile, 64 x 50001 in bf16 with 20
-// alternatives takes 10.6 us, one after the other and to the last bit 11.7.
-template <int kThreads>
-__device__ __forceinline__ float bound_of(const float *mine, int K) {
-    const int lane = static_cast<int>(threadIdx.x) & 63;
-    float x = mine[lane];
+// A bound that at least `want` and hardly more of a wave's values reach, found by
+// halving from the first bit on in which they differ to the last (in bf16 the
+// lower half never does), two bits at a time.
+template <int kParts>
+__device__ __forceinline__ float bound_among(const uint32_t (&o)[kParts], uint32_t want) {
+    const uint32_t one = __builtin_amdgcn_readfirstlane(o[0]);
+    uint32_t differ = 0;
 #pragma unroll
-    for (int i = 1; i < kThreads / 64; ++i) x = __builtin_fmaxf(x, mine[lane + 64 * i]);
-    const uint32_t o = order_of(x), one = __builtin_amdgcn_readfirstlane(o);
-    const uint32_t differ = __builtin_amdgcn_readfirstlane(float_bits(lanes_of<Or, 64>(bits_float(o ^ one))));
+    for (int i = 0; i < kParts; ++i) differ |= o[i] ^ one;
+    differ = __builtin_amdgcn_readfirstlane(float_bits(lanes_of<Or, 64>(bits_float(differ))));
     if (differ == 0) return float_of(one);      // (no first bit: the loop's end needs one)
     const uint32_t top = (31u - static_cast<uint32_t>(__builtin_clz(differ))) | 1u, least = differ & (0u - differ);
-    const auto reached = [&](uint32_t b) { return static_cast<uint32_t>(__builtin_popcountll(__ballot(o >= b))); };
-    uint32_t bound = one & ~((2u << top) - 1u), bit = 1u << top, reach = 64;
-    const uint32_t want = K, most = min(want + want / 4, 63u);      // (64 reach the prefix alone)
-    do {                                      // two bits at a time
+    const auto reached = [&](uint32_t b) {
+        uint32_t n = 0;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) n += static_cast<uint32_t>(__builtin_popcountll(__ballot(o[i] >= b)));
+        return n;
+    };
+    uint32_t bound = one & ~((2u << top) - 1u), bit = 1u << top, reach = 64 * kParts;
+    const uint32_t most = min(want + want / 4, reach - 1u);         // (all of them reach the prefix alone)
+    do {
         const uint32_t b1 = bound | bit >> 1, b2 = bound | bit, b3 = b1 | b2;
         const uint32_t r1 = reached(b1), r2 = reached(b2), r3 = reached(b3);
         if (r1 >= want) bound = b1, reach = r1;
@@ -186,6 +187,29 @@ __device__ __forceinline__ float bound_of(const float *mine, int K) {
         bit >>= 2;
     } while ((bit >= least) & (reach > most));
     return float_of(bound);
+}
+
+// A bound that at least K of a row's logits reach (K <= 64), by one wave: about
+// the K-th largest of 64, each of them the largest of every 64th thread.  With the
+// statistics computed meanwhile, 64 x 50001 in bf16 with 20 alternatives takes
+// 10.6 us, one after the other and to the last bit 11.7.  For many alternatives
+// it is one of 128, or much more than they would reach it (4096 x 32000 in bf16
+// with 64: 73 us, of 64 137; with 33: 56.5 and 58.7).
+template <int kThreads>
+__device__ __forceinline__ float bound_of(const float *mine, int K) {
+    constexpr int kEach = kThreads / 64;
+    const int lane = static_cast<int>(threadIdx.x) & 63;
+    float x = mine[lane], y = -kInf;
+    if constexpr (kEach > 1) {
+        y = mine[lane + 64];
+#pragma unroll
+        for (int i = 2; i < kEach; i += 2) {
+            x = __builtin_fmaxf(x, mine[lane + 64 * i]);
+            y = __builtin_fmaxf(y, mine[lane + 64 * i + 64]);
+        }
+        if (K > 32) return bound_among<2>({order_of(x), order_of(y)}, K);
+    }
+    return bound_among<1>({order_of(__builtin_fmaxf(x, y))}, K);
 }
 
 // Logits of a row that reach the bound: those of rows of one round (kTop = 1)
