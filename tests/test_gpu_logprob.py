@@ -110,6 +110,16 @@ def test_many_rows_of_long_vocabularies(gpu_lib, dtype):
     check(z, torch.randint(0, 20011, (530,), generator=gen(3)), 1.0, 7)
 
 
+@pytest.mark.parametrize("K", [32, 33, 51, 64])
+@pytest.mark.parametrize("N,V", [(270, 9001), (3, 20000), (3, 40000)])
+def test_many_alternatives(gpu_lib, N, V, K):
+    # bf16: many logits are equal, the K-th among them
+    z = logits(N, V, K, BF16)
+    z[1] = 0.0
+    z[1, 17::V // 40] = 1.0            # (40 or 41 of one value above all the others of another)
+    check(z, torch.randint(0, V, (N,), generator=gen(K)), 1.0, K)
+
+
 def test_rows_of_several_rounds_a_block(gpu_lib):
     # 256 threads a row, nine rounds of 32 logits a thread in eight blocks
     N, V, K = 520, 70001, 11
