@@ -36,9 +36,12 @@ constexpr float kLn2 = 0.693147180559945309f;
 // Powers of two below this one are 0 in fp32; a bound for exponents that may
 // be minus infinity and get multiplied by 0.
 constexpr float kNothing = -1000.0f;
-// Where the largest logit times c (scale in units of log2) is beyond this, the
-// product with c is no longer safe from overflow and differences come first.
-constexpr float kFar = 1e38f;
+// Products with c (scale in units of log2) up to this size are off by a quarter
+// at most, which the differences from them carry and L takes off again.  Beyond,
+// the rounding itself grows past what a power of two can hold: a thread whose
+// logits are all below -kFar / c keeps -kFar, relative to which they are nothing,
+// and a row whose largest is as far is summed again, differences first.
+constexpr float kFar = 8388608.0f;
 constexpr int kMaxTop = 64;
 
 __device__ __forceinline__ float max3(float a, float b, float c) {

@@ -376,3 +376,53 @@ def test_the_same_results_every_time(gpu_lib):
         _lib.sft_logprob(z, target, out[0], stats=out[1], entropy=out[2], top_logp=out[3], top_index=out[4])
         first = first or out
         assert all(torch.equal(a, b) for a, b in zip(first, out))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [300, 700, 5000, 20000, 40000])
+def test_masks_of_large_finite_values(gpu_lib, V, dtype):
+    # a padded vocabulary's end, all but three tokens, half of them at random, and a whole row masked by a finite value
+    target = torch.tensor([5, V // 2, V // 3, 7])
+    for i, mask in enumerate([-1e5, -3e7, -2e9, -1e10, -3e10, -7e12, -1e18, -1e21, -5e24, -1e30, -3e30, -7e33, -1e37]):
+        z = logits(4, V, V + i)
+        z[0, V - V // 3:] = mask
+        z[1] = mask
+        z[1, V // 2], z[1, 0], z[1, V - 1] = 0.5, -2.0, 3.25
+        z[2, (torch.rand(V, generator=gen(i)) < 0.5) & (torch.arange(V) != V // 3)] = mask
+        z[3] = mask
+        z = z.to(dtype)
+        check(z, target, [1.0, 0.7, 1.9][i % 3], 3)
+        got = call(z, target, [1.0, 0.7, 1.9][i % 3])
+        # the row of one value: V terms of 1, their sum as in exact(), the logarithm, a difference of 0
+        L, H, logp = (float(x) for x in (got["stats"][3, 1], got["entropy"][3], got["logp"][3]))
+        e = (V / (64 if V <= 2048 else 256) * 1.125 + 46 + 4 * math.log(V)) * U
+        assert abs(L - math.log(V)) <= e and abs(H - math.log(V)) <= e and abs(logp + math.log(V)) <= e
+        # and what is masked gets no gradient, what is given its own
+        dz = torch.full(z.shape, MARK, device="cuda")
+        _lib.sft_logprob_grad(z.float().cuda(), target.int().cuda(), got["stats"], torch.ones(4, device="cuda"), dz)
+        dz = dz.cpu()
+        assert (dz[:3][z[:3].float() < -5e4] == 0.0).all()
+        own = (z[torch.arange(4), target].double() - z.amax(1).double() - got["stats"][:, 1].double().cpu()).exp()
+        assert ((dz[torch.arange(4), target].double() - (1.0 - own)).abs() <= 80 * U).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_logits_far_from_zero(gpu_lib, dtype):
+    # all of a row around a large value: as exact as differences of such logits are, with products with the scale near
+    # and far past what fp32 holds to a unit
+    for V in (300, 5000, 20000):
+        for i, far in enumerate([3e6, 1e8, -4e9, 2e12, -1e17, 6e25, -1e36]):
+            z = normal((3, V), abs(far) * 2.0 ** -20, V + i) + far
+            z = z.to(dtype)
+            d = z.double() - z.double().amax(1, keepdim=True)
+            for bits in (18, 25, 40):
+                scale = float(torch.tensor(2.0 ** bits / abs(far), dtype=F32))
+                got = call(z, torch.tensor([0, 1, V - 1]), scale)
+                lp = d * scale
+                p, L = lp.exp(), lp.exp().sum(1).log()
+                pd = (torch.where(p > 0, p * lp, 0.0).sum(1) / p.sum(1)).abs()
+                logp = lp[torch.arange(3), torch.tensor([0, 1, V - 1])] - L
+                # additions as in exact(), three roundings of an exponent, the logarithm and what is taken off it
+                e = (V / (64 if V <= 2048 else 256) * 1.125 + 46 + 3 * pd + 4 * L) * U
+                assert ((got["stats"][:, 1].double().cpu() - L).abs() <= e).all(), (far, bits)
+                assert ((got["logp"].double().cpu() - logp).abs() <= e + 4 * U * logp.abs()).all(), (far, bits)
