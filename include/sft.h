@@ -1129,8 +1129,9 @@ int sft_rotary(const sft_rotary_args *args, void *stream);
  * index -1 and logp -infinity.  A row of nothing else has M = L = logp =
  * -infinity and entropy 0.  A row with +infinity or NaN has NaN for L, logp
  * and entropy, and its alternatives, NaN never among them, have logp NaN.
- * Sums are in fp32; results are deterministic, and a row's do not depend on
- * the other rows.  Pointers are aligned to their types.  No workspace.
+ * Sums are in fp32, in an order that goes by V and the type alone: a row's
+ * results do not depend on the other rows, nor on how many there are, nor on
+ * where the row lies.  Pointers are aligned to their types.  No workspace.
  * Limits: 1 <= V < 2^30, N < 2^31, distances and spans as in sft_norm_forward.
  * What is written must not overlap anything else.
  * Errors: SFT_EINVAL (null pointers, negative sizes, bad type, scale or top_k,

@@ -9,14 +9,14 @@
 // so far, m, and relative to it the sums of e^(scale (z - m)) and of that
 // times scale (z - m); the threads' parts are joined at the row's end.  The
 // gradient reads a row and its statistics and writes a row.  Both are bound by
-// HBM: 4096 x 32000 in bf16 takes 44.6 us (262 MB read, 5.9 TB/s; the vector
-// units are busy for 87% of it, as an entropy needs about ten operations a
+// HBM: 4096 x 32000 in bf16 takes 45.2 us (262 MB read, 5.8 TB/s; the vector
+// units are busy for most of it, as an entropy needs about ten operations a
 // logit), its gradient 82 us (5.8 TB/s, rows without one only written); 1003 x
-// 50001 in fp32 with 5 alternatives 36.5 us.  Few long rows are bound by their
+// 50001 in fp32 with 5 alternatives 37 us.  Few long rows are bound by their
 // CUs instead, about 70 ps a logit in bf16: 8 x 32000 takes 4.5 us, with 20
-// alternatives 7.0, of which about 1.2 are passing over the logits that reach
+// alternatives 6.9, of which about 1.2 are passing over the logits that reach
 // their bound.  Where the alternatives are looked for one by one, all logits
-// equal, 4096 x 32000 with 20 takes about 1 ms, not 54 us.
+// equal, 4096 x 32000 with 20 takes about 1 ms, not 55 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -75,23 +75,23 @@ struct Logprob {
     float scale, c;                // c = scale * log2(e)
 };
 
-// A row's running state in one thread, relative to m2 = m * c.
+// A row's running state in one slot, relative to m2, the largest logit so far times c.
 struct Running {
-    float m, m2, sum, along;
+    float m2, sum, along;
 };
 
-// Takes up n logits; returns the largest of them.
+// Takes up n logits, after others where there are any (begun); returns the largest of them.
 template <bool kEntropy, int n>
-__device__ __forceinline__ float take_up(Running &r, const float (&z)[n], float c) {
+__device__ __forceinline__ float take_up(Running &r, const float (&z)[n], float c, bool begun) {
     float own = -kInf;
 #pragma unroll
     for (int i = 0; i < n; i += 2) own = max3(own, z[i], z[i + 1]);
-    const float m = __builtin_fmaxf(own, r.m);
-    const float m2 = __builtin_fmaxf(m * c, -kFar);       // (of minus infinity as well)
-    const float less = limit(r.m2 - m2, kNothing, 0.0f), part = exp2_of(less);
-    r.along = kEntropy ? part * __builtin_fmaf(r.sum, less, r.along) : 0.0f;
-    r.sum *= part;
-    r.m = m;
+    const float m2 = __builtin_fmaxf(own * c, r.m2);      // (-kFar at first)
+    if (begun) {
+        const float less = limit(r.m2 - m2, kNothing, 0.0f), part = exp2_of(less);
+        r.along = kEntropy ? part * __builtin_fmaf(r.sum, less, r.along) : 0.0f;
+        r.sum *= part;
+    }
     r.m2 = m2;
 #pragma unroll
     for (int i = 0; i < n; ++i) {
@@ -100,6 +100,48 @@ __device__ __forceinline__ float take_up(Running &r, const float (&z)[n], float 
         if (kEntropy) r.along = __builtin_fmaf(e, __builtin_fmaxf(d, kNothing), r.along);
     }
     return own;
+}
+
+// Where 256 threads that sum four quarters of a row keep them.
+template <int kThreads>
+struct Quarters {
+    static constexpr int kOf = kThreads == 256 ? 256 : 1;
+    float m2[4][kOf], sum[4][kOf], along[4][kOf];
+    __device__ __forceinline__ Running get(int q) const {
+        return Running{m2[q][threadIdx.x], sum[q][threadIdx.x], along[q][threadIdx.x]};
+    }
+    __device__ __forceinline__ void put(int q, const Running &r) {
+        m2[q][threadIdx.x] = r.m2, sum[q][threadIdx.x] = r.sum, along[q][threadIdx.x] = r.along;
+    }
+};
+
+// Halves K values over pairs of lanes: the sums of the first half stay where
+// `up` is false, those of the second in the others.
+template <int kControl, int K>
+__device__ __forceinline__ void halve(const float (&x)[K], bool up, float (&y)[(K + 1) / 2]) {
+    if constexpr (K == 1) {
+        y[0] = x[0] + dpp<kControl>(x[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < K / 2; ++i) y[i] = (up ? x[i + K / 2] : x[i]) + dpp<kControl>(up ? x[i] : x[i + K / 2]);
+    }
+}
+
+// Sums of K values (1, 2, 4 or 8) over a wave, the k-th in lanes of k * 16 / K on.
+// Lanes that would add the same share the values out between them, which makes
+// 8 sums cost little more than 2; the order of a sum is the same for any K.
+template <int K>
+__device__ __forceinline__ float sums_of(const float (&x)[K]) {
+    const int lane = static_cast<int>(threadIdx.x);
+    float a[(K + 1) / 2], b[(K + 3) / 4], c[1];
+    halve<0x128>(x, lane & 8, a);          // over lanes 8 apart, mirrored within 8, 2 apart, neighbours
+    halve<0x141>(a, lane & 4, b);
+    halve<0x4e>(b, lane & 2, c);
+    float s = c[0] + dpp<0xb1>(c[0]);
+    const u32x2 t = __builtin_amdgcn_permlane16_swap(float_bits(s), float_bits(s), false, false);
+    s = bits_float(t.x) + bits_float(t.y);
+    const u32x2 u = __builtin_amdgcn_permlane32_swap(float_bits(s), float_bits(s), false, false);
+    return bits_float(u.x) + bits_float(u.y);
 }
 
 template <class Op, int kThreads>
@@ -129,14 +171,43 @@ __device__ __forceinline__ float logit(const typename Z::type *z, int at) {
     return Z::up(z[at]);
 }
 
-// How a row's logits are shared out: those before the first whole cache line
-// one each to the first threads, then groups by turns, as many turns at a time
-// (a round) as make kRound logits of a thread.
+// How a row's logits are shared out: by rounds of 4 waves (or of the single one
+// that a short row has), of which a wave takes a run of R logits a lane, its lanes
+// groups of it by turns.  Rows of up to kLong logits have 256 threads that
+// take all rounds.  Longer rows have four quarters of the rounds, each summed on
+// its own: 1024 threads take them side by side, 256 one after the other.  So the
+// order of a row's sums goes by V and the type alone, whatever the address and
+// however many rows there are.  A run's lines are whole but for the first and the
+// last, which keeps loads past L2 worth while where rows start between lines.
 constexpr int kRound = 32;
+constexpr int kLong = 16384;
 
+// wave: 0 to 3 (0 of a single one).
+template <class Z, int kThreads, int R>
+__device__ __forceinline__ int place_of(int round, int step, int wave, int lane) {
+    return (round * (kThreads == 64 ? 1 : 4) + wave) * (64 * R) + (step * 64 + lane) * Z::kGroup;
+}
+
+// N elements of 2 bytes from an odd one on, by words: an access that starts
+// between words takes longer (1000 x 50001 in bf16: 26.4 us, by words 21.1).  The
+// first and the last word hold one of them each; their other halves may lie
+// outside the row, but never on another page.
+template <class Z, int N>
+__device__ __forceinline__ Raw<Z, N> get_odd(const typename Z::type *p) {
+    const Raw<Z, N> a = get<Z, N, true>(p - 1);
+    const uint32_t next = *reinterpret_cast<const typename Z::word *>(p + N - 1);
+    Raw<Z, N> r;
+#pragma unroll
+    for (int i = 0; i < words_of<Z, N>; ++i)
+        r.w[i] = __builtin_amdgcn_alignbit(i + 1 < words_of<Z, N> ? a.w[i + 1] : next, a.w[i], 16);
+    return r;
+}
+
+// The first logit behind those in groups: the last few of a row go to the first
+// threads one each, but for the rows of a wave.
 template <class Z, int kThreads>
-__device__ __forceinline__ int place_of(int head, int turn, int thread) {
-    return head + (turn * kThreads + thread) * Z::kGroup;
+__device__ __forceinline__ int grouped(int V) {
+    return kThreads > 64 ? V & ~(Z::kGroup - 1) : V;
 }
 
 // What a workgroup looks for a row's alternatives with.  The rounds of a row
@@ -149,9 +220,14 @@ template <int kThreads, int kTop>
 struct TopPlace {
     static constexpr int kFound = kThreads == 64 ? 512 : 1024;
     static constexpr int kItems = kTop == 1 ? 1 : kThreads == 64 ? 64 : 1024;
-    uint64_t found[kFound];
+    union {
+        struct {
+            uint64_t found[kFound];
+            int32_t item[kItems];
+        };
+        Quarters<kThreads> quarters;      // until the sums are joined
+    };
     float mine[kThreads], block[kTop == 2 ? kBlocks<kThreads> : 1][kTop == 2 ? kThreads : 1];
-    int32_t item[kItems];
     float threshold, M, L;
     bool plain;
     int items, n;
@@ -194,7 +270,7 @@ __device__ __forceinline__ float bound_among(const uint32_t (&o)[kParts], uint32
 
 // A bound that at least K of a row's logits reach (K <= 64), by one wave: about
 // the K-th largest of 64, each of them the largest of every 64th thread.  With the
-// statistics computed meanwhile, 64 x 50001 in bf16 with 20 alternatives takes
+// statistics computed meanwhile, 64 x 50001 in bf16 with 20 alternatives took
 // 10.6 us, one after the other and to the last bit 11.7.  For many alternatives
 // it is one of 128, or much more than they would reach it (4096 x 32000 in bf16
 // with 64: 73 us, of 64 137; with 33: 56.5 and 58.7).
@@ -221,11 +297,13 @@ __device__ __forceinline__ float bound_of(const float *mine, int K) {
 // in bf16, 5 alternatives: 55 us, with them 72; where the wave holds 2048 it
 // loses, 30000 x 2000 62 us, by blocks 48).
 template <class Z, int kThreads, int kTop, int R>
-__device__ __forceinline__ void collect(const float (&last)[R], float first, float mine, int head, int turns, int rounds,
+__device__ __forceinline__ void collect(const float (&last)[R], float behind, float mine, int whole, int count, int rounds,
                                         TopPlace<kThreads, kTop> &s) {
-    constexpr int N = Z::kGroup, kSteps = R / N, kFound = TopPlace<kThreads, kTop>::kFound;
+    constexpr int N = Z::kGroup, kFound = TopPlace<kThreads, kTop>::kFound;
     constexpr int kItems = TopPlace<kThreads, kTop>::kItems;
-    const int thread = static_cast<int>(threadIdx.x);
+    int thread = static_cast<int>(threadIdx.x);
+    if constexpr (kTop == 1) asm volatile("" : "+v"(thread));     // or the places of all logits stay in registers between rows
+    const int wave = __builtin_amdgcn_readfirstlane(thread >> 6);
     const float threshold = s.threshold;
     const auto keep = [&](float x, int at) {
         const int k = atomicAdd(&s.n, 1);
@@ -239,14 +317,13 @@ __device__ __forceinline__ void collect(const float (&last)[R], float first, flo
             const uint64_t which = __ballot(last[i] >= threshold);      // (-infinity behind the row's end)
             if (which == 0) continue;
             const int k = n + __builtin_popcountll(which & ((uint64_t(1) << thread) - 1));
-            if (last[i] >= threshold) s.found[k] = key_of(last[i], place_of<Z, 64>(0, i / N, thread) + i % N);
+            if (last[i] >= threshold) s.found[k] = key_of(last[i], place_of<Z, 64, R>(0, i / N, 0, thread) + i % N);
             n += __builtin_popcountll(which);
         }
         if (thread == 0) s.n = n;
     } else if (mine >= threshold) {
-        if (first >= threshold) keep(first, thread);
+        if (behind >= threshold) keep(behind, whole + thread);
         if constexpr (kTop == 1) {
-            if (turns == 0) return;
 #pragma unroll
             for (int g = 0; g < R; g += 8) {
                 float most = last[g];
@@ -255,11 +332,11 @@ __device__ __forceinline__ void collect(const float (&last)[R], float first, flo
                 if (!(most >= threshold)) continue;
 #pragma unroll
                 for (int i = g; i < g + 8; ++i)
-                    if (last[i] >= threshold) keep(last[i], place_of<Z, kThreads>(head, i / N, thread) + i % N);
+                    if (last[i] >= threshold) keep(last[i], place_of<Z, kThreads, R>(wave >> 2, i / N, wave & 3, thread & 63) + i % N);
             }
         } else {
             uint32_t hits = 0;
-            const int blocks = (turns + kSteps * rounds - 1) / (kSteps * rounds);
+            const int blocks = (count + rounds - 1) / rounds;
 #pragma unroll
             for (int b = kBlocks<kThreads> - 1; b >= 0; --b)
                 hits += hits + (b < blocks && s.block[b][thread] >= threshold);
@@ -276,7 +353,7 @@ __device__ __forceinline__ void collect(const float (&last)[R], float first, flo
 // too much reaches the bound, or a NaN may have hidden a thread's largest, they
 // are looked for one by one, the row read again for each.
 template <class Z, int kThreads, int kTop, int R>
-__device__ __forceinline__ void top_of(const Logprob &a, int64_t row, int head, int rounds,
+__device__ __forceinline__ void top_of(const Logprob &a, int64_t row, int end, int count, int rounds,
                                        TopPlace<kThreads, kTop> &s) {
     constexpr int N = Z::kGroup, kSteps = R / N, kFound = TopPlace<kThreads, kTop>::kFound, kWaves = kThreads / 64;
     constexpr int kItems = TopPlace<kThreads, kTop>::kItems;
@@ -302,10 +379,12 @@ __device__ __forceinline__ void top_of(const Logprob &a, int64_t row, int head, 
             whole = items <= kItems;
             if (whole) {
                 const float threshold = s.threshold;
-                const int each = kSteps * rounds;            // turns of a block
+                const int each = kSteps * rounds;            // groups of a block
                 for (int p = thread; p < items * each; p += kThreads) {
-                    const int k = p / each, item = s.item[k], b = item / kThreads;
-                    const int at = place_of<Z, kThreads>(head, b * each + p - k * each, item - b * kThreads), n = a.V - at;
+                    const int k = p / each, item = s.item[k], b = item / kThreads, t = item - b * kThreads, g = p - k * each;
+                    const int i = b * rounds + g / kSteps, round = kThreads == 1024 ? (t >> 8) * count + i : i;
+                    const int at = place_of<Z, kThreads, R>(round, g % kSteps, t >> 6 & 3, t & 63);
+                    const int n = i < count ? end - at : 0;
                     if (n <= 0) continue;
                     float x[N];
                     open<Z, N>(get_group<Z, N>(z + at, n), x);
@@ -374,29 +453,82 @@ __device__ __forceinline__ void top_of(const Logprob &a, int64_t row, int head, 
     }
 }
 
-// kTop: 0 = no alternatives, 1 = of rows of at most one round, 2 = of any.
-// R: logits of a thread in a round.
-template <class Z, int kThreads, int R, bool kEntropy, int kTop>
-__global__ __launch_bounds__(kThreads) void k_logprob(const Logprob a) {
-    constexpr int kWaves = kThreads / 64, N = Z::kGroup, kSteps = R / N;
-    __shared__ float red[3][kWaves];
+// kTop: 0 = no alternatives, 1 = of rows of at most one round a thread, 2 = of any.
+// R: logits of a thread in a round.  kQuarters: of rows of four quarters.
+template <class Z, int kThreads, int R, bool kQuarters, bool kEntropy, int kTop>
+__global__ __launch_bounds__(kThreads, kTop == 0 ? 8 : kTop == 2 && kThreads == 256 ? 6 : 1) void k_logprob(const Logprob a) {
+    constexpr int kWaves = kThreads / 64, N = Z::kGroup, kSteps = R / N, kSpan = R * (kThreads == 64 ? 64 : 256);
+    constexpr int kEach = kQuarters && kThreads == 256 ? 4 : 1, kSums = kWaves * kEach;
+    constexpr bool kOne = kTop == 1 || kThreads == 64;
+    __shared__ float red[kWaves], sums[kEntropy ? 2 : 1][kSums];
     __shared__ typename std::conditional<(kTop > 0), TopPlace<kThreads, kTop>, char>::type top;
-    const int thread = static_cast<int>(threadIdx.x);
+    __shared__ typename std::conditional<(kTop == 0 && kEach > 1), Quarters<kThreads>, char>::type room;
+    const int thread = static_cast<int>(threadIdx.x), lane = thread & 63;
+    const int wave = kThreads == 64 ? 0 : __builtin_amdgcn_readfirstlane(thread >> 6);
+    auto &quarters = [&]() -> auto & {
+        if constexpr (kTop > 0) return top.quarters;
+        else return room;
+    }();
+    const int end = grouped<Z, kThreads>(a.V);
+    // rounds of the row, of a quarter, of a thread, of a block; the wave's first one and the one behind its last
+    const int all = (end + kSpan - 1) / kSpan, quarter = kQuarters ? (all + 3) / 4 : all;
+    const int count = kOne ? 1 : kThreads == 1024 ? quarter : all;
+    const int rounds = kTop == 2 ? (count + kBlocks<kThreads> - 1) / kBlocks<kThreads> : 1;
+    const int begin = kThreads == 1024 ? (wave >> 2) * quarter : 0;
+    const int behind_last = kOne ? begin + 1 : min(begin + count, (end - (wave & 3) * (64 * R) + kSpan - 1) / kSpan);
     for (int64_t row = blockIdx.x; row < a.N; row += gridDim.x) {
         const typename Z::type *z = static_cast<const typename Z::type *>(a.z) + row * a.ld;
         const int target = a.target ? a.target[row] : -1;
-        const int head = kThreads > 64 ? before_line<Z>(z, a.V) : 0;     // (a short row's few loads may cross lines)
-        const int turns = (a.V - head + kThreads * N - 1) / (kThreads * N);
-        const int rounds = kTop == 2 ? (turns + kSteps * kBlocks<kThreads> - 1) / (kSteps * kBlocks<kThreads>) : 1;
-        float first[2] = {-kInf, -kInf};
-        if (thread < head) first[0] = logit<Z>(z, thread);
-        Running r{-kInf, -kFar, 0.0f, 0.0f};
-        float x[R], most = -kInf;
-        int block = 0, left = rounds;
-        const auto round_of = [&](const float (&x)[R]) {
-            const float m = take_up<kEntropy>(r, x, a.c);
+        const bool odd = Z::kType == SFT_BF16 && kThreads > 64 && (reinterpret_cast<uintptr_t>(z) & 2);
+        float behind[2] = {-kInf, -kInf};
+        if (end + thread < a.V) behind[0] = logit<Z>(z, end + thread);
+        Running r{-kFar, 0.0f, 0.0f};
+        float x[R], m = -kInf, most = -kInf;
+        int block = 0, left = rounds, part = 0, round = begin;
+        const auto take_round = [&]() {
+            Raw<Z, N> raw[kSteps];
+            const auto at = [&](int u) { return place_of<Z, kThreads, R>(round, u, wave & 3, lane); };
+            if (!kOne && at(kSteps) - lane * N <= end) {
+                if (odd) {
+#pragma unroll
+                    for (int u = 0; u < kSteps; ++u) raw[u] = get_odd<Z, N>(z + at(u));
+                } else {
+#pragma unroll
+                    for (int u = 0; u < kSteps; ++u) raw[u] = get<Z, N, true>(z + at(u));
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < kSteps; ++u) {
+#pragma unroll
+                    for (int i = 0; i < words_of<Z, N>; ++i) raw[u].w[i] = Z::kLowest;
+                    if (at(u) + N <= end) {
+                        if (odd) raw[u] = get_odd<Z, N>(z + at(u));
+                        else raw[u] = get<Z, N, true>(z + at(u));
+                    }
+                }
+            }
+            if constexpr (kThreads == 64) {       // a group that the row ends in
+#pragma unroll
+                for (int u = 0; u < kSteps; ++u) {
+                    const int n = end - at(u);
+                    if (n > 0 && n < N) raw[u] = get_group<Z, N>(z + at(u), n);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kSteps; ++u) {
+                open<Z, N>(raw[u], x + u * N);
+                if constexpr (kThreads == 64) {
+                    const int n = end - at(u);
+                    if (n > 0 && n < N) {
+#pragma unroll
+                        for (int i = 0; i < N; ++i) x[u * N + i] = i < n ? x[u * N + i] : -kInf;
+                    }
+                }
+            }
+            const float own = take_up<kEntropy>(r, x, a.c, !kOne && round != (kEach > 1 ? part * quarter : begin));
+            m = __builtin_fmaxf(m, own);
             if constexpr (kTop == 2) {
-                most = __builtin_fmaxf(most, m);
+                most = __builtin_fmaxf(most, own);
                 if (--left == 0) {
                     top.block[block][thread] = most;
                     ++block;
@@ -405,84 +537,82 @@ __global__ __launch_bounds__(kThreads) void k_logprob(const Logprob a) {
                 }
             }
         };
-        Raw<Z, N> raw[kSteps];
-        int turn = 0;
-        for (; place_of<Z, kThreads>(head, turn + kSteps, 0) <= a.V; turn += kSteps) {
-#pragma unroll
-            for (int u = 0; u < kSteps; ++u) raw[u] = get<Z, N, true>(z + place_of<Z, kThreads>(head, turn + u, thread));
-#pragma unroll
-            for (int u = 0; u < kSteps; ++u) open<Z, N>(raw[u], x + u * N);
-            round_of(x);
-        }
-        if (turn < turns) {       // the last round
-#pragma unroll
-            for (int u = 0; u < kSteps; ++u) {
-                const int at = place_of<Z, kThreads>(head, turn + u, thread);
-                raw[u] = raw_zero<Z, N>();
-                if (at + N <= a.V) raw[u] = get<Z, N, true>(z + at);
-            }
-#pragma unroll
-            for (int u = 0; u < kSteps; ++u) {
-                const int at = place_of<Z, kThreads>(head, turn + u, thread), n = a.V - at;
-                if (n > 0 && n < N) raw[u] = get_group<Z, N>(z + at, n);
-            }
-#pragma unroll
-            for (int u = 0; u < kSteps; ++u) {
-                const int n = a.V - place_of<Z, kThreads>(head, turn + u, thread);
-                open<Z, N>(raw[u], x + u * N);
-                if (n < N) {
-#pragma unroll
-                    for (int i = 0; i < N; ++i) x[u * N + i] = i < n ? x[u * N + i] : -kInf;
+        if constexpr (kOne) {
+            take_round();
+        } else {
+#pragma unroll 1
+            for (; part < kEach; ++part) {
+                const int stop = kEach > 1 ? min(behind_last, (part + 1) * quarter) : behind_last;
+#pragma unroll 1
+                for (; round < stop; ++round) take_round();
+                if constexpr (kEach > 1) {
+                    quarters.put(part, r);
+                    r = Running{-kFar, 0.0f, 0.0f};
                 }
             }
-            round_of(x);
         }
         if constexpr (kTop == 2)
             if (left < rounds) top.block[block][thread] = most;
         const bool given = target >= 0 && target < a.V;
         const float at_target = given ? logit<Z>(z, target) : 0.0f;
-        if (head) take_up<kEntropy>(r, first, a.c);
+        if constexpr (kEach > 1) r = quarters.get(0);
+        if (end < a.V) m = __builtin_fmaxf(m, take_up<kEntropy>(r, behind, a.c, true));
         if constexpr (kTop > 0) {
-            top.mine[thread] = r.m;
+            top.mine[thread] = m;
             if (thread == 0) top.items = top.n = 0;
             if (kThreads == 64) __syncthreads();
         }
-        float M = block_of<Max, kThreads>(r.m, red[0]);
+        float M = block_of<Max, kThreads>(m, red);
         if constexpr (kTop > 0) {       // meanwhile one wave looks for the bound
-            if (kThreads == 64 || thread >> 6 == 1) {
+            if (kThreads == 64 || wave == 1) {
                 const float bound = bound_of<kThreads>(top.mine, a.top);
-                if ((thread & 63) == 0) top.threshold = __builtin_fmaxf(bound, -kLargest);      // (not minus infinity)
+                if (lane == 0) top.threshold = __builtin_fmaxf(bound, -kLargest);      // (not minus infinity)
             }
         }
         const float m2 = __builtin_fmaxf(M * a.c, -kFar);
-        const float less = limit(r.m2 - m2, kNothing, 0.0f), part = exp2_of(less);
-        float along = part * __builtin_fmaf(r.sum, less, r.along), sum = r.sum * part;
         // what m2 is off M * c by
         float off = __builtin_fmaf(M, a.c, -m2);
-        const bool finite = __builtin_fabsf(M) < kInf;
-        if (finite && !(__builtin_fabsf(M * a.c) < kFar)) {
-            sum = along = off = 0.0f;
-            for (int i = thread; i < a.V; i += kThreads) {
-                const float d = (logit<Z>(z, i) - M) * a.c, e = exp2_of(d);
-                sum += e;
-                along = __builtin_fmaf(e, __builtin_fmaxf(d, kNothing), along);
+        const bool finite = __builtin_fabsf(M) < kInf, far = finite && !(__builtin_fabsf(M * a.c) < kFar);
+        if (far) off = 0.0f;
+        float own[(kEntropy ? 2 : 1) * kEach];      // of each quarter: the sums, then the others
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) {
+            float sum = 0.0f, along = 0.0f;
+            if (far) {
+#pragma unroll 1
+                for (int i = q * kThreads + thread; i < a.V; i += kEach * kThreads) {
+                    const float d = (logit<Z>(z, i) - M) * a.c, e = exp2_of(d);
+                    sum += e;
+                    along = __builtin_fmaf(e, __builtin_fmaxf(d, kNothing), along);
+                }
+            } else {
+                if constexpr (kEach > 1)
+                    if (q) r = quarters.get(q);
+                const float less = limit(r.m2 - m2, kNothing, 0.0f), part = exp2_of(less);
+                along = part * __builtin_fmaf(r.sum, less, r.along);
+                sum = r.sum * part;
             }
+            own[q] = sum;
+            if constexpr (kEntropy) own[kEach + q] = along;
         }
-        sum = lanes_of<Sum, 64>(sum);
-        if (kEntropy) along = lanes_of<Sum, 64>(along);
-        if (kWaves > 1 && (thread & 63) == 0) {
-            red[1][thread >> 6] = sum;
-            if (kEntropy) red[2][thread >> 6] = along;
+        float sum = 0.0f, along = 0.0f;
+        if constexpr (kThreads == 64) {
+            sum = lanes_of<Sum, 64>(own[0]);
+            if constexpr (kEntropy) along = lanes_of<Sum, 64>(own[1]);
+        } else {
+            constexpr int kGap = 16 / ((kEntropy ? 2 : 1) * kEach);
+            const float s = sums_of(own);
+            if (lane < 16 && lane % kGap == 0) sums[lane / kGap / kEach][lane / kGap % kEach * kWaves + wave] = s;
         }
         __syncthreads();
         if (thread < 64) {        // one wave finishes the row
-            if constexpr (kWaves > 1) {
-                sum = red[1][0];
-                if (kEntropy) along = red[2][0];
+            if constexpr (kThreads > 64) {
+                sum = sums[0][0];
+                if (kEntropy) along = sums[kEntropy][0];
 #pragma unroll
-                for (int i = 1; i < kWaves; ++i) {
-                    sum += red[1][i];
-                    if (kEntropy) along += red[2][i];
+                for (int i = 1; i < kSums; ++i) {
+                    sum += sums[0][i];
+                    if (kEntropy) along += sums[kEntropy][i];
                 }
             }
             const bool none = M == -kInf && sum == 0.0f;      // a row without an allowed token
@@ -511,9 +641,9 @@ __global__ __launch_bounds__(kThreads) void k_logprob(const Logprob a) {
                 }
         }
         if constexpr (kTop > 0) {
-            collect<Z, kThreads, kTop, R>(x, first[0], r.m, head, turns, rounds, top);
+            collect<Z, kThreads, kTop, R>(x, behind[0], m, end, behind_last - begin, rounds, top);
             __syncthreads();
-            top_of<Z, kThreads, kTop, R>(a, row, head, rounds, top);
+            top_of<Z, kThreads, kTop, R>(a, row, end, count, rounds, top);
         }
         __syncthreads();
     }
@@ -619,35 +749,39 @@ constexpr int64_t kMaxGrid = 1 << 21;
 
 float scaled(float scale) { return static_cast<float>(double(scale) * 1.4426950408889634074); }
 
-template <class Z, int kThreads, int R, int kTop>
+template <class Z, int kThreads, int R, bool kQuarters, int kTop>
 void send(const Logprob &a, int64_t most, hipStream_t st) {
     const dim3 grid(static_cast<uint32_t>(std::min<int64_t>(a.N, most))), block(kThreads);
-    if (a.entropy) hipLaunchKernelGGL((k_logprob<Z, kThreads, R, true, kTop>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((k_logprob<Z, kThreads, R, false, kTop>), grid, block, 0, st, a);
+    if (a.entropy) hipLaunchKernelGGL((k_logprob<Z, kThreads, R, kQuarters, true, kTop>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((k_logprob<Z, kThreads, R, kQuarters, false, kTop>), grid, block, 0, st, a);
 }
 
 // Short rows go to a wave each, as many at a time as the device holds: starting
 // a workgroup takes longer than reading one of them.  Long rows go to 1024
 // threads where there is at most one for each CU (250 x 50001 in bf16, with 20
-// alternatives: 11.1 us, by 256 threads 14.0), else to 256 (272 of them: 15.5, by
-// 1024 threads 19.8), and from 16384 logits on (16 x 20000 in fp32, with 5: 7.0
-// and 8.0; 16 x 16384 in bf16: 6.4 and 6.3; 16 x 5000 in fp32: 6.6 and 5.9).
+// alternatives: 10.8 us, by 256 threads 14.4), else to 256 (272 of them: 15.8, by
+// 1024 threads 19.0), and beyond 16384 logits (16 x 20000 in fp32, with 5: 6.9
+// and 8.8; when tried below, 16 x 16384 in bf16: 6.4 and 6.3, 16 x 5000 in fp32:
+// 6.6 and 5.9).
 template <class Z>
 void send(const Logprob &a, hipStream_t st) {
     const int64_t waves = 32 * int64_t(num_cus());
     if (a.V <= 64 * 8) {
-        if (a.top) send<Z, 64, 8, 1>(a, waves, st);
-        else send<Z, 64, 8, 0>(a, waves, st);
+        if (a.top) send<Z, 64, 8, false, 1>(a, waves, st);
+        else send<Z, 64, 8, false, 0>(a, waves, st);
     } else if (a.V <= 64 * kRound) {
-        if (a.top) send<Z, 64, kRound, 2>(a, waves, st);
-        else send<Z, 64, kRound, 0>(a, waves, st);
-    } else if (a.N <= num_cus() && a.V >= 16384) {
-        if (!a.top) send<Z, 1024, kRound, 0>(a, kMaxGrid, st);
-        else if (a.V <= 1024 * kRound) send<Z, 1024, kRound, 1>(a, kMaxGrid, st);
-        else send<Z, 1024, kRound, 2>(a, kMaxGrid, st);
+        if (a.top) send<Z, 64, kRound, false, 2>(a, waves, st);
+        else send<Z, 64, kRound, false, 0>(a, waves, st);
+    } else if (a.V <= kLong) {
+        if (a.top) send<Z, 256, kRound, false, 2>(a, kMaxGrid, st);
+        else send<Z, 256, kRound, false, 0>(a, kMaxGrid, st);
+    } else if (a.N <= num_cus()) {
+        if (!a.top) send<Z, 1024, kRound, true, 0>(a, kMaxGrid, st);
+        else if (a.V <= 1024 * kRound) send<Z, 1024, kRound, true, 1>(a, kMaxGrid, st);
+        else send<Z, 1024, kRound, true, 2>(a, kMaxGrid, st);
     } else {
-        if (a.top) send<Z, 256, kRound, 2>(a, kMaxGrid, st);
-        else send<Z, 256, kRound, 0>(a, kMaxGrid, st);
+        if (a.top) send<Z, 256, kRound, true, 2>(a, kMaxGrid, st);
+        else send<Z, 256, kRound, true, 0>(a, kMaxGrid, st);
     }
 }
 

@@ -29,6 +29,7 @@ struct Fp32 {
     typedef float type;
     static constexpr int kGroup = 4;
     static constexpr int32_t kType = SFT_F32;
+    static constexpr uint32_t kLowest = 0xff800000u;      // a word of minus infinity
     typedef u32x4 __attribute__((aligned(4))) quad;
     typedef u32x2 __attribute__((aligned(4))) twin;
     typedef uint32_t word;
@@ -41,6 +42,7 @@ struct Bf16 {
     typedef uint16_t type;
     static constexpr int kGroup = 8;
     static constexpr int32_t kType = SFT_BF16;
+    static constexpr uint32_t kLowest = 0xff80ff80u;
     typedef u32x4 __attribute__((aligned(2))) quad;
     typedef u32x2 __attribute__((aligned(2))) twin;
     typedef uint32_t __attribute__((aligned(2))) word;

@@ -426,3 +426,49 @@ def test_logits_far_from_zero(gpu_lib, dtype):
                 e = (V / (64 if V <= 2048 else 256) * 1.125 + 46 + 3 * pd + 4 * L) * U
                 assert ((got["stats"][:, 1].double().cpu() - L).abs() <= e).all(), (far, bits)
                 assert ((got["logp"].double().cpu() - logp).abs() <= e + 4 * U * logp.abs()).all(), (far, bits)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [300, 500, 1001, 2048, 2049, 5000, 16383, 16384, 20000, 33001, 50001, 70001])
+def test_a_row_is_the_same_in_any_batch_and_at_any_address(gpu_lib, V, dtype):
+    # one row alone, as the last of more rows than the device has CUs, at other addresses, with and without the optional
+    # outputs; around a value far from zero, too
+    z = torch.empty(600, V, dtype=dtype, device="cuda")
+    z.copy_(torch.randn(600, V, device="cuda", generator=torch.Generator("cuda").manual_seed(V)) * 2.5)
+    for far in (0.0, -3e7):
+        row = normal((1, V), 2.5, V, dtype).cuda()
+        if far:
+            row = (row.float() * 3e3 + far).to(dtype)
+        z[599] = z[7] = row[0]
+        target = torch.arange(600, device="cuda").int()
+        target[599] = target[7] = V // 3
+        want = None
+        for at in (None, 0, 1, 3, 8, 16, 31, 57):
+            if at is None:
+                rows, given = z, target
+            else:
+                room = torch.zeros(V + 64, dtype=dtype, device="cuda")
+                rows, given = room[at:at + V].view(1, V), target[7:8].contiguous()
+                rows.copy_(row)
+            for K in (0, 5):
+                N = rows.shape[0]
+                logp, H = torch.empty(N, device="cuda"), torch.empty(N, device="cuda")
+                stats = torch.empty(N, 2, device="cuda")
+                top, index = torch.empty(N, 5, device="cuda"), torch.empty(N, 5, dtype=torch.int32, device="cuda")
+                more = dict(top_logp=top, top_index=index) if K else {}
+                _lib.sft_logprob(rows, given, logp, stats=stats, entropy=H, **more)
+                only = torch.empty(N, device="cuda")
+                _lib.sft_logprob(rows, given, only)
+                assert torch.equal(only, logp)
+                dz = torch.empty_like(rows) if at is None else torch.empty(V + 64, dtype=dtype,
+                                                                           device="cuda")[at:at + V].view(1, V)
+                _lib.sft_logprob_grad(rows, given, stats, torch.ones(N, device="cuda"), dz, entropy=H,
+                                      dentropy=torch.ones(N, device="cuda"))
+                for i in ((7, 599) if at is None else (0,)):
+                    got = [x[i].clone() for x in (logp, stats, H, dz)]
+                    want = want or got
+                    assert all(torch.equal(a, b) for a, b in zip(want, got)), (far, at, K, i)
+                    if K:
+                        best = [x[i].clone() for x in (top, index)]
+                        want = want + best if len(want) == 4 else want
+                        assert all(torch.equal(a, b) for a, b in zip(want[4:], best)), (far, at, K, i)
