@@ -947,8 +947,13 @@ enum { SFT_NORM_LAYER = 0, SFT_NORM_RMS = 1 };
  * aligned to their types; nothing else is asked of sizes or addresses.
  * What is written must not overlap anything else, but H may be X or res
  * itself (the same address and row distance).
+ * Rows whose squares overflow fp32, or vanish in it with eps as small, are
+ * taken in other units: finite rows have finite results, but where values
+ * differ from their mean by more than fp32 holds.
  * With eps = 0 a row of equal values (of zeros, for SFT_NORM_RMS) becomes
- * NaN, as the formula has it; a row that holds NaN or infinities as well.
+ * NaN, as the formula has it; so does a row that holds NaN, and for
+ * SFT_NORM_LAYER one that holds an infinity.  For SFT_NORM_RMS an infinity
+ * makes rstd 0: Y is NaN in its place and the bias elsewhere.
  * Limits: 1 <= C <= 16384, T < 2^31, rows less than 2^40 elements apart,
  * arrays that span less than 2^46 bytes.
  * Errors: SFT_EINVAL (null pointers, negative sizes, bad kind or type, eps

@@ -325,3 +325,38 @@ def test_the_same_results_every_time(gpu_lib):
     one = torch.empty(1, 4096, dtype=BF16, device="cuda")
     _lib.sft_norm_backward(x[77:78], None, rstd[:1], dy[77:78], one, None, kind="rms")
     assert torch.equal(one[0], first[0][77])
+
+
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+def test_forward_of_rows_whose_squares_leave_fp32(gpu_lib, kind):
+    # among ordinary rows some whose squares or sums overflow (as bf16 can hold them, too), and, without eps, some whose
+    # squares underflow; every kind of team, and rows of H that replaced the ones of X
+    for i, C in enumerate((9, 100, 200, 400, 1000, 1024, 2000, 4096, 12000, 16384)):
+        scale = torch.ones(9)
+        scale[2], scale[3], scale[4], scale[7] = 1e19, 3e25, 1e37, 4e18
+        for x_type, y_type in TYPES:
+            x = (normal((9, C), 1.0, C) * scale[:, None]).to(x_type)
+            run_forward(9, C, kind, x_type, y_type, x=x, pad=i % 3)
+            run_forward(9, C, kind, x_type, y_type, x=x, res=True, inplace=[None, "x", "res"][i % 3])
+        scale[2], scale[3], scale[4], scale[7] = 1e-20, 1e-26, 1e-33, 1e12
+        for x_type, y_type in TYPES:
+            x = (normal((9, C), 1.0, C) * scale[:, None]).to(x_type)
+            run_forward(9, C, kind, x_type, y_type, x=x, pad=i % 3, eps=0.0)
+
+
+def test_backward_of_rows_whose_squares_leave_fp32(gpu_lib):
+    # the statistics of the forward pass serve the backward pass, at such rows as well
+    T, C = 9, 1000
+    for kind in ("layer", "rms"):
+        scale = torch.ones(9)
+        scale[2], scale[3], scale[7] = 1e19, 3e25, 1e30
+        h = normal((T, C), 1.0, 3) * scale[:, None]
+        dy = normal((T, C), 0.1, 4)
+        y, mean, rstd = torch.empty(T, C, device="cuda"), torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+        _lib.sft_norm_forward(h.cuda(), None, y, kind=kind, eps=EPS, mean=mean, rstd=rstd)
+        dx, dgain = torch.empty(T, C, device="cuda"), torch.empty(C, device="cuda")
+        ws = torch.empty(_lib.sft_norm_backward_workspace(T, C), dtype=torch.uint8, device="cuda")
+        _lib.sft_norm_backward(h.cuda(), None, rstd, dy.cuda(), dx, dgain, kind=kind, mean=mean, ws=ws)
+        want, bound = backward64(h.double(), None, mean.cpu().double(), rstd.cpu().double(), dy.double(), None, kind, depth(T))
+        close(dx, want[0], bound[0], "dX")
+        close(dgain, want[1], bound[1], "dgain")
