@@ -1002,10 +1002,12 @@ size_t sft_norm_backward_workspace(int64_t T, int64_t C, int32_t with_bias);
  *               neither dgain nor dbias is wanted; calls sharing it must be
  *               ordered on one stream
  *   ldh, ldy, ldr, ldx   row distances of H, dY, dH and dX
- * Sums over a row and over the rows are in fp32, in an order that depends
- * only on T, C and the device: results are deterministic.  What is written
- * must not overlap anything else, but dX may be dY or dH itself (the same
- * address, row distance and type).
+ * Sums over a row and over the rows are in fp32.  A row's are in an order that
+ * depends only on C and x_type; those over the rows depend on T, C, x_type,
+ * the device's number of CUs, and on whether dX is dY.  So results are
+ * deterministic, but the last bits of dgain and dbias may differ between
+ * dX in dY's place and elsewhere.  What is written must not overlap anything
+ * else, but dX may be dY or dH itself (the same address, row distance and type).
  * Limits and errors: as sft_norm_forward, SFT_ECAPACITY (workspace too small).
  */
 typedef struct sft_norm_grad_args {

@@ -360,3 +360,30 @@ def test_backward_of_rows_whose_squares_leave_fp32(gpu_lib):
         want, bound = backward64(h.double(), None, mean.cpu().double(), rstd.cpu().double(), dy.double(), None, kind, depth(T))
         close(dx, want[0], bound[0], "dX")
         close(dgain, want[1], bound[1], "dgain")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_in_place_gradients_are_those_of_a_separate_array(gpu_lib, dtype):
+    # dX bit by bit; the sums over the rows the same on every call, and within their bound of one another
+    for T, C in ((37, 1375), (700, 300), (1024, 2048), (3000, 64), (2000, 3000)):
+        h, dy, dh = (normal((T, C), 1.0, s, dtype).cuda() for s in (1, 2, 3))
+        mean, rstd = h.float().mean(1), torch.ones(T, device="cuda")
+        ws = torch.empty(_lib.sft_norm_backward_workspace(T, C, bias=True), dtype=torch.uint8, device="cuda")
+
+        def call(place):
+            g, r = dy.clone(), dh.clone()
+            dx = {"apart": torch.empty_like(h), "dY": g, "dH": r}[place]
+            sums = [torch.empty(C, device="cuda") for _ in range(2)]
+            _lib.sft_norm_backward(h, None, rstd, g, dx, sums[0], kind="layer", mean=mean, dbias=sums[1], dH=r, ws=ws)
+            return [dx, *sums]
+
+        apart = call("apart")
+        size = [(dy.double() * (h.double() - mean.double()[:, None])).abs().sum(0), dy.double().abs().sum(0)]
+        for place in ("dY", "dH"):
+            first = call(place)
+            assert all(torch.equal(a, b) for a, b in zip(first, call(place))), (T, C, place)
+            assert torch.equal(first[0], apart[0]), (T, C, place)
+            for a, b, s in zip(first[1:], apart[1:], size):
+                # at most T additions each, and two roundings of a product
+                assert ((a.double() - b.double()).abs() <= 2 * (min(T, 200) + 4) * U * s).all(), (T, C, place)
+                assert place != "dH" or torch.equal(a, b)
