@@ -142,6 +142,16 @@ __device__ __forceinline__ void turn_item(const Item &it, const Raw<E, E::kGroup
     put_group<E, N, kPast>(y + it.at1, close<E, N>(v), it.n1);
 }
 
+// The turns that pos steps of `angle` make, but for whole ones.  Both products
+// carry what their roundings leave out, and 1/(2 pi) its second part: rounded to
+// fp64 alone, three of them would be 6 units of fp32 at position 2^30.
+__device__ __forceinline__ double turns_of(double angle, int32_t pos) {
+    constexpr double kTurn = 0x1.45f306dc9c883p-3, kTurnRest = -0x1.6b01ec5417056p-57;
+    const double step = angle * kTurn, step_rest = __builtin_fma(angle, kTurn, -step) + angle * kTurnRest;
+    const double all = step * pos, rest = __builtin_fma(step, double(pos), -all) + step_rest * pos;
+    return (all - __builtin_rint(all)) + rest;
+}
+
 template <class E, bool kHalf, bool kPast>
 __global__ __launch_bounds__(kThreads) void k_rotary(const Rotary a) {
     extern __shared__ f32x4 room[];       // cosine and sine of each token's pairs, and 8 pairs more for a last short group
@@ -165,12 +175,11 @@ __global__ __launch_bounds__(kThreads) void k_rotary(const Rotary a) {
             r0 = get_group<E, N>(x + it.x + it.at0, it.n0);
             r1 = get_group<E, N>(x + it.x + it.at1, it.n1);
         }
-        // in turns, of which whole ones do not matter: what is left is exact to fp32 however far the position
+        // in turns, of which whole ones do not matter
         for (uint32_t k = threadIdx.x; k < tokens * uint32_t(half); k += kThreads) {
             const uint32_t t = over(k, a.pairs), token = first + t, b = over(token, a.rows);
             const int32_t pos = a.pos[b * a.pos_batch + (token - b * a.rows.by)];
-            double turns = a.freq[k - t * half] * 0.15915494309189533577 * pos;
-            turns -= __builtin_rint(turns);
+            const double turns = turns_of(a.freq[k - t * half], pos);
             float s, c;
             sincospif(static_cast<float>(2.0 * turns), &s, &c);
             sines[2 * k] = c * a.amplitude;

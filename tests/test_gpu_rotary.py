@@ -193,3 +193,44 @@ def test_offsets_past_32_bits(gpu_lib):
     check(y, x, pos, freq, D, "half")
     _lib.sft_rotary([(view, view)], pos.cuda(), on_freq, D)
     assert torch.equal(view, y)
+
+
+@pytest.mark.parametrize("inverse", [False, True])
+def test_far_positions_are_as_good_as_near_ones(gpu_lib, inverse):
+    # positions over the whole range of int32 whose angle is close to a whole number of half turns: there a sine is as small
+    # as the distance, and shows what the angle is off by
+    cand = np.random.default_rng(5).integers(-2 ** 31, 2 ** 31, 2_000_000)
+    sine = np.sin(cand.astype(np.longdouble))
+    pos = cand[np.abs(sine) < 5e-4]
+    assert len(pos) > 300 and np.abs(pos).max() > 2 ** 30
+    T = len(pos)
+    freq, on_freq = table(2)          # one radian a position
+    x = torch.zeros(T, 1, 2, device="cuda")
+    x[..., 0] = 1.0
+    y = torch.empty_like(x)
+    _lib.sft_rotary([(x, y)], torch.from_numpy(pos.astype(np.int32)).cuda(), on_freq, 2, inverse=inverse)
+    want = np.sin(pos.astype(np.longdouble)).astype(np.float64) * (-1 if inverse else 1)
+    # relative: the reduced turns in fp32, 2 units in the last place of the sine, the product; 2 ** -33 of the angle here.
+    # Close to half a turn, where the cosine is negative, twice the turns are a number in [1/2, 1], which fp32 holds to
+    # 2 ** -25: pi times that of the angle, whatever the distance
+    far_side = np.cos(pos.astype(np.longdouble)) < 0
+    bound = 8 * U * np.abs(want) + 1e-9 + 1.01 * np.pi * U / 2 * far_side
+    assert (np.abs(y[:, 0, 1].cpu().double().numpy() - want) <= bound).all()
+
+
+def test_more_workgroups_than_a_launch_has(gpu_lib):
+    # tokens of 16 elements, 64 of them a workgroup: more than 2^23 workgroups, in place (17 GB)
+    B, T, D = 1 << 10, (1 << 19) + 3, 16
+    freq, on_freq = table(D)
+    x = torch.empty(B, T, 1, D, dtype=BF16, device="cuda")
+    row = torch.arange(T, device="cuda", dtype=torch.int32)
+    for b in range(0, B, 64):
+        x[b:b + 64] = torch.randn(64, T, 1, D, dtype=BF16, device="cuda",
+                                  generator=torch.Generator("cuda").manual_seed(b))
+    at = [(0, 0), (0, 70), (511, 12345), (B - 1, T - 70), (B - 1, T - 3)]
+    at += [(b, (t * 7919) % (T - 3)) for b, t in zip(range(0, B, 8), range(128))]
+    before = torch.stack([x[b, t:t + 3] for b, t in at]).cpu()
+    _lib.sft_rotary([(x, x)], row, on_freq, D)
+    after = torch.stack([x[b, t:t + 3] for b, t in at])
+    pos = torch.stack([row[t:t + 3] for _, t in at]).cpu()
+    check(after, before, pos, freq, D, "half")
