@@ -97,7 +97,7 @@
 extern "C" {
 #endif
 
-#define SFT_ABI_VERSION 17
+#define SFT_ABI_VERSION 18
 
 enum {
     SFT_OK = 0,

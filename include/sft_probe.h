@@ -61,6 +61,16 @@ int sft_probe_dw_plan(const sft_dw_group *groups, int32_t n_groups, int32_t cus,
  */
 int sft_probe_expert_tiles(int32_t op, int64_t E, int64_t T, int64_t R, int64_t C, int32_t cus, int32_t *out);
 
+/*
+ * The bound that sft_logprob would look for a row's alternatives with, from n
+ * (1 to 128) of its threads' largest logits (host only): at least `want` of
+ * them reach it.  Where more than want + want / 4 do, it is so close to the
+ * want-th largest that none lies between.  It may be NaN where minus infinity
+ * is among those wanted.
+ * Errors: SFT_EINVAL (null pointers, n or want out of range, NaN).
+ */
+int sft_probe_logprob_bound(const float *values, int32_t n, int32_t want, float *bound);
+
 #ifdef __cplusplus
 }
 #endif

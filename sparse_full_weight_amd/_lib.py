@@ -39,7 +39,7 @@ EXPORTS = (
     "sft_plan_upload", "sft_grad_clip_workspace", "sft_grad_clip", "sft_adamw",
     "sft_expert_forward", "sft_expert_dx", "sft_expert_dw", "sft_probe_expert_tiles",
     "sft_norm_forward", "sft_norm_backward_workspace", "sft_norm_backward", "sft_rotary_table", "sft_rotary",
-    "sft_logprob", "sft_logprob_grad",
+    "sft_logprob", "sft_logprob_grad", "sft_probe_logprob_bound",
 )
 
 
@@ -257,6 +257,7 @@ def lib() -> C.CDLL:
         L.sft_probe_mfma.argtypes = [i64, p, p]
         L.sft_probe_dw_plan.argtypes = [C.POINTER(CDwGroup), i32, i32, p, i32]
         L.sft_probe_expert_tiles.argtypes = [i32, i64, i64, i64, i64, i32, p]
+        L.sft_probe_logprob_bound.argtypes = [p, i32, i32, p]
         L.sft_helix_init.argtypes = [C.POINTER(CHelix)]
         L.sft_helix_step.argtypes = [C.POINTER(CHelix), C.c_double, i32, C.POINTER(C.c_int32),
                                      C.POINTER(C.c_double)]
@@ -1550,3 +1551,13 @@ def sft_probe_expert_tiles(op: str, E: int, T: int, R: int, Cc: int, cus: int = 
     out = np.zeros(4, np.int32)
     _check(lib().sft_probe_expert_tiles(EXPERT_OPS.index(op), E, T, R, Cc, cus, _np_ptr(out)))
     return tuple(out.tolist())
+
+
+def sft_probe_logprob_bound(values: np.ndarray, want: int) -> float:
+    """The bound that sft_logprob would take from these largest logits of
+    threads (float32, up to 128), so that at least `want` reach it (no device
+    work)."""
+    values = np.ascontiguousarray(values, np.float32)
+    out = np.zeros(1, np.float32)
+    _check(lib().sft_probe_logprob_bound(_np_ptr(values), values.size, want, _np_ptr(out)))
+    return float(out[0])

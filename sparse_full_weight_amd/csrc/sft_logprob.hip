@@ -25,6 +25,7 @@
 
 #include "sft_blocks.h"
 #include "sft_internal.h"
+#include "sft_probe.h"
 #include "sft_vec.h"
 
 namespace {
@@ -55,11 +56,11 @@ __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2
 __device__ __forceinline__ float limit(float x, float lo, float hi) { return __builtin_amdgcn_fmed3f(x, lo, hi); }
 
 // Order of floats (without NaN; the two zeros are one value) as unsigned integers; 0 is below all of them.
-__device__ __forceinline__ uint32_t order_of(float x) {
+__host__ __device__ __forceinline__ uint32_t order_of(float x) {
     const uint32_t b = float_bits(x + 0.0f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
-__device__ __forceinline__ float float_of(uint32_t order) {
+__host__ __device__ __forceinline__ float float_of(uint32_t order) {
     return bits_float(order & 0x80000000u ? order & 0x7fffffffu : ~order);
 }
 // Larger for a larger logit, of equal ones for the lower index.
@@ -237,26 +238,17 @@ struct Or {
     static __device__ __forceinline__ float of(float a, float b) { return bits_float(float_bits(a) | float_bits(b)); }
 };
 
-// A bound that at least `want` and hardly more of a wave's values reach, found by
-// halving from the first bit on in which they differ to the last (in bf16 the
-// lower half never does), two bits at a time.
-template <int kParts>
-__device__ __forceinline__ float bound_among(const uint32_t (&o)[kParts], uint32_t want) {
-    const uint32_t one = __builtin_amdgcn_readfirstlane(o[0]);
-    uint32_t differ = 0;
-#pragma unroll
-    for (int i = 0; i < kParts; ++i) differ |= o[i] ^ one;
-    differ = __builtin_amdgcn_readfirstlane(float_bits(lanes_of<Or, 64>(bits_float(differ))));
-    if (differ == 0) return float_of(one);      // (no first bit: the loop's end needs one)
+// A bound that at least `want` and hardly more of `all` values reach (want <= all),
+// found by halving from the first bit on in which they differ to the last (in bf16
+// the lower half never does), two bits at a time.  one: any of them; differ: the
+// bits in which another differs from it, not 0 (the loop's end needs one);
+// reached(b): how many are b or larger.
+template <class Reached>
+__host__ __device__ __forceinline__ uint32_t bound_bits(uint32_t one, uint32_t differ, uint32_t want, uint32_t all,
+                                                        const Reached &reached) {
     const uint32_t top = (31u - static_cast<uint32_t>(__builtin_clz(differ))) | 1u, least = differ & (0u - differ);
-    const auto reached = [&](uint32_t b) {
-        uint32_t n = 0;
-#pragma unroll
-        for (int i = 0; i < kParts; ++i) n += static_cast<uint32_t>(__builtin_popcountll(__ballot(o[i] >= b)));
-        return n;
-    };
-    uint32_t bound = one & ~((2u << top) - 1u), bit = 1u << top, reach = 64 * kParts;
-    const uint32_t most = min(want + want / 4, reach - 1u);         // (all of them reach the prefix alone)
+    uint32_t bound = one & ~((2u << top) - 1u), bit = 1u << top, reach = all;
+    const uint32_t enough = want + want / 4, most = enough < all ? enough : all - 1u;      // (all of them reach the prefix alone)
     do {
         const uint32_t b1 = bound | bit >> 1, b2 = bound | bit, b3 = b1 | b2;
         const uint32_t r1 = reached(b1), r2 = reached(b2), r3 = reached(b3);
@@ -265,7 +257,24 @@ __device__ __forceinline__ float bound_among(const uint32_t (&o)[kParts], uint32
         if (r3 >= want) bound = b3, reach = r3;
         bit >>= 2;
     } while ((bit >= least) & (reach > most));
-    return float_of(bound);
+    return bound;
+}
+
+// The same of kParts values of each lane of a wave.
+template <int kParts>
+__device__ __forceinline__ float bound_among(const uint32_t (&o)[kParts], uint32_t want) {
+    const uint32_t one = __builtin_amdgcn_readfirstlane(o[0]);
+    uint32_t differ = 0;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) differ |= o[i] ^ one;
+    differ = __builtin_amdgcn_readfirstlane(float_bits(lanes_of<Or, 64>(bits_float(differ))));
+    if (differ == 0) return float_of(one);
+    return float_of(bound_bits(one, differ, want, 64 * kParts, [&](uint32_t b) {
+        uint32_t n = 0;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) n += static_cast<uint32_t>(__builtin_popcountll(__ballot(o[i] >= b)));
+        return n;
+    }));
 }
 
 // A bound that at least K of a row's logits reach (K <= 64), by one wave: about
@@ -883,6 +892,23 @@ int sft_logprob_grad(const sft_logprob_grad_args *v, void *stream) {
     else send_grad<Fp32, Fp32>(a, st);
     const hipError_t e = hipGetLastError();
     SFT_CHECK(e == hipSuccess, SFT_EHIP, "%s: launch failed: %s", who, hipGetErrorString(e));
+    return SFT_OK;
+}
+
+int sft_probe_logprob_bound(const float *values, int32_t n, int32_t want, float *bound) {
+    const char *const who = "sft_probe_logprob_bound";
+    clear_error();
+    SFT_CHECK(values && bound, SFT_EINVAL, "%s: null pointer", who);
+    SFT_CHECK(n >= 1 && n <= 128 && want >= 1 && want <= n, SFT_EINVAL, "%s: n outside [1, 128] or want outside [1, n]", who);
+    uint32_t order[128], differ = 0;
+    for (int32_t i = 0; i < n; ++i) {
+        SFT_CHECK(values[i] == values[i], SFT_EINVAL, "%s: a value is NaN", who);
+        order[i] = order_of(values[i]);
+        differ |= order[i] ^ order[0];
+    }
+    *bound = float_of(differ == 0 ? order[0] : bound_bits(order[0], differ, want, n, [&](uint32_t b) {
+        return static_cast<uint32_t>(std::count_if(order, order + n, [&](uint32_t o) { return o >= b; }));
+    }));
     return SFT_OK;
 }
 

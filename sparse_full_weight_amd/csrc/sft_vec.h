@@ -15,8 +15,8 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ float bits_float(uint32_t x) { return __builtin_bit_cast(float, x); }
-__device__ __forceinline__ uint32_t float_bits(float x) { return __builtin_bit_cast(uint32_t, x); }
+__host__ __device__ __forceinline__ float bits_float(uint32_t x) { return __builtin_bit_cast(float, x); }
+__host__ __device__ __forceinline__ uint32_t float_bits(float x) { return __builtin_bit_cast(uint32_t, x); }
 __device__ __forceinline__ uint32_t bf16_bits(float x) {
     return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));     // to nearest even
 }

@@ -259,3 +259,57 @@ def test_no_rows_ask_for_nothing():
     none = dict(N=0, Z=None, target=None, logp=None, stats=None, entropy=None, top_logp=None, top_index=None)
     assert _logprob(**none) == _lib.SFT_OK
     assert _logprob_grad(N=0, Z=None, dZ=None, target=None, stats=None, entropy=None, dlogp=None, dentropy=None) == _lib.SFT_OK
+
+
+# ------------------------------------------------------------------ the bound of the alternatives
+def _values(rs, n, kind):
+    x = rs.standard_normal(n).astype(np.float32) * 3
+    if kind == "bf16":
+        x = (x.view(np.uint32) & 0xffff0000).view(np.float32)
+    elif kind == "few":
+        x = np.round(x)
+    elif kind == "equal":
+        x[:] = x[0]
+    elif kind == "two":
+        x = np.where(rs.random(n) < rs.random(), x[0], x[-1])
+    elif kind == "near":
+        x = (np.float32(rs.choice([1.0, -1.0, 1e30, -1e-40])).view(np.uint32) + rs.integers(0, 3, n).astype(np.uint32)).view(
+            np.float32)
+    elif kind == "bits":
+        x = rs.integers(0, 1 << 32, n, dtype=np.uint64).astype(np.uint32).view(np.float32)
+        x = np.where(np.isnan(x), np.float32(0), x)
+    elif kind == "masked":
+        x = np.where(rs.random(n) < rs.random(), np.float32(rs.choice([-np.inf, -1e30, -3.4028235e38])), x)
+    elif kind == "zeros":
+        x = rs.choice(np.array([0.0, -0.0, 1e-45, -1e-45], np.float32), n)
+    return x.astype(np.float32)
+
+
+@pytest.mark.parametrize("kind", ["any", "bf16", "few", "equal", "two", "near", "bits", "masked", "zeros"])
+def test_bound_of_the_alternatives(kind):
+    # the search ends, and at least `want` values reach what it finds; where many more do, they are equal to the want-th
+    rs = np.random.default_rng(len(kind))
+    for n in (64, 128, 1, 2, 3, 63):
+        for want in sorted({1, 2, 5, 20, 32, 33, 51, 63, 64, n} & set(range(1, n + 1))):
+            for _ in range(40):
+                x = _values(rs, n, kind)
+                with np.errstate(invalid="ignore"):
+                    bound = _lib.sft_probe_logprob_bound(x, want)
+                wanted = np.sort(x)[::-1][want - 1]
+                if math.isnan(bound):      # below minus infinity: all of them
+                    assert wanted == -INF
+                    continue
+                reach = int((x >= bound).sum())
+                assert reach >= want
+                assert reach <= want + want // 4 or reach == int((x >= wanted).sum())
+
+
+def test_bound_of_the_alternatives_refuses():
+    x, out = np.ones(128, np.float32), np.zeros(1, np.float32)
+    probe = _lib.lib().sft_probe_logprob_bound
+    for values, n, want, bound in ((None, 64, 1, out), (x, 64, 1, None), (x, 0, 1, out), (x, 129, 1, out), (x, 64, 0, out),
+                                   (x, 64, 65, out)):
+        assert probe(None if values is None else values.ctypes.data, n, want,
+                     None if bound is None else bound.ctypes.data) == EINVAL
+    x[3] = NAN
+    _refused(probe(x.ctypes.data, 64, 1, out.ctypes.data), EINVAL, b"NaN")
