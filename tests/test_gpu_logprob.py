@@ -472,3 +472,12 @@ def test_a_row_is_the_same_in_any_batch_and_at_any_address(gpu_lib, V, dtype):
                         best = [x[i].clone() for x in (top, index)]
                         want = want + best if len(want) == 4 else want
                         assert all(torch.equal(a, b) for a, b in zip(want[4:], best)), (far, at, K, i)
+
+
+@pytest.mark.parametrize("N,V", [(8300, 300), (16500, 77), (8300, 700)])
+def test_more_short_rows_than_waves(gpu_lib, N, V):
+    # a wave a row, past the rows that the device holds at a time
+    z = logits(N, V, V, BF16)
+    check(z, torch.randint(0, V, (N,), generator=gen(N)), 1.0, 5)
+    for dtype, out_type in ((F32, F32), (BF16, BF16), (F32, BF16)):
+        check_gradient(N, V, dtype, out_type, with_entropy=dtype == F32, seed=V)

@@ -387,3 +387,48 @@ def test_in_place_gradients_are_those_of_a_separate_array(gpu_lib, dtype):
                 # at most T additions each, and two roundings of a product
                 assert ((a.double() - b.double()).abs() <= 2 * (min(T, 200) + 4) * U * s).all(), (T, C, place)
                 assert place != "dH" or torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,C,dtype", [(8300, 1100, BF16), (8300, 600, F32), (4200, 2050, BF16), (4200, 2048, F32),
+                                       (4130, 4100, BF16)])
+def test_forward_of_more_rows_than_workgroups_that_share_sums(gpu_lib, T, C, dtype):
+    # teams of several waves, past the 16 workgroups a CU of a launch: the places of their sums by turns
+    run_forward(T, C, "layer", dtype, dtype, seed=T)
+    run_forward(T, C, "rms", dtype, BF16, seed=C, res=True)
+
+
+@pytest.mark.parametrize("T,C", [(16 * (1 << 21) + 21, 2), (600_007, 40), (100_003, 200), (70_001, 505), (40_001, 1000),
+                                 (20_011, 2050), (9001, 4096), (3001, 8192), (2001, 12000), (1100, 16384)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_every_row_counts_once_in_the_gradients(gpu_lib, T, C, dtype):
+    # small whole numbers, so that the sums over the rows are exact in any order: a row left out or taken twice, of a last
+    # turn that not all teams have, shows
+    g = torch.Generator("cuda").manual_seed(T)
+    h = torch.randint(-2, 3, (T, C), device="cuda", generator=g, dtype=torch.int8)
+    dy = torch.randint(-1, 2, (T, C), device="cuda", generator=g, dtype=torch.int8)
+    dy[-3:] = 1                              # the last rows count for certain
+    want_gain, want_bias = torch.zeros(2, C, dtype=torch.int64, device="cuda")
+    for at in range(0, T, 1 << 20):
+        a, b = h[at:at + (1 << 20)].long(), dy[at:at + (1 << 20)].long()
+        want_gain, want_bias = want_gain + (a * b).sum(0), want_bias + b.sum(0)
+    h, dy = h.to(dtype), dy.to(dtype)
+    dx, rstd, mean = torch.empty_like(h), torch.ones(T, device="cuda"), torch.zeros(T, device="cuda")
+    dgain, dbias = torch.empty(2, C, device="cuda")
+    ws = torch.empty(_lib.sft_norm_backward_workspace(T, C, bias=True), dtype=torch.uint8, device="cuda")
+    for kind in ("rms", "layer"):
+        _lib.sft_norm_backward(h, None, rstd, dy, dx, dgain, kind=kind, mean=mean if kind == "layer" else None,
+                               dbias=dbias, ws=ws)
+        assert torch.equal(dgain.long(), want_gain) and torch.equal(dgain, dgain.round())
+        assert torch.equal(dbias.long(), want_bias) and torch.equal(dbias, dbias.round())
+        for at in range(0, T, 1 << 18):
+            x, d, got = (t[at:at + (1 << 18)].double() for t in (h, dy, dx))
+            along, flat = (x * d).mean(1, keepdim=True), d.mean(1, keepdim=True) * (kind == "layer")
+            want = d - x * along - flat
+            # exact sums; the quotients' two roundings each, a product, two differences
+            bound = 4 * U * ((x * along).abs() + flat.abs()) + 3 * U * (d.abs() + (x * along).abs() + flat.abs())
+            if dtype == BF16:
+                bound = bound + 2.0 ** -8 * (want.abs() + bound)
+            assert ((got - want).abs() <= bound).all(), (kind, at)
+    # frozen biases take the other instance
+    _lib.sft_norm_backward(h, None, rstd, dy, dx, dgain, kind="rms", ws=ws)
+    assert torch.equal(dgain.long(), want_gain)
