@@ -286,6 +286,7 @@ int sft_rotary(const sft_rotary_args *v, void *stream) {
     Rotary a{};
     const int64_t half = rot / 2, group = 16 / size, pair_units = (half + group - 1) / group;
     int64_t blocks = 0, sines = 0;
+    bool whole = true;          // every head of the results starts at a multiple of 64 bytes
     for (int32_t i = 0; i < n_mats; ++i) {
         const sft_rotary_mat &m = mats[i];
         if (m.heads == 0) continue;
@@ -305,6 +306,8 @@ int sft_rotary(const sft_rotary_args *v, void *stream) {
         r.parts = div_by(static_cast<uint32_t>(parts));
         r.tokens = static_cast<int32_t>(tokens);
         r.items = static_cast<int32_t>((tokens * units * m.heads + parts - 1) / parts);
+        whole = whole && aligned_to(m.Y, 64) && (m.heads <= 1 || m.y_head * size % 64 == 0) &&
+                (T <= 1 || m.y_row * size % 64 == 0) && (B <= 1 || m.y_batch * size % 64 == 0);
         r.begin = static_cast<uint32_t>(blocks);
         blocks += (total + tokens - 1) / tokens * parts;
         sines = std::max(sines, tokens * half);
@@ -321,10 +324,11 @@ int sft_rotary(const sft_rotary_args *v, void *stream) {
     const dim3 grid(static_cast<uint32_t>(std::min<int64_t>(blocks, 1 << 23))), block(kThreads);
     const size_t lds = static_cast<size_t>(sines + 8) * 8;
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    // Results go past L2 where a wave's stores are whole pieces of 64 bytes or long ones; short pieces, and heads that
-    // start between, are put together in L2 (134 MB in bf16: heads of 128, 64, 32 21.6, 26.8, 37.1 us past it, 26.0,
-    // 26.6, 27.8 through it; 48 of 128 turned in pairs 47.6 and 30.1)
-    const bool past = D * size % 16 == 0 && (pair_units % 4 == 0 || pair_units >= 12);
+    // Results go past L2 where a wave's stores are whole pieces of 64 bytes or long ones; others are put together in L2.
+    // 132 MB in bf16, us past it and through it: heads of 128, 64 and 32 21 and 26, 26.0 and 26.5, 36.5 and 27.1; those of
+    // 64 and 128 that start 16 bytes further on 37.3 and 28.5, 30.5 and 27.6; pieces of 7 groups (112) 30.0 and 27.1, of 9
+    // that start anywhere (130) 40.1 and 40.2, of 10 (160) 23.9 and 26.2, of 16 that start anywhere (256) 24.5 and 26.8.
+    const bool past = pair_units >= 10 || (whole && (layout == SFT_ROTARY_HALF ? half * size : pair_units * 16) % 64 == 0);
 #define SFT_SEND(E, half)                                                                        \
     do {                                                                                         \
         if (past) hipLaunchKernelGGL((k_rotary<E, half, true>), grid, block, lds, st, a);        \
