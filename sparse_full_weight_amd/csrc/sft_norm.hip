@@ -8,8 +8,8 @@
 //
 // A row is read once into the registers of a team of lanes, its mean and the
 // squares of the centred values are summed over the team, and the results are
-// written from the same registers, past L2 (30 us through it): both passes are
-// bound by HBM, and by launch latency where there are few rows.  4096 x 4096 in
+// written from the same registers, many of them past L2 (30 us through it): both
+// passes are bound by HBM, and by launch latency where there are few rows.  4096 x 4096 in
 // bf16: forward with residual 21.8 us (134 MB, 6.2 TB/s); backward with dh and
 // dgain 27.3 us, 24.3 of them the rows (139 MB with the partial sums, 5.7
 // TB/s), the rest the second launch that adds 256 workgroups' sums.  Rows of
@@ -100,8 +100,8 @@ struct NormForward {
 // than six of them leave (4096 x 3001: 23.4 us, with five 28.2).
 constexpr int forward_waves(int type, int groups, bool even) { return type == SFT_F32 && groups == 2 && !even ? 6 : 1; }
 
-// kEven: C is a multiple of a group.
-template <class X, class Y, int kLanes, int kGroups, bool kEven>
+// kEven: C is a multiple of a group.  kPast: results go past L2.
+template <class X, class Y, int kLanes, int kGroups, bool kEven, bool kPast>
 __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes, (forward_waves(X::kType, kGroups, kEven))) void k_norm_forward(const NormForward a) {
     constexpr int N = X::kGroup, kThreads = kLanes < 256 ? 256 : kLanes, kTeams = kThreads / kLanes;
     __shared__ float red[2][3][kThreads / 64];       // by turns, so that one barrier a sum is enough
@@ -134,7 +134,7 @@ __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes, (forward_waves(X::kTyp
                 const Raw<X, N> sum = close<X, N>(x[g]);
                 open<X, N>(sum, x[g]);                    // what is normed is what is kept
                 const int at = (g * kLanes + lane) * N;
-                if (live) put_group<X, N, true, kEven>(h + at, sum, C - at);
+                if (live) put_group<X, N, kPast, kEven>(h + at, sum, C - at);
             }
         } else {
             join_row<X, N, kLanes, kEven>(lane, C, raw, few);
@@ -193,7 +193,7 @@ __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes, (forward_waves(X::kTyp
 #pragma unroll
                 for (int i = 0; i < N; ++i) x[g][i] += w[i];
             }
-            put_group<Y, N, true, kEven>(y + at, close<Y, N>(x[g]), n);
+            put_group<Y, N, kPast, kEven>(y + at, close<Y, N>(x[g]), n);
         }
     }
 }
@@ -239,7 +239,7 @@ __device__ __forceinline__ void get_norm_row(const NormBackward &a, int64_t row,
 // its sums go to its own place in the workspace.
 // kSums: 0 = no sums over rows, 1 = dgain, 2 = dgain and dbias.  The widest
 // rows leave no registers for a row ahead or for the gains.
-template <class X, class Y, int kLanes, int kGroups, bool kEven, int kSums>
+template <class X, class Y, int kLanes, int kGroups, bool kEven, int kSums, bool kPast>
 __device__ __forceinline__ void norm_rows(const NormBackward &a, uint32_t block, uint32_t blocks) {
     constexpr int N = X::kGroup, kTeams = kRowThreads / kLanes, kWidth = kLanes * kGroups * N;
     constexpr bool kAhead = kWidth <= 8192;
@@ -330,7 +330,7 @@ __device__ __forceinline__ void norm_rows(const NormBackward &a, uint32_t block,
 #pragma unroll
                 for (int i = 0; i < N; ++i) d[g][i] += other[i];
             }
-            if (live) put_group<X, N, true, kEven>(dx + at, close<X, N>(d[g]), C - at);
+            if (live) put_group<X, N, kPast, kEven>(dx + at, close<X, N>(d[g]), C - at);
         }
     }
     if constexpr (kSums > 0) {
@@ -442,17 +442,19 @@ constexpr int few_columns(int width) { return width <= 256 ? 8 : width <= 1024 ?
 
 template <class X, class Y, int kLanes, int kGroups, bool kEven, int kSums>
 __global__ __launch_bounds__(kRowThreads) void k_norm_backward(const NormBackward a) {
-    norm_rows<X, Y, kLanes, kGroups, kEven, kSums>(a, blockIdx.x, gridDim.x);
+    norm_rows<X, Y, kLanes, kGroups, kEven, kSums, true>(a, blockIdx.x, gridDim.x);
 }
 
-// Rows and columns in one launch, the columns' workgroups first.
+// Rows and columns in one launch, the columns' workgroups first.  Results stay in
+// L2, as forward (192 x 4096 in bf16 with the product that reads them 29.0 us past
+// it, 28.4 through it, 512 41.1 and 41.2; alone 5.0 and 5.0, 8.0 and 8.1).
 template <class X, class Y, int kLanes, int kGroups, bool kEven>
 __global__ __launch_bounds__(kRowThreads) void k_norm_backward_few(const NormBackward a, const NormSums s,
                                                                    uint32_t columns) {
     if (blockIdx.x < columns)
         norm_columns<X, Y, few_columns(kLanes * kGroups * X::kGroup)>(a, s, blockIdx.x);
     else
-        norm_rows<X, Y, kLanes, kGroups, kEven, 0>(a, blockIdx.x - columns, gridDim.x - columns);
+        norm_rows<X, Y, kLanes, kGroups, kEven, 0, false>(a, blockIdx.x - columns, gridDim.x - columns);
 }
 
 // The workgroups' sums in a fixed order.
@@ -522,7 +524,7 @@ int check_apart(const Block *written, int n_written, const Block *read, int n_re
 #define SFT_BACKWARD_WIDTHS(go) \
     go(16, 1) go(32, 1) go(64, 1) go(128, 1) go(256, 1) go(512, 1) go(1024, 1) go(1024, 2)
 
-template <class X, class Y, bool kEven>
+template <class X, class Y, bool kEven, bool kPast>
 void send_forward(const NormForward &a, hipStream_t st) {
 #define SFT_GO(lanes, eights)                                                                                   \
     if (a.C <= lanes * eights * 8) {                                                                            \
@@ -530,7 +532,7 @@ void send_forward(const NormForward &a, hipStream_t st) {
         constexpr int kThreads = lanes < 256 ? 256 : lanes, kTeams = kThreads / lanes;                          \
         const int64_t rounds = (int64_t(a.T) + kTeams - 1) / kTeams;                                            \
         const uint32_t grid = static_cast<uint32_t>(std::min<int64_t>(rounds, 16 * num_cus()));                 \
-        hipLaunchKernelGGL((k_norm_forward<X, Y, lanes, kGroups, kEven>), dim3(grid), dim3(kThreads), 0, st, a); \
+        hipLaunchKernelGGL((k_norm_forward<X, Y, lanes, kGroups, kEven, kPast>), dim3(grid), dim3(kThreads), 0, st, a); \
         return;                                                                                                 \
     }
     if constexpr (X::kType == SFT_BF16) {
@@ -541,10 +543,20 @@ void send_forward(const NormForward &a, hipStream_t st) {
 #undef SFT_GO
 }
 
+// Results of up to 2 MB stay in L2 for the product that reads them next: of 4096
+// columns in bf16 with residual, norm and product of 8 rows take 18.5 us past it
+// and 16.3 through it, of 192 36.5 and 31.0, of 256 26.0 and 23.5, of 2048 77.8 and
+// 78.8; the norm alone 3.6 and 3.6, 3.9 and 4.1, 4.1 and 4.2, 12.4 and 13.4.
 template <class X, class Y>
 void send_forward(const NormForward &a, hipStream_t st) {
-    if (a.C % X::kGroup) send_forward<X, Y, false>(a, st);
-    else send_forward<X, Y, true>(a, st);
+    const bool past = int64_t(a.T) * a.C * int64_t(sizeof(typename Y::type)) > (1 << 21), even = a.C % X::kGroup == 0;
+    if (past) {
+        if (even) send_forward<X, Y, true, true>(a, st);
+        else send_forward<X, Y, false, true>(a, st);
+    } else {
+        if (even) send_forward<X, Y, true, false>(a, st);
+        else send_forward<X, Y, false, false>(a, st);
+    }
 }
 
 int backward_teams(int64_t C) {
