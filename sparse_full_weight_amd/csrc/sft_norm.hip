@@ -10,9 +10,9 @@
 // squares of the centred values are summed over the team, and the results are
 // written from the same registers, many of them past L2 (30 us through it): both
 // passes are bound by HBM, and by launch latency where there are few rows.  4096 x 4096 in
-// bf16: forward with residual 21.8 us (134 MB, 6.2 TB/s); backward with dh and
-// dgain 27.3 us, 24.3 of them the rows (139 MB with the partial sums, 5.7
-// TB/s), the rest the second launch that adds 256 workgroups' sums.  Rows of
+// bf16: forward with residual 21.9 us (134 MB, 6.1 TB/s); backward with dh and
+// dgain 27.3 us: under the tracer 24.5 the rows (139 MB with the partial sums, 5.7
+// TB/s) and 3.9 the second launch that adds 256 workgroups' sums.  Rows of
 // odd widths start between cache lines and cost a quarter more (16384 x 767 in
 // bf16: backward 28.5 us, 768 22.0).
 #include <hip/hip_runtime.h>

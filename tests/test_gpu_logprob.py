@@ -481,3 +481,36 @@ def test_more_short_rows_than_waves(gpu_lib, N, V):
     check(z, torch.randint(0, V, (N,), generator=gen(N)), 1.0, 5)
     for dtype, out_type in ((F32, F32), (BF16, BF16), (F32, BF16)):
         check_gradient(N, V, dtype, out_type, with_entropy=dtype == F32, seed=V)
+
+
+@pytest.mark.parametrize("N,dtype", [(1, F32), (300, BF16)])
+def test_very_long_rows(gpu_lib, N, dtype):
+    # 2^28 logits and some in one row by 1024 threads; 2^22 and some in each of more rows than CUs
+    V, K = ((1 << 28) + 13, 9) if N == 1 else ((1 << 22) + 5, 9)
+    z = torch.empty(N, V, dtype=dtype, device="cuda")
+    for i in range(N):
+        z[i] = torch.randn(V, device="cuda", generator=torch.Generator("cuda").manual_seed(i)) * 2.0
+    best = torch.randperm(V, device="cuda", generator=torch.Generator("cuda").manual_seed(77))[:K]
+    best[0], best[1] = V - 1, 0                     # the tail, and the first logit
+    z[:, best] = torch.arange(30, 30 - K, -1, device="cuda").to(dtype)
+    z[:, best[3]] = z[0, best[2]]                   # two alike
+    target = torch.full((N,), V // 2 + 1, dtype=torch.int32, device="cuda")
+    logp, H, stats = torch.empty(N, device="cuda"), torch.empty(N, device="cuda"), torch.empty(N, 2, device="cuda")
+    top, index = torch.empty(N, K, device="cuda"), torch.empty(N, K, dtype=torch.int32, device="cuda")
+    _lib.sft_logprob(z, target, logp, stats=stats, entropy=H, top_logp=top, top_index=index)
+    order = best.clone()
+    order[2:4] = best[2:4].sort().values
+    assert (index.long() == order).all()
+    for i in range(0, N, 60):
+        total = along = 0.0
+        for part in z[i].split(1 << 25):
+            d = part.double() - 30.0
+            total, along = total + d.exp().sum(), along + (d.exp() * d).sum()
+        L = total.log()
+        # additions as in exact(), differences of at most 45 from the largest logit
+        e = (V / 256 * 1.125 + 50) * U + 3 * U * 45
+        assert abs(stats[i, 0] - 30.0) == 0 and abs(stats[i, 1].double() - L) <= e
+        assert abs(H[i].double() - (L - along / total)) <= 2 * e * (1 + abs(along / total))
+        lp = z[i, V // 2 + 1].double() - 30.0 - L
+        assert abs(logp[i].double() - lp) <= e + 4 * U * abs(lp)
+        assert ((top[i].double() - (z[i, order].double() - 30.0 - L)).abs() <= e + 4 * U * 45).all()
